@@ -92,6 +92,23 @@ class QsaGatherParams(ctypes.Structure):
                 ("maxPagesPerSeq", _i32), ("topK", _i32), ("stream", _vp)]
 
 
+class QsaAppendKvParams(ctypes.Structure):
+    _fields_ = [("qkv", _vp), ("qNormW", _vp), ("kNormW", _vp), ("contextLengths", _vp), ("newLengths", _vp),
+                ("qOut", _vp), ("kOut", _vp), ("vOut", _vp), ("kvPool", _vp), ("kvScale", _vp), ("pageTable", _vp),
+                ("status", _vp), ("batchSize", _i32), ("seqLen", _i32), ("numQHeads", _i32), ("numKVHeads", _i32),
+                ("headDim", _i32), ("rotDim", _i32), ("poolHeadDim", _i32), ("numFlatPages", _i32),
+                ("maxPagesPerSeq", _i32), ("scaleBlock", _i32), ("ropeTheta", _f32), ("rmsNormEps", _f32),
+                ("stream", _vp)]
+
+
+class QsaSparsePagedKv8Params(ctypes.Structure):
+    _fields_ = [("qPtr", _vp), ("kvPool", _vp), ("kvScale", _vp), ("pageTable", _vp), ("indices", _vp),
+                ("contextLengths", _vp), ("newLengths", _vp), ("oPtr", _vp), ("batchSize", _i32), ("seqLen", _i32),
+                ("numQHeads", _i32), ("numKVHeads", _i32), ("headDim", _i32), ("poolHeadDim", _i32),
+                ("numFlatPages", _i32), ("maxPagesPerSeq", _i32), ("topK", _i32), ("scaleBlock", _i32),
+                ("attentionScale", _f32), ("stream", _vp), ("status", _vp)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -116,7 +133,13 @@ def lib() -> ctypes.CDLL:
                              ("qsa_sparse_prefill_tcgen05_bf16", QsaSparsePrefillParams),
                              ("qsa_sparse_decode_bf16", QsaSparseDecodeParams),
                              ("qsa_rope_qkv", QsaRopeQkvParams),
-                             ("qsa_gather_selected", QsaGatherParams)):
+                             ("qsa_gather_selected", QsaGatherParams),
+                             ("qsa_append_kv", QsaAppendKvParams),
+                             ("qsa_append_kv_bf16", QsaAppendKvParams),
+                             ("qsa_append_kv8", QsaAppendKvParams),
+                             ("qsa_append_kv8_bf16", QsaAppendKvParams),
+                             ("qsa_sparse_paged_kv8", QsaSparsePagedKv8Params),
+                             ("qsa_sparse_paged_kv8_bf16", QsaSparsePagedKv8Params)):
                 f = getattr(L, name)
                 f.argtypes = [ctypes.POINTER(st)]
                 f.restype = ctypes.c_int
@@ -400,3 +423,100 @@ def sparse_decode_noalloc(q, pool, page_table, indices, ctx, out, *, D, scale, s
         headDim=D, poolHeadDim=phd, numFlatPages=nflat, maxPagesPerSeq=page_table.shape[-1], topK=topK,
         attentionScale=scale, stream=_stream(stream))
     _check(lib().qsa_sparse_decode_noalloc(ctypes.byref(p)))
+
+
+# -------------------------------------------------------------- paged cache
+def _same_device(name: str, tensors) -> None:
+    """Every tensor on the current device: the kernels run there, on its current stream."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _append(name, qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
+            v_out, status, stream):
+    et = qkv.dtype
+    if et not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name}: qkv must be float16 or bfloat16")
+    if qkv.dim() != 4 or pool.dim() != 4 or page_table.dim() != 3:
+        raise ValueError(f"{name}: qkv and pool have 4 dimensions, page_table 3")
+    B, S, NH, D = qkv.shape
+    nflat, tpp, ph, phd = pool.shape
+    if NH != Hq + 2 * Hkv or tuple(q_out.shape) != (B, S, Hq, D) or tuple(wq.shape) != (D,) or \
+            tuple(wk.shape) != (D,) or tuple(ctx.shape) != (B,) or tpp != 128 or ph != Hkv or \
+            tuple(page_table.shape[:2]) != (B, 2):
+        raise ValueError(f"{name}: shape mismatch")
+    for t in (k_out, v_out):
+        if t is not None and tuple(t.shape) != (B, S, Hkv, D):
+            raise ValueError(f"{name}: k_out/v_out shape mismatch")
+    if new_lengths is not None and tuple(new_lengths.shape) != (B,):
+        raise ValueError(f"{name}: new_lengths must have shape ({B},)")
+    block = 0
+    if scale is not None:
+        if scale.dim() != 3 or scale.shape[0] != nflat or scale.shape[2] != Hkv or scale.shape[1] < 1 or \
+                128 % scale.shape[1]:
+            raise ValueError(f"{name}: scale must be [{nflat}, 128 / block, {Hkv}]")
+        block = 128 // scale.shape[1]
+    p = QsaAppendKvParams(
+        qkv=_ptr(qkv, et, "qkv"), qNormW=_ptr(wq, torch.float32, "qNormW"), kNormW=_ptr(wk, torch.float32, "kNormW"),
+        contextLengths=_ptr(ctx, torch.int32, "contextLengths"),
+        newLengths=_ptr(new_lengths, torch.int32, "new_lengths"), qOut=_ptr(q_out, et, "q_out"),
+        kOut=_ptr(k_out, et, "k_out"), vOut=_ptr(v_out, et, "v_out"),
+        kvPool=_ptr(pool, et if scale is None else torch.float8_e4m3fn, "pool"),
+        kvScale=_ptr(scale, torch.float32, "scale"), pageTable=_ptr(page_table, torch.int32, "pageTable"),
+        status=_ptr(status, torch.int32, "status"), batchSize=B, seqLen=S, numQHeads=Hq, numKVHeads=Hkv, headDim=D,
+        rotDim=rot, poolHeadDim=phd, numFlatPages=nflat, maxPagesPerSeq=page_table.shape[-1], scaleBlock=block,
+        ropeTheta=theta, rmsNormEps=eps, stream=_stream(stream))
+    _same_device(name, (qkv, wq, wk, ctx, new_lengths, q_out, k_out, v_out, pool, scale, page_table, status))
+    _check(getattr(lib(), "qsa_" + name + ("_bf16" if et == torch.bfloat16 else ""))(ctypes.byref(p)))
+
+
+def append_kv(qkv, wq, wk, ctx, q_out, pool, page_table, *, Hq, Hkv, rot, theta, eps, new_lengths=None, k_out=None,
+              v_out=None, status=None, stream=None):
+    """qsa_append_kv (fp16) or qsa_append_kv_bf16: the new tokens of packed qkv [B,S,Hq+2Hkv,D], normed and rotated
+    at their positions: q_out [B,S,Hq,D], the K/V rows of pool [numFlat,128,Hkv,poolHeadDim] (qkv's type) through
+    page_table [B,2,pages], and optional dense mirrors k_out / v_out [B,S,Hkv,D].  ctx int32 [B] holds total lengths,
+    new_lengths int32 [B] how many of them are new (None: min(S, ctx))."""
+    _append("append_kv", qkv, wq, wk, ctx, q_out, pool, None, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
+            v_out, status, stream)
+
+
+def append_kv8(qkv, wq, wk, ctx, q_out, pool, scale, page_table, *, Hq, Hkv, rot, theta, eps, new_lengths=None,
+               k_out=None, v_out=None, status=None, stream=None):
+    """qsa_append_kv8 (fp16) or qsa_append_kv8_bf16: append_kv into a float8_e4m3fn pool
+    [numFlat,128,Hkv,poolHeadDim] with scale float32 [numFlat,128/block,Hkv], one per block of tokens and head."""
+    if scale is None:
+        raise ValueError("append_kv8: scale is missing")
+    _append("append_kv8", qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths,
+            k_out, v_out, status, stream)
+
+
+def sparse_paged_kv8(q, pool, kv_scale, page_table, indices, ctx, out, *, scale, new_lengths=None, status=None,
+                     stream=None):
+    """qsa_sparse_paged_kv8 (fp16) or qsa_sparse_paged_kv8_bf16: q/out [B,S,Hq,D], pool float8_e4m3fn
+    [numFlat,128,Hkv,poolHeadDim], kv_scale float32 [numFlat,128/block,Hkv], indices int32 [B,S,topK], ctx int32 [B]
+    total lengths, new_lengths int32 [B] query rows (None: min(S, ctx)); scale multiplies q . k."""
+    et = q.dtype
+    if et not in (torch.float16, torch.bfloat16):
+        raise ValueError("sparse_paged_kv8: q must be float16 or bfloat16")
+    if q.dim() != 4 or pool.dim() != 4 or kv_scale.dim() != 3 or page_table.dim() != 3 or indices.dim() != 3:
+        raise ValueError("sparse_paged_kv8: q and pool have 4 dimensions, kv_scale, page_table and indices 3")
+    B, S, Hq, D = q.shape
+    nflat, tpp, Hkv, phd = pool.shape
+    nblk = kv_scale.shape[1]
+    if tuple(out.shape) != (B, S, Hq, D) or tpp != 128 or tuple(page_table.shape[:2]) != (B, 2) or \
+            tuple(indices.shape[:2]) != (B, S) or tuple(ctx.shape) != (B,) or \
+            tuple(kv_scale.shape) != (nflat, nblk, Hkv) or nblk < 1 or 128 % nblk or \
+            (new_lengths is not None and tuple(new_lengths.shape) != (B,)):
+        raise ValueError("sparse_paged_kv8: shape mismatch")
+    p = QsaSparsePagedKv8Params(
+        qPtr=_ptr(q, et, "q"), kvPool=_ptr(pool, torch.float8_e4m3fn, "pool"),
+        kvScale=_ptr(kv_scale, torch.float32, "kv_scale"), pageTable=_ptr(page_table, torch.int32, "pageTable"),
+        indices=_ptr(indices, torch.int32, "indices"), contextLengths=_ptr(ctx, torch.int32, "contextLengths"),
+        newLengths=_ptr(new_lengths, torch.int32, "new_lengths"), oPtr=_ptr(out, et, "out"), batchSize=B, seqLen=S,
+        numQHeads=Hq, numKVHeads=Hkv, headDim=D, poolHeadDim=phd, numFlatPages=nflat,
+        maxPagesPerSeq=page_table.shape[-1], topK=indices.shape[-1], scaleBlock=128 // nblk, attentionScale=scale,
+        stream=_stream(stream), status=_ptr(status, torch.int32, "status"))
+    _same_device("sparse_paged_kv8", (q, pool, kv_scale, page_table, indices, ctx, new_lengths, out, status))
+    _check(getattr(lib(), "qsa_sparse_paged_kv8" + ("_bf16" if et == torch.bfloat16 else ""))(ctypes.byref(p)))

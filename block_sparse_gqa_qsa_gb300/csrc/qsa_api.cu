@@ -147,6 +147,77 @@ qsa_status_t sparse_decode_entry(const QsaSparseDecodeParams* p, const char* fn,
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
+bool power_of_two(int x) { return x >= 1 && (x & (x - 1)) == 0; }
+
+// The append entry points share their checks; fn names the caller in messages.
+qsa_status_t append_kv_entry(const QsaAppendKvParams* p, const char* fn, bool bf16, bool kv8) {
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->qkv || !p->qNormW || !p->kNormW || !p->contextLengths || !p->qOut || !p->kvPool || !p->pageTable)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+  if (p->batchSize < 1 || p->seqLen < 1 || p->numQHeads < 1 || p->numKVHeads < 1 || p->headDim < 1 ||
+      p->numFlatPages < 1 || p->maxPagesPerSeq < 1)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
+  if (p->rotDim < 0 || p->rotDim > p->headDim || (p->rotDim & 1) || !(p->ropeTheta > 0.f) || !(p->rmsNormEps >= 0.f))
+    return fail(QSA_ERR_INVALID_ARG, "%s: rotDim must be even and <= headDim; theta > 0, eps >= 0", fn);
+  if (p->poolHeadDim < p->headDim) return fail(QSA_ERR_INVALID_ARG, "%s: poolHeadDim < headDim", fn);
+  if (kv8) {
+    if (!p->kvScale) return fail(QSA_ERR_INVALID_ARG, "%s: kvScale is NULL", fn);
+    if (!power_of_two(p->scaleBlock) || p->scaleBlock > qsa::kTokensPerPageHost)
+      return fail(QSA_ERR_INVALID_ARG, "%s: scaleBlock %d is not a power of two in 1..128", fn, p->scaleBlock);
+  } else if (p->kvScale || p->scaleBlock) {
+    return fail(QSA_ERR_INVALID_ARG, "%s: a 16-bit pool has no kvScale (NULL) and no scaleBlock (0)", fn);
+  }
+  if (p->headDim != 64 && p->headDim != 128)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: headDim %d not 64 or 128", fn, p->headDim);
+  if (p->rotDim % 16)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: rotDim %d is not a multiple of 16", fn, p->rotDim);
+  if (p->poolHeadDim % (kv8 ? 16 : 8))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: poolHeadDim %d: pool rows must be whole 16-byte chunks", fn, p->poolHeadDim);
+  if (p->numQHeads > 1024 || p->numKVHeads > 1024)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: numQHeads or numKVHeads above 1024", fn);
+  if (!aligned(p->qkv, 16) || !aligned(p->qOut, 16) || !aligned(p->kOut, 16) || !aligned(p->vOut, 16) ||
+      !aligned(p->kvPool, 16) || !aligned(p->kvScale, 4) || !aligned(p->pageTable, 4) ||
+      !aligned(p->contextLengths, 4) || !aligned(p->newLengths, 4) || !aligned(p->qNormW, 4) ||
+      !aligned(p->kNormW, 4) || !aligned(p->status, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: qkv, qOut, kOut, vOut and kvPool must be 16-byte aligned, the others 4", fn);
+  if (static_cast<long long>(p->batchSize) * p->seqLen > 0x7fffffffLL ||
+      static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen, maxPagesPerSeq or numFlatPages too large", fn);
+  const cudaError_t e = qsa::launch_append_kv(*p, rope_freqs(p->ropeTheta, p->rotDim), bf16, kv8);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+qsa_status_t sparse_paged_kv8_entry(const QsaSparsePagedKv8Params* p, const char* fn, bool bf16) {
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->qPtr || !p->kvPool || !p->kvScale || !p->pageTable || !p->indices || !p->contextLengths || !p->oPtr)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a tensor pointer is NULL", fn);
+  if (p->batchSize < 1 || p->seqLen < 1 || p->numQHeads < 1 || p->numKVHeads < 1 || p->headDim < 1 || p->topK < 1 ||
+      p->numFlatPages < 1 || p->maxPagesPerSeq < 1)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
+  if (p->numQHeads % p->numKVHeads) return fail(QSA_ERR_INVALID_ARG, "%s: numQHeads %% numKVHeads != 0", fn);
+  if (p->poolHeadDim < p->headDim) return fail(QSA_ERR_INVALID_ARG, "%s: poolHeadDim < headDim", fn);
+  if (!power_of_two(p->scaleBlock) || p->scaleBlock > qsa::kTokensPerPageHost)
+    return fail(QSA_ERR_INVALID_ARG, "%s: scaleBlock %d is not a power of two in 1..128", fn, p->scaleBlock);
+  if (!qsa_sparse_prefill_can_implement(p->numQHeads, p->numKVHeads, p->headDim))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: needs headDim 128 and a GQA group of at most 16", fn);
+  if (p->poolHeadDim % 16)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: poolHeadDim %d is not a multiple of 16", fn, p->poolHeadDim);
+  if (p->topK > (1 << 24)) return fail(QSA_ERR_UNSUPPORTED, "%s: topK > %d", fn, 1 << 24);
+  if (!aligned(p->qPtr, 16) || !aligned(p->kvPool, 16) || !aligned(p->oPtr, 16) || !aligned(p->kvScale, 4) ||
+      !aligned(p->pageTable, 4) || !aligned(p->indices, 4) || !aligned(p->contextLengths, 4) ||
+      !aligned(p->newLengths, 4) || !aligned(p->status, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: q, kvPool and o must be 16-byte aligned, the others 4", fn);
+  if (static_cast<long long>(p->batchSize) * p->seqLen > 0x7fffffffLL ||
+      static_cast<long long>(p->batchSize) * p->seqLen * p->numKVHeads > 0x7fffffffLL ||
+      static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen * numKVHeads, maxPagesPerSeq or numFlatPages too large",
+                fn);
+  const cudaError_t e = qsa::launch_sparse_paged_kv8(*p, bf16);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -354,6 +425,21 @@ qsa_status_t qsa_indexer_prefill_handoff(const QsaIndexerHandoffParams* p) {
                                    "aligned, for this shape", need);
   const cudaError_t e = qsa::launch_indexer_handoff(*p);
   return e == cudaSuccess ? ok() : cuda_fail(e, "qsa_indexer_prefill_handoff");
+}
+
+qsa_status_t qsa_append_kv(const QsaAppendKvParams* p) { return append_kv_entry(p, "qsa_append_kv", false, false); }
+qsa_status_t qsa_append_kv_bf16(const QsaAppendKvParams* p) {
+  return append_kv_entry(p, "qsa_append_kv_bf16", true, false);
+}
+qsa_status_t qsa_append_kv8(const QsaAppendKvParams* p) { return append_kv_entry(p, "qsa_append_kv8", false, true); }
+qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* p) {
+  return append_kv_entry(p, "qsa_append_kv8_bf16", true, true);
+}
+qsa_status_t qsa_sparse_paged_kv8(const QsaSparsePagedKv8Params* p) {
+  return sparse_paged_kv8_entry(p, "qsa_sparse_paged_kv8", false);
+}
+qsa_status_t qsa_sparse_paged_kv8_bf16(const QsaSparsePagedKv8Params* p) {
+  return sparse_paged_kv8_entry(p, "qsa_sparse_paged_kv8_bf16", true);
 }
 
 int32_t qsa_gather_scratch_pages(int32_t topK) { return topK < 1 ? 0 : qsa::gather_scratch_pages(topK); }

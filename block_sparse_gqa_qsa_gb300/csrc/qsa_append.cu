@@ -1,0 +1,414 @@
+// qsa_append.cu -- new tokens' keys and values into a paged cache, with the
+// per-head norm and the rotation on the way (qsa_append_kv: a pool of the
+// inputs' 16-bit type; qsa_append_kv8: e4m3 codes with block scales).
+//
+//   y = x / sqrt(mean(x^2) + eps) * (1 + w),  (y_i, y_{i+h}) rotated by p theta^(-2i/rot), h = rot / 2
+//
+// A stream of the packed heads: every input is read once and every output
+// written once, so HBM bounds a large call and latency a small one.  A CTA
+// takes the rows of one tile of kTile (or scaleBlock, where that is more)
+// consecutive cache positions, aligned in the page: the tile lies in one page,
+// its cos/sin table is formed once and shared by all heads, and every block of
+// scales lies in one tile, so one warp owns a block and no atomics are needed.
+// A warp takes one head of up to 16 of the tile's rows at a time, 8 values
+// (16 bytes) per lane, with all of the rows' loads in flight before the first
+// is used.  The D/8 lanes of a row reduce its sum of squares with shuffles;
+// rotDim is a multiple of 16, so a chunk's rotation partner is a whole chunk of
+// another lane of the row, fetched as four 32-bit shuffles of the raw values.
+// For an 8-bit pool a K or V head is passed over twice in registers: the
+// blocks' largest values first, then the codes.  Blocks of more than 16 tokens
+// read their rows twice (the second time from L1/L2).
+#include <algorithm>
+
+#include "qsa_internal.h"
+#include "qsa_kv8.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 16;  // rows a warp holds in registers
+
+struct AppendArgs {
+  const void* qkv;
+  const float* qw;
+  const float* kw;
+  const int32_t* ctx;
+  const int32_t* newLen;  // may be null
+  void* qout;
+  void* kout;  // may be null
+  void* vout;  // may be null
+  uint8_t* pool;
+  float* scale;  // 8-bit only
+  const int32_t* pageTable;
+  int32_t* status;  // may be null
+  int S, Hq, Hkv, rot, poolHeadDim, numFlatPages, maxPagesPerSeq;
+  int blockShift;        // log2(scaleBlock)
+  int tile;              // positions per CTA: max(kTile, scaleBlock)
+  int tiles;             // tiles per sequence
+  float eps;
+  unsigned long long turn[64];  // inv_freq of pair i as a 64-bit fixed-point fraction of a turn
+};
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(const uint4 r, uint64_t (&v)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBf16) {
+      v[i] = static_cast<uint64_t>(w[i] << 16) | (static_cast<uint64_t>(w[i] & 0xffff0000u) << 32);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[i] = pack_f2(f.x, f.y);
+    }
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = kBf16 ? pack_bf162(lo_f2(v[i]), hi_f2(v[i])) : pack_half2(lo_f2(v[i]), hi_f2(v[i]));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Mean of (f x)^2 over a row; x: this lane's 8 of the row's D values, as pairs.
+template <int D>
+__device__ __forceinline__ float mean_square(const uint64_t (&x)[4], float f) {
+  const uint64_t f2 = pack_f2(f, f);
+  uint64_t acc = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t v = fmul2(x[k], f2);
+    acc = ffma2(v, v, acc);
+  }
+  float ss = lo_f2(acc) + hi_f2(acc);
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+  return ss * (1.0f / D);
+}
+
+// What a lane keeps of a head's norm and rotation: its chunk's weights and its partner chunk's.
+struct HeadWeights {
+  uint64_t own[4], partner[4];
+};
+
+// The 8 values of a lane's chunk after norm and rotation: with u = x w and the partner chunk's u',
+// y = inv (u cos -+ u' sin); cs: the row's table at this lane's chunk (unused past rotDim).
+template <int D, bool kBf16>
+__device__ __forceinline__ void norm_rotate(const uint4 raw, float inv, const HeadWeights& w, int partner, int side,
+                                            const ulonglong2* cs, int stride, uint64_t (&y)[4]) {
+  const uint4 other = make_uint4(__shfl_sync(kFull, raw.x, partner), __shfl_sync(kFull, raw.y, partner),
+                                 __shfl_sync(kFull, raw.z, partner), __shfl_sync(kFull, raw.w, partner));
+  const uint64_t inv2 = pack_f2(inv, inv);
+  unpack8<kBf16>(raw, y);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], w.own[k]);
+  if (side) {  // -1: first half of a pair, +1: second half
+    uint64_t u[4];
+    unpack8<kBf16>(other, u);
+    const float sg = static_cast<float>(side);
+    const uint64_t sg2 = pack_f2(sg, sg);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const ulonglong2 t = cs[k * stride];  // (cos, cos), (sin, sin) of elements 2k, 2k + 1
+      y[k] = ffma2(fmul2(fmul2(u[k], w.partner[k]), sg2), t.y, fmul2(y[k], t.x));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], inv2);
+}
+
+// Largest finite magnitude of 8 values (0 for none).
+__device__ __forceinline__ float finite_max(const uint64_t (&y)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = fabsf(lo_f2(y[k])), b = fabsf(hi_f2(y[k]));
+    m = fmaxf(m, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
+  }
+  return m;
+}
+
+// 8 codes of y * inv; infinities become NaN.
+__device__ __forceinline__ uint2 quantise8(const uint64_t (&y)[4], float inv) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = lo_f2(y[k]), b = hi_f2(y[k]);
+    v[2 * k] = fabsf(a) < INFINITY ? a * inv : NAN;
+    v[2 * k + 1] = fabsf(b) < INFINITY ? b * inv : NAN;
+  }
+  return make_uint2(f32_to_e4m3(v[0], v[1], v[2], v[3]), f32_to_e4m3(v[4], v[5], v[6], v[7]));
+}
+
+// 8 stored codes multiplied by f and rounded to codes again (exact for a power of two, above 2^-6).
+__device__ __forceinline__ uint2 rescale8(const uint2 c, float f) {
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t lo, hi;
+    e4m3_to_f16(i ? c.y : c.x, lo, hi);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    r[i] = f32_to_e4m3(a.x * f, a.y * f, b.x * f, b.y * f);
+  }
+  return make_uint2(r[0], r[1]);
+}
+
+template <int D, bool kBf16, bool kKv8>
+__global__ void __launch_bounds__(kThreads, 2) append_kv_kernel(const AppendArgs a) {
+  constexpr int LPR = D / 8;              // lanes per row
+  constexpr int RPW = 32 / LPR;           // rows a warp reads with one load instruction
+  constexpr int ITER = kTile / RPW;
+  extern __shared__ __align__(16) ulonglong2 table[];  // [row of the tile][4][rot / 16]: see norm_rotate
+  __shared__ __align__(16) float w1[2][D];             // 1 + w of q and k heads
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = lane & (LPR - 1), sub = lane / LPR;
+  const int b = blockIdx.x / a.tiles, tileIdx = blockIdx.x - b * a.tiles;
+  const int L = max(a.ctx[b], 0);
+  const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
+  const int c = L - n;                            // position of row 0
+  const int t0 = tileIdx * a.tile - c % a.tile;   // row at the tile's first position
+  if (t0 >= a.S) return;
+  const int tlo = max(t0, 0);                     // first row of this CTA
+  const int thi = min(min(a.S, n), t0 + a.tile);  // past its last live row; later rows of the tile are padding
+  const int hl = a.rot >> 4;                      // chunks of half a rotation
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) w1[i / D][i % D] = 1.0f + __ldg((i < D ? a.qw : a.kw) + i % D);
+  for (int i = threadIdx.x; i < (thi - tlo) * 8 * hl; i += kThreads) {  // pairs of the live rows
+    const int r = i / (8 * hl), pair = i - r * 8 * hl;
+    float cv, sv;
+    rope_cos_sin_turns(static_cast<unsigned>(c + tlo + r), a.turn[pair], cv, sv);
+    const int e = pair & 7;
+    float* dst = reinterpret_cast<float*>(table + ((tlo - t0 + r) * 4 + (e >> 1)) * hl + (pair >> 3)) + (e & 1);
+    dst[0] = cv;
+    dst[2] = sv;
+  }
+  // the tile's pages
+  const int page = (c + tlo) >> 7;  // of live rows; the tile lies in one page
+  int pg[2] = {-1, -1};
+  if (thi > tlo) {
+    if (page < a.maxPagesPerSeq) {
+      const int32_t* pt = a.pageTable + static_cast<size_t>(b) * 2 * a.maxPagesPerSeq + page;
+      pg[0] = __ldg(pt);
+      pg[1] = __ldg(pt + a.maxPagesPerSeq);
+    }
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (static_cast<unsigned>(pg[i]) >= static_cast<unsigned>(a.numFlatPages)) {
+        pg[i] = -1;
+        bad = true;
+      }
+    if (bad && threadIdx.x == 0 && a.status) atomicOr(a.status, kErrBadPage);
+  }
+  __syncthreads();
+
+  const int NH = a.Hq + 2 * a.Hkv;
+  const int side = j < hl ? -1 : (j < 2 * hl ? 1 : 0);
+  const int partner = lane - side * hl;
+  const uint4* src = static_cast<const uint4*>(a.qkv) + static_cast<size_t>(b) * a.S * NH * LPR + j;
+  for (int h = blockIdx.y * kWarps + warp; h < NH; h += gridDim.y * kWarps) {
+    const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
+    const int hk = isq ? 0 : (isv ? h - a.Hq - a.Hkv : h - a.Hq);
+    HeadWeights w;
+    if (!isv) {
+      const int jp = j - side * hl;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w.own[k] = *reinterpret_cast<const uint64_t*>(&w1[isq ? 0 : 1][8 * j + 2 * k]);
+        w.partner[k] = *reinterpret_cast<const uint64_t*>(&w1[isq ? 0 : 1][8 * jp + 2 * k]);
+      }
+    }
+    // dense output of this head: row t at dense + t * denseStride (16-byte chunks)
+    uint4* dense = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
+    const size_t denseStride = static_cast<size_t>(isq ? a.Hq : a.Hkv) * LPR;
+    if (dense) dense += static_cast<size_t>(b) * a.S * denseStride + static_cast<size_t>(isq ? h : hk) * LPR + j;
+    const int pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
+
+    uint4 raw[ITER];
+    float inv[ITER];
+    // Loads the rows base .. base + 15 and forms the norm's factors.
+    auto load = [&](int base) {
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        const int t = base + i * RPW + sub;
+        raw[i] = t >= tlo && t < thi ? __ldg(src + (static_cast<size_t>(t) * NH + h) * LPR) : make_uint4(0, 0, 0, 0);
+      }
+      if (isv) return;
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        uint64_t x[4];
+        unpack8<kBf16>(raw[i], x);
+        float m = mean_square<D>(x, 1.0f) + a.eps, back = 1.0f;
+        if (kBf16 && __any_sync(kFull, m == INFINITY)) {  // squares past fp32: the same on values scaled by 2^-64
+          const float ms = mean_square<D>(x, 0x1p-64f) + a.eps * 0x1p-128f;
+          back = m == INFINITY ? 0x1p-64f : 1.0f;
+          m = m == INFINITY ? ms : m;
+        }
+        const float r = rsqrtf(m);
+        inv[i] = back * r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
+      }
+    };
+    auto value = [&](int base, int i, uint64_t (&y)[4]) {
+      if (isv)
+        unpack8<kBf16>(raw[i], y);
+      else
+        norm_rotate<D, kBf16>(raw[i], inv[i], w, partner, side,
+                              table + static_cast<size_t>(base - t0 + i * RPW + sub) * 4 * hl + (side > 0 ? j - hl : j),
+                              hl, y);
+    };
+
+    float rowInv = 0.f;  // 8-bit K/V heads, lanes 0..15: 1 / scale of row `lane`
+    if constexpr (kKv8) {
+      if (!isq && thi > tlo) {
+        const int sb = 1 << a.blockShift, seg = min(sb, kTile);
+        float bm = 0.f;
+        for (int base = t0; base < t0 + a.tile; base += kTile) {
+          if (base + kTile <= tlo || base >= thi) continue;
+          load(base);
+          float rm = 0.f;  // of row `lane`
+#pragma unroll
+          for (int i = 0; i < ITER; ++i) {
+            uint64_t y[4];
+            value(base, i, y);
+            const int t = base + i * RPW + sub;
+            float m = t >= tlo && t < thi ? finite_max(y) : 0.f;
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+            m = __shfl_sync(kFull, m, (lane % RPW) * LPR);
+            if (lane / RPW == i) rm = m;
+          }
+          for (int o = 1; o < seg; o <<= 1) rm = fmaxf(rm, __shfl_xor_sync(kFull, rm, o));
+          bm = fmaxf(bm, rm);
+        }
+        // the scale of this lane's block (lanes 0..15; the upper half only follows)
+        const int rr = lane & (kTile - 1);
+        const int tb = t0 + (sb > kTile ? 0 : rr & ~(sb - 1));  // row at the block's first position
+        const bool fill = max(tb, tlo) < min(tb + sb, thi) && pageId >= 0;
+        float* sp = a.scale +
+                    ((static_cast<size_t>(fill ? pageId : 0) << (7 - a.blockShift)) +
+                     (fill ? ((c + tb) & 127) >> a.blockShift : 0)) * a.Hkv + hk;
+        float now = 1.f, shrink = 1.f;
+        if (fill) {
+          if (tb < 0) {  // older tokens: keep their scale, or grow it by the smallest power of two that fits
+            const float kept = read_scale(*sp);
+            const float over = __fdiv_rn(bm, kE4m3Max * kept);
+            now = kept;
+            if (over > 1.f) {
+              const int bits = __float_as_int(over);
+              const int k = (bits >> 23) - 127 + ((bits & 0x7fffff) ? 1 : 0);
+              now = fminf(ldexpf(kept, k), kScaleHi);
+              shrink = kept / now;
+            }
+          } else {
+            now = fminf(fmaxf(__fdiv_rn(bm, kE4m3Max), kScaleLo), kScaleHi);
+          }
+        }
+        __syncwarp();  // every lane of a block has read its scale
+        if (fill && (sb > kTile ? lane == 0 : lane < kTile && (rr & (sb - 1)) == 0)) *sp = now;
+        rowInv = 1.0f / now;
+        // older rows of the grown block (at most one block of the tile holds older tokens)
+        const float f = __shfl_sync(kFull, shrink, sb > kTile || t0 >= 0 ? 0 : (-t0) & ~(sb - 1));
+        if (t0 < 0 && f != 1.f && pageId >= 0) {
+          const int first = c & ~(sb - 1);
+          for (int p = first + sub; p < c; p += RPW) {
+            uint2* row = reinterpret_cast<uint2*>(
+                             a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + (p & 127)) * a.Hkv + hk) *
+                                          a.poolHeadDim) + j;
+            *row = rescale8(*row, f);
+          }
+        }
+      }
+    }
+
+    const bool held = kKv8 && !isq && a.tile == kTile;  // the amax pass left the rows in registers
+    for (int base = t0; base < t0 + a.tile; base += kTile) {
+      if (base + kTile <= tlo || base >= a.S) continue;
+      const bool any = base < thi;
+      if (any && !held) load(base);
+#pragma unroll
+      for (int i = 0; i < ITER; ++i) {
+        const int rr = i * RPW + sub, t = base + rr;
+        const bool live = t >= tlo && t < thi;
+        uint64_t y[4] = {0, 0, 0, 0};
+        if (any) value(base, i, y);
+        if (dense && t >= tlo && t < a.S && t < t0 + a.tile) {
+          uint4 out = make_uint4(0, 0, 0, 0);
+          if (live) out = isv ? raw[i] : pack8<kBf16>(y);
+          dense[static_cast<size_t>(t) * denseStride] = out;
+        }
+        if (isq) continue;
+        const float qs = kKv8 ? __shfl_sync(kFull, rowInv, rr) : 0.f;
+        if (live && pageId >= 0) {
+          const size_t row = (static_cast<size_t>(pageId) * kTokensPerPage + ((c + t) & 127)) * a.Hkv + hk;
+          if constexpr (kKv8)
+            *(reinterpret_cast<uint2*>(a.pool + row * a.poolHeadDim) + j) = quantise8(y, qs);
+          else
+            *(reinterpret_cast<uint4*>(a.pool + row * a.poolHeadDim * 2) + j) = isv ? raw[i] : pack8<kBf16>(y);
+        }
+      }
+    }
+  }
+}
+
+template <int D, bool kBf16, bool kKv8>
+cudaError_t append_go(const AppendArgs& a, int B, cudaStream_t st) {
+  auto kernel = append_kv_kernel<D, kBf16, kKv8>;
+  const size_t smem = static_cast<size_t>(a.tile) * (a.rot / 2) * 8;  // at most 128 x 64 pairs: 64 KB
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokensPerPage * (D / 2) * 8);
+  if (attr != cudaSuccess) return attr;
+  // One CTA per tile when the tiles fill the GPU a few times over; otherwise the heads of a tile are dealt
+  // out to several CTAs, down to one head per warp.
+  const long long tiles = static_cast<long long>(B) * a.tiles;
+  const int most = (a.Hq + 2 * a.Hkv + kWarps - 1) / kWarps;
+  const long long want = 4LL * sm_count();
+  const int parts = static_cast<int>(std::min<long long>(most, std::max<long long>(1, (want + tiles - 1) / tiles)));
+  kernel<<<dim3(static_cast<unsigned>(tiles), parts), kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t append_d(const AppendArgs& a, int B, bool bf16, bool kv8, cudaStream_t st) {
+  if (kv8) return bf16 ? append_go<D, true, true>(a, B, st) : append_go<D, false, true>(a, B, st);
+  return bf16 ? append_go<D, true, false>(a, B, st) : append_go<D, false, false>(a, B, st);
+}
+
+}  // namespace
+
+cudaError_t launch_append_kv(const QsaAppendKvParams& p, const RopeFreqs& rf, bool bf16, bool kv8) {
+  AppendArgs a;
+  a.qkv = p.qkv;
+  a.qw = p.qNormW;
+  a.kw = p.kNormW;
+  a.ctx = p.contextLengths;
+  a.newLen = p.newLengths;
+  a.qout = p.qOut;
+  a.kout = p.kOut;
+  a.vout = p.vOut;
+  a.pool = static_cast<uint8_t*>(p.kvPool);
+  a.scale = p.kvScale;
+  a.pageTable = p.pageTable;
+  a.status = p.status;
+  a.S = p.seqLen;
+  a.Hq = p.numQHeads;
+  a.Hkv = p.numKVHeads;
+  a.rot = p.rotDim;
+  a.poolHeadDim = p.poolHeadDim;
+  a.numFlatPages = p.numFlatPages;
+  a.maxPagesPerSeq = p.maxPagesPerSeq;
+  a.blockShift = 0;
+  while (kv8 && (1 << a.blockShift) < p.scaleBlock) ++a.blockShift;
+  a.tile = std::max(kTile, p.scaleBlock);
+  // the most aligned tiles that seqLen consecutive positions touch
+  a.tiles = static_cast<int>((static_cast<long long>(p.seqLen) + a.tile - 2) / a.tile + 1);
+  a.eps = p.rmsNormEps;
+  for (int i = 0; i < 64; ++i) a.turn[i] = rf.turn[i];
+  cudaStream_t st = static_cast<cudaStream_t>(p.stream);
+  return p.headDim == 64 ? append_d<64>(a, p.batchSize, bf16, kv8, st) : append_d<128>(a, p.batchSize, bf16, kv8, st);
+}
+
+}  // namespace qsa

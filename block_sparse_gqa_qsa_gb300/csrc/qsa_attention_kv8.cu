@@ -1,0 +1,508 @@
+// qsa_attention_kv8.cu -- sparse GQA attention over an 8-bit paged cache
+// (qsa_sparse_paged_kv8): for every live row and query head
+//
+//   o = sum_j softmax_j(scale q . k_j) v_j,   k_j = ks_j c^K_j,  v_j = vs_j c^V_j
+//
+// over the row's list, with e4m3 codes c and one fp32 scale per block of
+// tokens and head.  In log2 units, with x_j = ks_j scale log2(e) (q . c^K_j) and
+// e_j = x_j + log2(vs_j), one pass keeps M = max e_j, l = sum 2^(e_j - M) / vs_j
+// and O = sum 2^(e_j - M) c^V_j: the V scale rides in the exponent, so the
+// probabilities that the second product rounds to fp16 are at most 1 whatever
+// the scales are, and o = O / l.  (log2(vs_j) is the hardware's approximation;
+// its error enters O and l alike.)
+//
+// One CTA of 4 warps takes a (row, KV head) pair; when there are few pairs a
+// cluster of up to 8 CTAs shares one.  The list is dealt out to the warps of
+// the pair in steps of 32 entries, and each warp runs by itself: lane i
+// resolves entry i of its step (list entry two steps ahead, page ids one step
+// ahead, so each dependent load has a step to arrive), then the warp gathers
+// the 32 K and V rows of 128 bytes with cp.async into its own two-slot ring
+// and computes on the step before: no CTA barrier inside the loop.
+// S^T = C^K Q^T and O^T += (C^V)^T P^T are m16n8k16 MMAs with the head group as
+// N.  The summed dims of the first and the output dims of the second may be
+// permuted freely, so a lane reads its codes as whole 16-byte chunks and
+// converts them to fp16 pairs in registers (exact), for V after interleaving
+// the bytes of two keys.
+#include <algorithm>
+
+#include "qsa_internal.h"
+#include "qsa_kv8.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kD = 128;
+constexpr int kStep = 32;                      // list entries of a warp's step
+constexpr int kSlotBytes = kStep * kD * 2;     // K and V rows of a step
+constexpr int kStages = 2;
+constexpr int kRingBytes = kStages * kSlotBytes;
+constexpr int kSmem = kWarps * kRingBytes;
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct PagedArgs {
+  const void* q;
+  const uint8_t* pool;
+  const float* scale;
+  const int32_t* pageTable;
+  const int32_t* indices;
+  const int32_t* ctx;
+  const int32_t* newLen;  // may be null
+  void* o;
+  int32_t* status;  // may be null
+  int S, Hq, Hkv, G, poolHeadDim, numFlatPages, maxPagesPerSeq, topK;
+  int blockShift;  // log2(scaleBlock)
+  int split;       // CTAs per pair: the cluster size
+  float sl2;       // attentionScale * log2(e)
+};
+
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint2 pack4(float4 v) {
+  return kBf16 ? make_uint2(pack_bf162(v.x, v.y), pack_bf162(v.z, v.w))
+               : make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+}
+
+// Byte offset of 16-byte chunk c of key row r in a step's K tile (a lane group reads chunks 0..3 or 4..7 of
+// two neighbouring rows) and V tile (chunks 0, 1 of rows 0, 2, 4, 6): each access covers all banks once.
+__device__ __forceinline__ uint32_t k_off(int r, int c) { return r * kD + ((c ^ ((r & 1) << 2)) << 4); }
+__device__ __forceinline__ uint32_t v_off(int r, int c) { return kStep * kD + r * kD + ((c ^ (r & 6)) << 4); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// A warp's running state: O^T fragments, max and sum of its heads 8 nt + 2 q, 8 nt + 2 q + 1 (q = lane & 3).
+// Tile mt holds dims 16 g + 2 mt (rows g) and 16 g + 2 mt + 1 (rows g + 8), g = lane >> 2.
+template <int NT>
+struct Acc {
+  float o[8][NT][4];
+  float m[NT][2];
+  float l[NT][2];
+};
+
+// What lane i knows of entry i of a step.
+struct Entry {
+  float ks;  // K scale * attentionScale * log2(e); 0 for an entry that names nothing
+  float lv;  // log2(V scale); -inf for an entry that names nothing
+  float iv;  // 1 / V scale; 0 for an entry that names nothing
+};
+
+template <int NT, bool kBf16>
+__device__ __forceinline__ void attend32(Acc<NT>& A, uint32_t slot, const uint32_t (&qf)[NT][8][2],
+                                         const float (&qs)[NT][2], const Entry& en) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  float s[2][NT][4];
+#pragma unroll
+  for (int gk = 0; gk < 2; ++gk) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[gk][nt][0] = s[gk][nt][1] = s[gk][nt][2] = s[gk][nt][3] = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint4 r0 = lds16(slot + k_off(16 * gk + g, q + 4 * half));
+      const uint4 r1 = lds16(slot + k_off(16 * gk + g + 8, q + 4 * half));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a[4];
+        e4m3_to_f16(word(r0, w), a[0], a[2]);
+        e4m3_to_f16(word(r1, w), a[1], a[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[gk][nt], a, qf[nt][4 * half + w][0], qf[nt][4 * half + w][1]);
+      }
+    }
+  }
+  float ks[4], lv[4], iv[4];  // of keys g, g + 8, g + 16, g + 24
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ks[i] = __shfl_sync(kFull, en.ks, g + 8 * i);
+    lv[i] = __shfl_sync(kFull, en.lv, g + 8 * i);
+    iv[i] = __shfl_sync(kFull, en.iv, g + 8 * i);
+  }
+  uint32_t pb[2][NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float& x = s[i >> 1][nt][2 * (i & 1) + h];
+        if constexpr (kBf16) x *= qs[nt][h];
+        x = fmaf(x, ks[i], lv[i]);
+      }
+    float al[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      const float mn = fmaxf(A.m[nt][h], mx);
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      al[h] = ex2_ftz(A.m[nt][h] - mu);
+      A.m[nt][h] = mn;
+      float l = A.l[nt][h] * al[h];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float& x = s[i >> 1][nt][2 * (i & 1) + h];
+        x = ex2_ftz(x - mu);
+        l = fmaf(x, iv[i], l);
+      }
+      A.l[nt][h] = l;
+    }
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      A.o[mt][nt][0] *= al[0];
+      A.o[mt][nt][1] *= al[1];
+      A.o[mt][nt][2] *= al[0];
+      A.o[mt][nt][3] *= al[1];
+    }
+    // P in fp16: at most 1, off by 2^-11 of itself, which the output's own rounding hides
+#pragma unroll
+    for (int gk = 0; gk < 2; ++gk) {
+      pb[gk][nt][0] = movmatrix_t(pack_half2(s[gk][nt][0], s[gk][nt][1]));
+      pb[gk][nt][1] = movmatrix_t(pack_half2(s[gk][nt][2], s[gk][nt][3]));
+    }
+  }
+#pragma unroll
+  for (int gk = 0; gk < 2; ++gk) {
+    const uint4 va = lds16(slot + v_off(16 * gk + 2 * q, g)), vb = lds16(slot + v_off(16 * gk + 2 * q + 1, g));
+    const uint4 vc = lds16(slot + v_off(16 * gk + 2 * q + 8, g)), vd = lds16(slot + v_off(16 * gk + 2 * q + 9, g));
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {  // dims 16 g + 4 w + 2 d and the next one
+        const uint32_t sel = d ? 0x7362 : 0x5140;
+        uint32_t a[4];
+        e4m3_to_f16(__byte_perm(word(va, w), word(vb, w), sel), a[0], a[1]);
+        e4m3_to_f16(__byte_perm(word(vc, w), word(vd, w), sel), a[2], a[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(A.o[2 * w + d][nt], a, pb[gk][nt][0], pb[gk][nt][1]);
+      }
+  }
+}
+
+// The group's Q^T fragments: k-step 4 half + w of a lane covers dims 16 (q + 4 half) + 4 w .. + 3, as the K
+// chunks do.  bf16 values are scaled by a power of two per head to fp16's upper range; qs gets its inverse for
+// the lane's heads 2 q, 2 q + 1.
+template <int NT, bool kBf16>
+__device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT][8][2], float (&qs)[NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int h = 8 * nt + g;
+    uint4 raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      raw[i] = h < G ? __ldg(q + h * (kD / 8) + 2 * (c + 4 * (i >> 1)) + (i & 1)) : make_uint4(0, 0, 0, 0);
+    float up = 1.f, down = 1.f;
+    if constexpr (kBf16) {
+      uint32_t m = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max(m, max(word(raw[i], w) & 0x7fff, (word(raw[i], w) >> 16) & 0x7fff));
+      m = max(m, __shfl_xor_sync(kFull, m, 1));
+      m = max(m, __shfl_xor_sync(kFull, m, 2));
+      // exponent e of the largest: scaled by 2^(14 - e), in two steps that stay normal; none for 0, inf and NaN
+      const int e = static_cast<int>(m >> 7) - 127;
+      if (m != 0 && e < 128) {
+        const int k = 14 - max(e, -100);
+        up = __int_as_float((127 + k) << 23);
+        down = __int_as_float((127 - k) << 23);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t v = word(raw[i], w);
+        if constexpr (kBf16) v = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+        // 16-byte piece i holds dims 16 (c + 4 (i / 2)) + 8 (i & 1) + 2 w: k-step 4 (i / 2) + 2 (i & 1) + w / 2
+        qf[nt][4 * (i >> 1) + 2 * (i & 1) + (w >> 1)][w & 1] = v;
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(kFull, down, 4 * (2 * c + j));
+  }
+}
+
+template <int NT, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 3) sparse_paged_kv8_kernel(const PagedArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(blockIdx.x % a.split);
+  const int pair = static_cast<int>(blockIdx.x / a.split);
+  // a sequence's rows from the last position down: the longest lists start first
+  const int kvh = pair % a.Hkv, rowid = pair / a.Hkv;
+  const int b = rowid / a.S, t = a.S - 1 - rowid % a.S;
+  const int L = static_cast<int>(max(0, min(a.ctx[b], a.maxPagesPerSeq * kTokensPerPage)));
+  const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
+  const size_t bt = static_cast<size_t>(b) * a.S + t;
+  const size_t head0 = bt * a.Hq + static_cast<size_t>(kvh) * a.G;
+  uint2* out = static_cast<uint2*>(a.o) + head0 * (kD / 4);  // 4 values each
+  if (t >= n) {  // the whole cluster leaves
+    if (rank == 0)
+      for (int e = tid; e < a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int32_t* lst = a.indices + bt * a.topK;
+  const int32_t* ptK = a.pageTable + static_cast<size_t>(b) * 2 * a.maxPagesPerSeq;
+  const int32_t* ptV = ptK + a.maxPagesPerSeq;
+  const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
+  const int first = kStep * (rank * kWarps + warp) + lane;
+  const uint32_t ring = smem_addr(smem) + warp * kRingBytes;
+  const size_t rowBytes = static_cast<size_t>(a.Hkv) * a.poolHeadDim;
+  const uint8_t* base = a.pool + static_cast<size_t>(kvh) * a.poolHeadDim + (lane & 7) * 16;
+
+  int bad = 0;
+  auto list_at = [&](int slot) { return slot < a.topK ? __ldg(lst + slot) : -1; };
+  struct Pages {
+    int j, k, v;  // entry (-1: none), its page ids
+  };
+  auto pages_of = [&](int j) {
+    Pages p{-1, -1, -1};
+    if (static_cast<unsigned>(j) < static_cast<unsigned>(L)) {
+      p.j = j;
+      p.k = __ldg(ptK + (j >> 7));
+      p.v = __ldg(ptV + (j >> 7));
+    } else if (j != -1) {
+      bad |= kErrBadIndex;
+    }
+    return p;
+  };
+  // Gathers a step's rows into ring slot `stage` (one copy group, empty if the step names nothing).
+  auto gather = [&](const Pages& p, int stage, Entry& en) -> bool {
+    const bool ok = p.j >= 0 && static_cast<unsigned>(p.k) < static_cast<unsigned>(a.numFlatPages) &&
+                    static_cast<unsigned>(p.v) < static_cast<unsigned>(a.numFlatPages);
+    if (p.j >= 0 && !ok) bad |= kErrBadPage;
+    const bool any = __any_sync(kFull, ok);
+    en = Entry{0.f, -INFINITY, 0.f};
+    if (any) {
+      const int in = p.j & 127;
+      const int krow = ok ? p.k * kTokensPerPage + in : -1, vrow = ok ? p.v * kTokensPerPage + in : -1;
+      float ks = 0.f, vs = 0.f;
+      if (ok) {
+        ks = __ldg(a.scale + static_cast<size_t>(krow >> a.blockShift) * a.Hkv + kvh);
+        vs = __ldg(a.scale + static_cast<size_t>(vrow >> a.blockShift) * a.Hkv + kvh);
+      }
+      const uint32_t dst = ring + stage * kSlotBytes;
+#pragma unroll
+      for (int i = 0; i < kStep / 4; ++i) {  // 8 lanes copy one 128-byte row
+        const int r = 4 * i + (lane >> 3), c = lane & 7;
+        const int kr = __shfl_sync(kFull, krow, r), vr = __shfl_sync(kFull, vrow, r);
+        cp_async16(dst + k_off(r, c), base + static_cast<size_t>(max(kr, 0)) * rowBytes, kr >= 0);
+        cp_async16(dst + v_off(r, c), base + static_cast<size_t>(max(vr, 0)) * rowBytes, vr >= 0);
+      }
+      if (ok) {
+        vs = read_scale(vs);
+        en = Entry{read_scale(ks) * a.sl2, __log2f(vs), 1.0f / vs};
+      }
+    }
+    cp_async_commit();
+    return any;
+  };
+
+  Acc<NT> A;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) A.o[mt][nt][0] = A.o[mt][nt][1] = A.o[mt][nt][2] = A.o[mt][nt][3] = 0.f;
+    A.m[nt][0] = A.m[nt][1] = -INFINITY;
+    A.l[nt][0] = A.l[nt][1] = 0.f;
+  }
+  const int steps = max(0, (a.topK - (first - lane) + hop - 1) / hop);
+  int j2 = list_at(first + hop);
+  Pages p1 = pages_of(list_at(first));
+  uint32_t qf[NT][8][2];
+  float qs[NT][2];
+  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + head0 * (kD / 8), a.G, qf, qs);
+  Entry now, next;
+  bool anyNow = gather(p1, 0, now), anyNext = false;
+  p1 = pages_of(j2);
+  j2 = list_at(first + 2 * hop);
+  for (int i = 0; i < steps; ++i) {
+    __syncwarp();  // every lane is done with the slot of step i - 1
+    anyNext = gather(p1, (i + 1) & 1, next);
+    p1 = pages_of(j2);
+    j2 = i + 3 < steps ? list_at(first + (i + 3) * hop) : -1;
+    cp_async_wait<1>();
+    __syncwarp();
+    if (anyNow) attend32<NT, kBf16>(A, ring + (i & 1) * kSlotBytes, qf, qs, now);
+    now = next;
+    anyNow = anyNext;
+  }
+  cp_async_wait<0>();
+  bad = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
+  if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
+  __syncthreads();  // the rings become the merge buffers
+
+  // Per warp [8 NT heads][128 dims] fp32 and (m, l); 16-byte units of a head XOR-swizzled by its pair index, so
+  // that both the writes below and the row-wise reads are free of bank conflicts.
+  constexpr int H = 8 * NT;
+  float4* ow = reinterpret_cast<float4*>(smem);                  // [kWarps][H][32]
+  float* mw = reinterpret_cast<float*>(ow + kWarps * H * 32);    // [kWarps][H]
+  float* lw = mw + kWarps * H;
+  float4* oc = reinterpret_cast<float4*>(lw + kWarps * H);       // the CTA's merged [H][32], in plain order
+  float* mc = reinterpret_cast<float*>(oc + H * 32);
+  float* lc = mc + H;
+  const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h = 8 * nt + 2 * q + j;
+      float l = A.l[nt][j];
+      l += __shfl_xor_sync(kFull, l, 4);
+      l += __shfl_xor_sync(kFull, l, 8);
+      l += __shfl_xor_sync(kFull, l, 16);
+      if (g == 0) {
+        mw[warp * H + h] = A.m[nt][j];
+        lw[warp * H + h] = l;
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        ow[(warp * H + h) * 32 + 4 * g + (w ^ q)] = make_float4(A.o[2 * w][nt][j], A.o[2 * w][nt][2 + j],
+                                                               A.o[2 * w + 1][nt][j], A.o[2 * w + 1][nt][2 + j]);
+    }
+  __syncthreads();
+  for (int h = warp; h < a.G; h += kWarps) {
+    float M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mw[w * H + h]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float m = mw[w * H + h], f = m == -INFINITY ? 0.f : exp2f(m - M);
+      const float4 x = ow[(w * H + h) * 32 + (lane ^ ((h >> 1) & 3))];
+      l += f * lw[w * H + h];
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
+    }
+    if (a.split > 1) {
+      oc[h * 32 + lane] = o;
+      if (lane == 0) {
+        mc[h] = M;
+        lc[h] = l;
+      }
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      out[h * 32 + lane] = pack4<kBf16>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+  }
+  if (a.split == 1) return;
+  // Join over the cluster: head h by one warp of it.
+  cluster_sync_all();
+  const uint32_t ocAddr = smem_addr(oc), mcAddr = smem_addr(mc);
+  for (int h = rank * kWarps + warp; h < a.G; h += a.split * kWarps) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ms[kMaxCluster], M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      ms[r] = r < a.split ? cluster_ld(cluster_addr(mcAddr + h * 4, r)) : -INFINITY;
+      M = fmaxf(M, ms[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < a.split) {
+        const float f = ms[r] == -INFINITY ? 0.f : exp2f(ms[r] - M);
+        const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * 32 + lane) * 16, r));
+        l += f * cluster_ld(cluster_addr(mcAddr + (H + h) * 4, r));
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    out[h * 32 + lane] = pack4<kBf16>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  }
+  cluster_sync_all();  // no CTA leaves while another reads its shared memory
+}
+
+template <int NT, bool kBf16>
+cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
+  auto kernel = sparse_paged_kv8_kernel<NT, kBf16>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  // As many CTAs per pair as stay resident at once (three per SM), at most one per 128 entries of the list.
+  const long long slots = 3LL * sm_count();
+  const int most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
+  a.split = static_cast<int>(std::max<long long>(1, std::min<long long>(most, slots / pairs)));
+  if (pairs * a.split > 0x7fffffffLL) a.split = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_sparse_paged_kv8(const QsaSparsePagedKv8Params& p, bool bf16) {
+  PagedArgs a;
+  a.q = p.qPtr;
+  a.pool = static_cast<const uint8_t*>(p.kvPool);
+  a.scale = p.kvScale;
+  a.pageTable = p.pageTable;
+  a.indices = p.indices;
+  a.ctx = p.contextLengths;
+  a.newLen = p.newLengths;
+  a.o = p.oPtr;
+  a.status = p.status;
+  a.S = p.seqLen;
+  a.Hq = p.numQHeads;
+  a.Hkv = p.numKVHeads;
+  a.G = p.numQHeads / p.numKVHeads;
+  a.poolHeadDim = p.poolHeadDim;
+  a.numFlatPages = p.numFlatPages;
+  a.maxPagesPerSeq = p.maxPagesPerSeq;
+  a.topK = p.topK;
+  a.blockShift = 0;
+  while ((1 << a.blockShift) < p.scaleBlock) ++a.blockShift;
+  a.split = 1;
+  a.sl2 = p.attentionScale * kLog2e;
+  const long long pairs = static_cast<long long>(p.batchSize) * p.seqLen * p.numKVHeads;
+  cudaStream_t st = static_cast<cudaStream_t>(p.stream);
+  if (bf16) return a.G <= 8 ? paged_go<1, true>(a, pairs, st) : paged_go<2, true>(a, pairs, st);
+  return a.G <= 8 ? paged_go<1, false>(a, pairs, st) : paged_go<2, false>(a, pairs, st);
+}
+
+}  // namespace qsa

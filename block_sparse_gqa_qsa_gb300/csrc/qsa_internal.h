@@ -54,6 +54,11 @@ cudaError_t launch_sparse_decode(const QsaSparseDecodeParams& p, bool bf16 = fal
 cudaError_t launch_rope_qkv(const QsaRopeQkvParams& p, const RopeFreqs& rf);
 constexpr int kRopeMaxRowBytes = 64 * 1024;  // one token's packed heads, staged in shared memory
 
+// Paged cache ---------------------------------------------------------------
+// kv8: an e4m3 pool with block scales instead of a pool of the inputs' 16-bit type.
+cudaError_t launch_append_kv(const QsaAppendKvParams& p, const RopeFreqs& rf, bool bf16, bool kv8);
+cudaError_t launch_sparse_paged_kv8(const QsaSparsePagedKv8Params& p, bool bf16);
+
 cudaError_t launch_gather(const QsaGatherParams& p);
 int gather_scratch_pages(int topK);
 int gather_max_row_chunks();  // 16-byte chunks of one K (or V) token row a warp copies

@@ -411,6 +411,152 @@ QSA_API int32_t qsa_gather_scratch_pages(int32_t topK);
 /* Elements (halves) of the scratch: 2 * batchSize * P * 128 * numKVHeads * headDim (0 when invalid). */
 QSA_API size_t qsa_gather_scratch_elems(int32_t batchSize, int32_t numKVHeads, int32_t headDim, int32_t topK);
 
+/* ------------------------------------------------------------- paged cache */
+
+/* Appends the keys and values of new tokens to a paged cache: the per-head
+ * norm and the rotation of qsa_rope_qkv for any number of new tokens per
+ * sequence behind any number of cached ones (one decoded token, drafted
+ * tokens, a chunk of a prompt, a whole prompt), into a pool of the inputs'
+ * 16-bit type or into an 8-bit pool.
+ *
+ * Sequence b has L = contextLengths[b] tokens, the last n of them new, with
+ * n = newLengths[b] cut to 0..min(seqLen, L) (newLengths NULL: min(seqLen, L),
+ * i.e. a prefill from position 0, or one token when seqLen is 1).  Row t < n
+ * is the token at position p = L - n + t:
+ *   q/k heads: y = x / sqrt(mean(x^2) + eps) * (1 + w), then the half-split
+ *              rotation of dims [0, rotDim) at p, in fp32;
+ *   v heads:   as they are.
+ * qOut gets the q heads, rounded once; kOut / vOut (dense mirrors, NULL for
+ * none) the k heads, rounded once, and the v heads.  Rows t >= n are padding:
+ * zeros there, and never read.  The pool row of token p (page table row 0 for
+ * K, row 1 for V, page p / 128) gets its leading headDim columns; nothing else
+ * of the pool is written, except in a block of an 8-bit pool (below).
+ *
+ * qsa_append_kv / _bf16: all tensors fp16 / bf16; the pool holds what kOut and
+ * vOut hold.  kvScale must be NULL and scaleBlock 0.
+ *
+ * qsa_append_kv8 / _bf16: qkv and the dense outputs fp16 / bf16, the pool one
+ * byte per value, e4m3 (4 significant bits, largest value 448, no infinities,
+ * NaN 0x7f), with one fp32 scale per block: the scaleBlock consecutive tokens
+ * (a power of two, 1..128, so blocks never cross a page) of one page and one
+ * KV head, at kvScale[page][token in page / scaleBlock][head].  A stored value
+ * stands for code * scale.  Values are quantised from fp32, to nearest even:
+ *   - a block whose first token is among the new ones: scale = amax / 448,
+ *     amax the largest finite |value| of its new tokens;
+ *   - a block that holds older tokens of the sequence keeps its scale s if
+ *     amax <= 448 s; otherwise its scale becomes s * 2^k with the smallest
+ *     sufficient k and the older tokens' codes are divided by 2^k, which is
+ *     exact unless a code leaves the normal range of e4m3 (below 2^-6).
+ * Scales stay in [2^-48, 2^48] (larger values saturate at 448 * 2^48); an
+ * infinite or NaN value is stored as NaN.  A block that receives new tokens
+ * must not be shared with another sequence of the call.
+ *
+ * status (may be NULL): a device int32 that the kernel ORs bits into and
+ * never clears -- bit 1 (value 2): a new token's page id lies outside
+ * [0, numFlatPages), or its position behind the page table; that row of the
+ * pool is not written (its dense outputs are).
+ * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1, an odd
+ * rotDim or rotDim > headDim, theta <= 0, eps < 0, poolHeadDim < headDim, a
+ * scaleBlock that is not a power of two in 1..128 (8-bit) or kvScale /
+ * scaleBlock given for a 16-bit pool; QSA_ERR_UNSUPPORTED for headDim not
+ * 64/128, rotDim not a multiple of 16, pool rows (poolHeadDim elements) not a
+ * multiple of 16 bytes, a tensor not 16-byte aligned (kvScale and the int32
+ * tensors: 4), numQHeads or numKVHeads above 1024, or sizes past int32 row
+ * ids (batchSize * seqLen and numFlatPages * 128 below 2^31).  Every buffer is
+ * the caller's; nothing is allocated and no workspace is used. */
+typedef struct {
+  const void* qkv;               /* fp16 or bf16 [B, S, numQHeads + 2*numKVHeads, headDim]: q, then k, then v heads */
+  const float* qNormW;           /* fp32 [headDim]                                                       */
+  const float* kNormW;           /* fp32 [headDim]                                                       */
+  const int32_t* contextLengths; /* int32 [B]: total lengths, new tokens included                        */
+  const int32_t* newLengths;     /* int32 [B]: new tokens, or NULL (see above)                           */
+  void* qOut;                    /* out [B, S, numQHeads, headDim], type of qkv                          */
+  void* kOut;                    /* out [B, S, numKVHeads, headDim], type of qkv, or NULL                */
+  void* vOut;                    /* out [B, S, numKVHeads, headDim], type of qkv, or NULL                */
+  void* kvPool;                  /* in/out [numFlatPages, 128, numKVHeads, poolHeadDim]: qkv's type, or e4m3 bytes */
+  float* kvScale;                /* in/out fp32 [numFlatPages, 128 / scaleBlock, numKVHeads] (8-bit), else NULL */
+  const int32_t* pageTable;      /* int32 [B, 2, maxPagesPerSeq] (row 1: V page ids)                     */
+  int32_t* status;               /* optional device error word, or NULL                                  */
+  int32_t batchSize;
+  int32_t seqLen;                /* S: padded rows per sequence                                          */
+  int32_t numQHeads;
+  int32_t numKVHeads;
+  int32_t headDim;               /* 64 or 128                                                            */
+  int32_t rotDim;                /* multiple of 16, <= headDim                                           */
+  int32_t poolHeadDim;           /* elements of a pool row, >= headDim                                   */
+  int32_t numFlatPages;
+  int32_t maxPagesPerSeq;
+  int32_t scaleBlock;            /* tokens per scale (8-bit): 1, 2, 4 .. 128; else 0                     */
+  float ropeTheta;
+  float rmsNormEps;
+  void* stream;
+} QsaAppendKvParams;
+
+QSA_API qsa_status_t qsa_append_kv(const QsaAppendKvParams* params);
+QSA_API qsa_status_t qsa_append_kv_bf16(const QsaAppendKvParams* params);
+QSA_API qsa_status_t qsa_append_kv8(const QsaAppendKvParams* params);
+QSA_API qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* params);
+
+/* Sparse GQA attention over an 8-bit paged cache (the pool and scales that
+ * qsa_append_kv8 fills), for any number of query rows per sequence: one
+ * decoded token, drafted tokens, a chunk of a prompt or a whole prompt.  For
+ * row t < n of sequence b (n = newLengths[b] cut to 0..min(seqLen, L);
+ * newLengths NULL: min(seqLen, L)) and query head h (KV head g = h /
+ * (numQHeads / numKVHeads)):
+ *   o[b,t,h] = sum_{j in list} softmax_j(attentionScale * q[b,t,h] . k[j,g]) v[j,g]
+ * over the entries j of indices[b,t,:] inside [0, L); k and v are the cached
+ * values code * scale.  Causality lives in the list, an entry named twice
+ * counts twice, and rows t >= n and rows whose list names nothing are exact
+ * zeros.  The lists are those of qsa_indexer_decode (seqLen 1) or
+ * qsa_indexer_prefill (a whole prompt).  A scale outside [2^-48, 2^48] is read
+ * as the nearer bound (NaN as the lower); a NaN code makes the outputs that
+ * use it NaN.
+ * Arithmetic: codes enter the products exactly (fp16), bf16 queries as fp16
+ * after a power-of-two scaling per row and head that keeps every value within
+ * 2^-38 of the row's largest; products accumulate in fp32, the softmax is
+ * fp32, each probability times its V scale is rounded to fp16 relative to the
+ * largest such product, and the output is rounded once.  Repeated calls give
+ * identical bits.
+ * When there are few (row, KV head) pairs, a list is split over the CTAs of a
+ * cluster (at most 8), which join their partial results on chip: there is no
+ * workspace, and calls may run concurrently.
+ * status (may be NULL): bits as for qsa_sparse_decode -- 2: a named token's
+ * page id lies outside [0, numFlatPages); 4: an entry other than -1 lies
+ * outside [0, L).  Such entries are skipped.
+ * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1,
+ * numQHeads not a multiple of numKVHeads, poolHeadDim < headDim or a scaleBlock
+ * that is not a power of two in 1..128; QSA_ERR_UNSUPPORTED for headDim other
+ * than 128, more than 16 query heads per KV head, poolHeadDim not a multiple of
+ * 16, q / kvPool / o not 16-byte aligned (kvScale and the int32 tensors: 4),
+ * topK above 2^24, or sizes past int32 ids (batchSize * seqLen * numKVHeads
+ * and numFlatPages * 128 below 2^31). */
+typedef struct {
+  const void* qPtr;              /* fp16 or bf16 [B, S, numQHeads, 128]                                   */
+  const void* kvPool;            /* e4m3 bytes [numFlatPages, 128, numKVHeads, poolHeadDim]               */
+  const float* kvScale;          /* fp32 [numFlatPages, 128 / scaleBlock, numKVHeads]                     */
+  const int32_t* pageTable;      /* int32 [B, 2, maxPagesPerSeq] (row 1: V page ids)                      */
+  const int32_t* indices;        /* int32 [B, S, topK]; -1 names nothing                                  */
+  const int32_t* contextLengths; /* int32 [B]: total lengths                                              */
+  const int32_t* newLengths;     /* int32 [B]: query rows, or NULL                                        */
+  void* oPtr;                    /* out [B, S, numQHeads, 128], type of q                                 */
+  int32_t batchSize;
+  int32_t seqLen;                /* S: padded rows per sequence                                           */
+  int32_t numQHeads;
+  int32_t numKVHeads;            /* numQHeads / numKVHeads must be 1..16                                  */
+  int32_t headDim;               /* 128                                                                   */
+  int32_t poolHeadDim;           /* bytes of a pool row, >= headDim, multiple of 16                       */
+  int32_t numFlatPages;
+  int32_t maxPagesPerSeq;
+  int32_t topK;
+  int32_t scaleBlock;            /* tokens per scale: 1, 2, 4 .. 128                                      */
+  float attentionScale;
+  void* stream;
+  int32_t* status;               /* optional device error word, or NULL                                   */
+} QsaSparsePagedKv8Params;
+
+QSA_API qsa_status_t qsa_sparse_paged_kv8(const QsaSparsePagedKv8Params* params);
+QSA_API qsa_status_t qsa_sparse_paged_kv8_bf16(const QsaSparsePagedKv8Params* params);
+
 /* Workspace bytes of the indexers (0 when the sizes are invalid). */
 QSA_API size_t qsa_indexer_prefill_workspace_size(int32_t batchSize, int32_t seqLen, int32_t headDim,
                                           int32_t compressRatio);

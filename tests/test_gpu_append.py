@@ -1,0 +1,296 @@
+"""qsa_append_kv / qsa_append_kv8 (fp16 and bf16) against plain 64-bit forms.
+
+Bars.  A dense output or 16-bit pool value is the fp32 evaluation rounded once: within one step of its type of the
+64-bit value's rounding, plus the evaluation's own error, 2^-18 for normalised values up to about 6 (a few units of
+2^-24 of each operand).  V values are copies.  A scale is amax / 448 within 2^-18 / 448 plus two fp32 roundings; a code
+times its scale is within half an e4m3 step of the value (2^-4 relative, 2^-10 scales absolute) plus the same 2^-18."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import paged_cache_ref as ref
+from block_sparse_gqa_qsa_gb300 import _binding as qb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+EVAL = 2.0 ** -18
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from block_sparse_gqa_qsa_gb300 import build
+    build.build()
+    qb.lib()
+
+
+def make(dtype, D, Hq, Hkv, S, ctx, new, block, extra=0, tail=0, seed=0):
+    """Inputs on the CPU; padding rows are NaN, the cache holds random values."""
+    g = torch.Generator().manual_seed(100 + seed)
+    B = len(ctx)
+    n = ref.new_rows(ctx, new, S)
+    qkv = torch.randn((B, S, Hq + 2 * Hkv, D), generator=g).to(dtype)
+    for b in range(B):
+        qkv[b, n[b]:] = float("nan")
+    pt, flat = ref.page_tables(ctx, 7 + seed, extra)
+    c = dict(qkv=qkv, wq=0.1 * torch.randn(D, generator=g), wk=0.1 * torch.randn(D, generator=g),
+             ctx=torch.tensor(ctx, dtype=torch.int32), pt=pt, n=n,
+             new=None if new is None else torch.tensor(new, dtype=torch.int32), Hq=Hq, Hkv=Hkv, S=S, D=D, block=block)
+    if block:
+        c["pool"] = ref.random_codes((flat, 128, Hkv, D + tail), 9 + seed)
+        c["scale"] = 0.0078 * torch.exp(0.3 * torch.randn((flat, 128 // block, Hkv), generator=g))
+    else:
+        c["pool"] = torch.randn((flat, 128, Hkv, D + tail), generator=g).to(dtype)
+    return c
+
+
+def run(c, rot, dense=True, status=None, stream=None):
+    """The call on the GPU; returns q, k, v, pool, scale on the CPU."""
+    B, S, D, Hq, Hkv = len(c["n"]), c["S"], c["D"], c["Hq"], c["Hkv"]
+    et = c["qkv"].dtype
+    q = torch.full((B, S, Hq, D), float("nan"), dtype=et, device=DEV)
+    k, v = (torch.full((B, S, Hkv, D), float("nan"), dtype=et, device=DEV) if dense else None for _ in range(2))
+    pool = c["pool"].to(DEV)
+    new = None if c["new"] is None else c["new"].to(DEV)
+    kw = dict(Hq=Hq, Hkv=Hkv, rot=rot, theta=ref.THETA, eps=ref.EPS, new_lengths=new, k_out=k, v_out=v, status=status,
+              stream=stream)
+    a = (c["qkv"].to(DEV), c["wq"].to(DEV), c["wk"].to(DEV), c["ctx"].to(DEV), q, pool)
+    if c["block"]:
+        scale = c["scale"].to(DEV)
+        qb.append_kv8(*a, scale, c["pt"].to(DEV), **kw)
+    else:
+        scale = None
+        qb.append_kv(*a, c["pt"].to(DEV), **kw)
+    torch.cuda.synchronize()
+    return [None if t is None else t.cpu() for t in (q, k, v, pool, scale)]
+
+
+def step_of(x, dtype):
+    """One step of a 16-bit type at |x| (float64)."""
+    bits, low = (11, -24) if dtype == torch.float16 else (8, -133)
+    _, e = torch.frexp(x.abs())
+    return torch.ldexp(torch.ones_like(x), (e - bits).clamp(min=low))
+
+
+def check_dense(got, want, dtype):
+    bar = step_of(want, dtype) + EVAL
+    err = (got.double() - want).abs()
+    assert bool((err <= bar).all()), float((err - bar).max())
+
+
+def check(c, rot, out, dense=True, skip=()):
+    """Every output of a call against 64 bits; `skip`: (b, plane, page index) whose rows must not be written."""
+    q, k, v, pool, scale = out
+    B, S, D, Hq, Hkv, blk = len(c["n"]), c["S"], c["D"], c["Hq"], c["Hkv"], c["block"]
+    et = c["qkv"].dtype
+    bytes_before, bytes_after = c["pool"].view(torch.uint8).flatten(-1), pool.view(torch.uint8)
+    allowed = torch.zeros(pool.shape, dtype=torch.bool)  # elements a call may write
+    scales_allowed = torch.zeros(c["scale"].shape, dtype=torch.bool) if blk else None
+    for b in range(B):
+        n, L = c["n"][b], int(c["ctx"][b])
+        start = L - n
+        for t in (q, k, v) if dense else (q,):
+            assert not t[b, n:].view(torch.int16).any(), "padding rows are zeros"
+        if n == 0:
+            continue
+        x = c["qkv"][b, :n]
+        pos = torch.arange(start, L)
+        wantq = ref.normed_rotated(x[:, :Hq], c["wq"], pos, rot)
+        wantk = ref.normed_rotated(x[:, Hq:Hq + Hkv], c["wk"], pos, rot)
+        check_dense(q[b, :n], wantq, et)
+        if dense:
+            check_dense(k[b, :n], wantk, et)
+            assert torch.equal(v[b, :n].view(torch.int16), x[:, Hq + Hkv:].contiguous().view(torch.int16))
+        for plane, want in ((0, wantk), (1, x[:, Hq + Hkv:].double())):
+            live = [i for i in range(n) if (b, plane, (start + i) // 128) not in skip]
+            if not live:
+                continue
+            live = torch.tensor(live)
+            p = pos[live]
+            page, off = c["pt"][b, plane, p // 128].long(), p % 128
+            allowed[page, off, :, :D] = True
+            rows = pool[page, off, :, :D] if not blk else None
+            if not blk:
+                if plane:
+                    assert torch.equal(rows.view(torch.int16), x[live][:, Hq + Hkv:].contiguous().view(torch.int16))
+                else:
+                    check_dense(rows, want[live], et)
+                    if dense:
+                        assert torch.equal(rows.view(torch.int16), k[b, live].view(torch.int16))
+                continue
+            s = scale[page, off // blk].double()
+            codes = ref.E4M3[bytes_after[page, off][..., :D].long()]
+            err = (codes * s[..., None] - want[live]).abs()
+            bar = torch.maximum(2.0 ** -4 * want[live].abs(), 2.0 ** -10 * s[..., None].expand_as(err)) + EVAL
+            assert bool((err <= bar).all()), float((err - bar).max())
+            first = start // blk
+            for i in sorted({int(y) // blk for y in p}):
+                mine = live[(p // blk) == i]
+                amax = want[mine].abs().amax((0, 2))
+                pg, at = int(c["pt"][b, plane, i * blk // 128]), (i * blk % 128) // blk
+                scales_allowed[pg, at] = True
+                got, had = scale[pg, at].double(), c["scale"][pg, at].double()
+                if i > first or start % blk == 0:
+                    expect = (amax / 448).clamp(2.0 ** -48, 2.0 ** 48)
+                    assert bool(((got - expect).abs() <= EVAL / 448 + 2.0 ** -22 * expect).all())
+                    continue
+                up = torch.log2(got / had)
+                assert torch.equal(up, up.round()) and bool((up >= 0).all()), "older blocks grow by powers of two"
+                assert bool((amax <= 448 * got * (1 + 2.0 ** -20) + EVAL).all()), "the new tokens fit"
+                assert bool(((up == 0) | (amax > 224 * got * (1 - 2.0 ** -20) - EVAL)).all()), "no more than needed"
+                old = torch.arange(i * blk, start) % 128
+                if old.numel():
+                    allowed[pg, old, :, :D] = True
+                    was = ref.E4M3[c["pool"].view(torch.uint8)[pg, old][..., :D].long()] * (had / got)[:, None]
+                    is_ = ref.E4M3[bytes_after[pg, old][..., :D].long()]
+                    exact = was.abs() >= 2.0 ** -6
+                    assert torch.equal(was[exact], is_[exact]), "a power of two is exact in e4m3's normal range"
+                    assert bool(((was - is_).abs() <= 2.0 ** -10).all())
+    same = c["pool"].view(torch.uint8) == bytes_after if blk else c["pool"].view(torch.int16) == pool.view(torch.int16)
+    assert bool(same[~allowed].all()), "only the new tokens' rows and their blocks change"
+    if blk:
+        assert torch.equal(scale[~scales_allowed], c["scale"][~scales_allowed])
+
+
+ONE = dict(S=1, ctx=(1, 16, 17, 128, 5000, 0), new=None)
+CHUNK = dict(S=41, ctx=(41, 140, 1033, 300, 12, 0, 77), new=(41, 37, 1, 0, 41, 5, -3))  # page ends inside, n > ctx, n < 0
+WHOLE = dict(S=301, ctx=(301, 1, 150), new=None)
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("rows", (ONE, CHUNK, WHOLE), ids=("one", "chunk", "whole"))
+@pytest.mark.parametrize("block", (0, 1, 16, 128))
+def test_append(dtype, rows, block):
+    c = make(dtype, 128, 8, 2, rows["S"], rows["ctx"], rows["new"], block, extra=2, tail=32, seed=block)
+    check(c, 64, run(c, 64))
+
+
+@pytest.mark.parametrize("block", (0, 2, 4, 8, 32, 64))
+@pytest.mark.parametrize("D,rot,Hq,Hkv", [(64, 32, 7, 1), (64, 0, 1, 1), (128, 128, 24, 2), (128, 16, 33, 3),
+                                          (128, 0, 16, 16), (64, 64, 64, 8)])
+def test_append_heads(block, D, rot, Hq, Hkv):
+    c = make(torch.float16, D, Hq, Hkv, 70, (70, 133, 700), (33, 70, 70), block, seed=D + rot + block)
+    out = run(c, rot, dense=False)
+    check(c, rot, out, dense=False)
+
+
+def test_append_many_tiles():
+    """More tiles than the GPU holds at once, and a whole prompt far from position 0."""
+    c = make(torch.bfloat16, 128, 8, 1, 2100, (2100, 65536, 1999, 2100), (2100, 2100, 1999, 700), 16, seed=5)
+    check(c, 64, run(c, 64))
+
+
+@pytest.mark.parametrize("block", (4, 16, 64))
+def test_growing_blocks(block):
+    """Tokens one at a time, each three times larger than the one before: every block's scale grows as it fills."""
+    c = make(torch.float16, 128, 4, 2, 1, (1, 60), None, block, extra=4, seed=3)
+    for i in range(11):
+        check(c, 32, (out := run(c, 32)))
+        c["pool"], c["scale"] = out[3], out[4]
+        c["ctx"] = c["ctx"] + 1
+        c["qkv"] = torch.randn(c["qkv"].shape, generator=torch.Generator().manual_seed(i)).half()
+        c["qkv"][:, :, 6:] *= min(3.0 ** i, 8000.0)  # V; K is normed, so its scales hardly grow
+
+
+def test_zeros_then_values():
+    """A block of zeros has the smallest scale; the first real token in it grows it and leaves the zeros zero."""
+    c = make(torch.float16, 128, 4, 1, 3, (3,), None, 16)
+    c["qkv"][:, :, 4:] = 0
+    out = run(c, 0)
+    check(c, 0, out)
+    assert float(out[4][int(c["pt"][0, 1, 0]), 0, 0]) == 2.0 ** -48
+    c["pool"], c["scale"], c["ctx"] = out[3], out[4], torch.tensor([4], dtype=torch.int32)
+    c["new"], c["n"] = torch.tensor([1], dtype=torch.int32), [1]
+    c["qkv"] = torch.randn(c["qkv"].shape, generator=torch.Generator().manual_seed(1)).half()
+    c["qkv"][:, 1:] = float("nan")
+    out = run(c, 0)
+    check(c, 0, out)
+    assert not ref.E4M3[out[3].view(torch.uint8)[int(c["pt"][0, 1, 0]), :3].long()].any()
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+def test_values_that_are_no_numbers(dtype):
+    """NaN and infinite V values are stored as NaN and do not enter the scale; their neighbours are unharmed."""
+    c = make(dtype, 128, 4, 2, 20, (20,), None, 16)
+    clean = run(c, 64)
+    c["qkv"][0, 3, 6, 5], c["qkv"][0, 9, 7, 0] = float("inf"), float("nan")
+    c["qkv"][0, 17, 6, 127] = float("-inf")
+    q, k, v, pool, scale = run(c, 64)
+    page = int(c["pt"][0, 1, 0])
+    codes = pool.view(torch.uint8)[page, :20, :, :128] & 0x7f
+    bad = torch.zeros(20, 2, 128, dtype=torch.bool)
+    bad[3, 0, 5] = bad[9, 1, 0] = bad[17, 0, 127] = True
+    assert bool((codes[bad] == 0x7f).all()) and not bool((codes[~bad] == 0x7f).any())
+    finite = torch.where(torch.isfinite(c["qkv"][0, :, 6:].float()), c["qkv"][0, :, 6:].float().abs(), torch.zeros(()))
+    want = torch.stack([finite[:16].amax((0, 2)), finite[16:].amax((0, 2))]) / 448
+    assert torch.equal(scale[page, :2], want)
+    assert torch.equal(k.view(torch.int16), clean[1].view(torch.int16))
+
+
+def test_large_bf16_values():
+    """Squares past fp32's range: the norm of rows of 1e30 is that of rows of 1."""
+    c = make(torch.bfloat16, 128, 4, 1, 5, (5,), None, 0)
+    small = run(c, 64)
+    c["qkv"] = (c["qkv"].float() * 2.0 ** 100).bfloat16()
+    big = run(c, 64)
+    # eps is 1e-6 of a mean square near 1: 5e-7 relative, under a quarter of which rounds differently
+    err = (big[0].double() - small[0].double()).abs()
+    assert bool((err <= step_of(small[0].double(), torch.bfloat16)).all())
+
+
+@pytest.mark.parametrize("block", (0, 16, 64))
+def test_bad_pages(block):
+    """Page ids outside the pool and positions behind the table: skipped, reported, the rest written."""
+    c = make(torch.float16, 128, 4, 2, 300, (300, 200), None, block, seed=8)
+    flat = c["pool"].shape[0]
+    c["pt"][0, 0, 1], c["pt"][1, 1, 0] = -1, flat
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = run(c, 64, status=status)
+    assert int(status) == 2
+    check(c, 64, out, skip={(0, 0, 1), (1, 1, 0)})
+    c = make(torch.float16, 128, 4, 2, 300, (300, 200), None, block, seed=9)
+    c["pt"] = c["pt"][:, :, :2].contiguous()  # tokens 256 .. 299 have no entry
+    status.zero_()
+    out = run(c, 64, status=status)
+    assert int(status) == 2
+    check(c, 64, out, skip={(0, 0, 2), (0, 1, 2)})
+    status.zero_()
+    c = make(torch.float16, 128, 4, 2, 30, (30, 20), None, block, seed=9)
+    check(c, 64, run(c, 64, status=status))
+    assert int(status) == 0
+
+
+def test_pool_beyond_4_gib():
+    """Rows past 2^32 bytes."""
+    flat, Hkv, D = 34000, 8, 128  # 4.46e9 bytes
+    pool = torch.zeros((flat, 128, Hkv, D), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    scale = torch.ones((flat, 8, Hkv), device=DEV)
+    g = torch.Generator().manual_seed(4)
+    qkv = torch.randn((1, 4, 8 + 2 * Hkv, D), generator=g).half()
+    pt = torch.tensor([[[5], [flat - 1]]], dtype=torch.int32)
+    ctx = torch.tensor([4], dtype=torch.int32)
+    q = torch.empty((1, 4, 8, D), dtype=torch.float16, device=DEV)
+    w = torch.zeros(D, device=DEV)
+    qb.append_kv8(qkv.to(DEV), w, w, ctx.to(DEV), q, pool, scale, pt.to(DEV), Hq=8, Hkv=Hkv, rot=64, theta=1e4, eps=1e-6)
+    v = qkv[0, :, 8 + Hkv:].double()
+    s = scale[flat - 1, 0].cpu().double()
+    got = ref.E4M3[pool[flat - 1, :4].view(torch.uint8).cpu().long()] * s[:, None]
+    assert torch.equal(s.float(), (v.abs().amax((0, 2)) / 448).float())
+    assert bool(((got - v).abs() <= torch.maximum(2.0 ** -4 * v.abs(), 2.0 ** -10 * s[:, None].expand_as(v)) + 2.0 ** -22 * v.abs()).all())
+    assert int(pool.view(torch.uint8)[6:flat - 1].max()) == 0
+
+
+def test_append_equals_rope():
+    """Where qsa_rope_qkv applies (fp16, from position 0 or one token) the 16-bit append writes what it writes, within
+    the two kernels' evaluation errors."""
+    c = make(torch.float16, 128, 8, 2, 200, (200, 77), None, 0, seed=12)
+    q, k, v, pool, _ = run(c, 64)
+    rq, rk, rv = (torch.empty_like(t, device=DEV) for t in (q, k, v))
+    rpool = c["pool"].to(DEV)
+    qb.rope_qkv(c["qkv"].to(DEV), c["wq"].to(DEV), c["wk"].to(DEV), c["ctx"].to(DEV), rq, Hq=8, Hkv=2, rot=64, theta=1e4,
+                eps=1e-6, k_out=rk, v_out=rv, pool=rpool, page_table=c["pt"].to(DEV))
+    for a, r in ((q, rq), (k, rk), (v, rv), (pool, rpool)):
+        bar = step_of(a.double(), torch.float16) + EVAL
+        assert bool(((a.double() - r.cpu().double()).abs() <= bar).all())
