@@ -10,14 +10,15 @@
 // consecutive cache positions, aligned in the page: the tile lies in one page,
 // its cos/sin table is formed once and shared by all heads, and every block of
 // scales lies in one tile, so one warp owns a block and no atomics are needed.
-// A warp takes one head of up to 16 of the tile's rows at a time, 8 values
-// (16 bytes) per lane, with all of the rows' loads in flight before the first
-// is used.  The D/8 lanes of a row reduce its sum of squares with shuffles;
-// rotDim is a multiple of 16, so a chunk's rotation partner is a whole chunk of
-// another lane of the row, fetched as four 32-bit shuffles of the raw values.
-// For an 8-bit pool a K or V head is passed over twice in registers: the
+// A warp takes one head of up to 16 of the tile's rows at a time, copied by
+// cp.async into its own two-slot ring in shared memory: the next head's rows
+// travel while this one is computed, whatever the registers hold.  A lane
+// works on 8 values (16 bytes); the D/8 lanes of a row reduce its sum of
+// squares with shuffles, and because rotDim is a multiple of 16 a chunk's
+// rotation partner is a whole chunk of the same row, read from shared memory.
+// For an 8-bit pool a K or V head is passed over twice in shared memory: its
 // blocks' largest values first, then the codes.  Blocks of more than 16 tokens
-// read their rows twice (the second time from L1/L2).
+// are copied twice (the second time from L2).
 #include <algorithm>
 
 #include "qsa_internal.h"
@@ -28,7 +29,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 16;  // rows a warp holds in registers
+constexpr int kTile = 16;  // rows of a ring slot
+constexpr int kCtasPerSm = 3;
 
 struct AppendArgs {
   const void* qkv;
@@ -74,51 +76,55 @@ __device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Mean of (f x)^2 over a row; x: this lane's 8 of the row's D values, as pairs.
+// Mean square of a row; x: this lane's 8 of its D values, as pairs.
 template <int D>
-__device__ __forceinline__ float mean_square(const uint64_t (&x)[4], float f) {
-  const uint64_t f2 = pack_f2(f, f);
-  uint64_t acc = 0;
+__device__ __forceinline__ float mean_square(const uint64_t (&x)[4]) {
+  uint64_t acc = fmul2(x[0], x[0]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint64_t v = fmul2(x[k], f2);
-    acc = ffma2(v, v, acc);
-  }
+  for (int k = 1; k < 4; ++k) acc = ffma2(x[k], x[k], acc);
   float ss = lo_f2(acc) + hi_f2(acc);
 #pragma unroll
   for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
   return ss * (1.0f / D);
 }
 
-// What a lane keeps of a head's norm and rotation: its chunk's weights and its partner chunk's.
+// What a lane keeps of a head's norm and rotation: (1 + w) of its chunk, and of its partner chunk with the
+// rotation's sign (- for the first half of a pair).
 struct HeadWeights {
   uint64_t own[4], partner[4];
 };
 
-// The 8 values of a lane's chunk after norm and rotation: with u = x w and the partner chunk's u',
-// y = inv (u cos -+ u' sin); cs: the row's table at this lane's chunk (unused past rotDim).
+// The 8 values of a lane's chunk after norm and rotation: with u = x (1 + w) and the partner chunk's u',
+// y = (u cos -+ u' sin) / sqrt(mean(x^2) + eps).  row: the 16-byte chunks of the head's row in shared memory;
+// cs: the row's table at this lane's chunk, `stride` apart (not read by lanes past rotDim).
 template <int D, bool kBf16>
-__device__ __forceinline__ void norm_rotate(const uint4 raw, float inv, const HeadWeights& w, int partner, int side,
-                                            const ulonglong2* cs, int stride, uint64_t (&y)[4]) {
-  const uint4 other = make_uint4(__shfl_sync(kFull, raw.x, partner), __shfl_sync(kFull, raw.y, partner),
-                                 __shfl_sync(kFull, raw.z, partner), __shfl_sync(kFull, raw.w, partner));
-  const uint64_t inv2 = pack_f2(inv, inv);
-  unpack8<kBf16>(raw, y);
+__device__ __forceinline__ void norm_rotate(const uint4* row, int j, int side, int hl, const HeadWeights& w, float eps,
+                                            const ulonglong2* cs, uint64_t (&y)[4]) {
+  unpack8<kBf16>(row[j], y);
+  float m = mean_square<D>(y) + eps, back = 1.0f;
+  if (kBf16 && __any_sync(kFull, m == INFINITY)) {  // squares past fp32: the same on values scaled by 2^-64
+    uint64_t z[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = fmul2(y[k], pack_f2(0x1p-64f, 0x1p-64f));
+    const float ms = mean_square<D>(z);  // eps is nothing beside squares of 2^128
+    back = m == INFINITY ? 0x1p-64f : 1.0f;
+    m = m == INFINITY ? ms : m;
+  }
+  const float r = rsqrtf(m);
+  const float inv = back * r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
 #pragma unroll
   for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], w.own[k]);
-  if (side) {  // -1: first half of a pair, +1: second half
+  if (side) {
     uint64_t u[4];
-    unpack8<kBf16>(other, u);
-    const float sg = static_cast<float>(side);
-    const uint64_t sg2 = pack_f2(sg, sg);
+    unpack8<kBf16>(row[j - side * hl], u);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const ulonglong2 t = cs[k * stride];  // (cos, cos), (sin, sin) of elements 2k, 2k + 1
-      y[k] = ffma2(fmul2(fmul2(u[k], w.partner[k]), sg2), t.y, fmul2(y[k], t.x));
+      const ulonglong2 t = cs[k * hl];  // (cos, cos), (sin, sin) of elements 2k, 2k + 1
+      y[k] = ffma2(fmul2(u[k], w.partner[k]), t.y, fmul2(y[k], t.x));
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], inv2);
+  for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], pack_f2(inv, inv));
 }
 
 // Largest finite magnitude of 8 values (0 for none).
@@ -159,12 +165,13 @@ __device__ __forceinline__ uint2 rescale8(const uint2 c, float f) {
 }
 
 template <int D, bool kBf16, bool kKv8>
-__global__ void __launch_bounds__(kThreads, 2) append_kv_kernel(const AppendArgs a) {
-  constexpr int LPR = D / 8;              // lanes per row
-  constexpr int RPW = 32 / LPR;           // rows a warp reads with one load instruction
-  constexpr int ITER = kTile / RPW;
-  extern __shared__ __align__(16) ulonglong2 table[];  // [row of the tile][4][rot / 16]: see norm_rotate
-  __shared__ __align__(16) float w1[2][D];             // 1 + w of q and k heads
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const AppendArgs a) {
+  constexpr int LPR = D / 8;              // lanes (16-byte chunks) per row
+  constexpr int RPW = 32 / LPR;           // rows of a warp-wide access
+  constexpr int kSlot = kTile * LPR;      // chunks of a ring slot
+  extern __shared__ __align__(16) uint4 smem[];  // [kWarps][2][kTile][LPR] rows, then the cos/sin table
+  __shared__ __align__(16) float w1[2][D];       // 1 + w of q and k heads
+  ulonglong2* table = reinterpret_cast<ulonglong2*>(smem + kWarps * 2 * kSlot);  // [row of the tile][4][rot / 16]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = lane & (LPR - 1), sub = lane / LPR;
   const int b = blockIdx.x / a.tiles, tileIdx = blockIdx.x - b * a.tiles;
@@ -174,8 +181,48 @@ __global__ void __launch_bounds__(kThreads, 2) append_kv_kernel(const AppendArgs
   const int t0 = tileIdx * a.tile - c % a.tile;   // row at the tile's first position
   if (t0 >= a.S) return;
   const int tlo = max(t0, 0);                     // first row of this CTA
-  const int thi = min(min(a.S, n), t0 + a.tile);  // past its last live row; later rows of the tile are padding
-  const int hl = a.rot >> 4;                      // chunks of half a rotation
+  const int thi = min(min(a.S, n), t0 + a.tile);  // past its last live row; the tile's later rows are padding
+  const int NH = a.Hq + 2 * a.Hkv;
+  const int step = gridDim.y * kWarps;
+
+  // A warp's work: its heads in turn; for a K or V head of an 8-bit pool with blocks above kTile, all of the
+  // tile's chunks of kTile rows for the largest values and once more for the codes; else each chunk once.
+  struct Item {
+    int h, base;  // head, first row of the chunk
+    bool second;
+  };
+  const int c0 = t0 < tlo ? t0 + (tlo - t0) / kTile * kTile : t0;  // first chunk with a row of the CTA
+  const bool twice = kKv8 && a.tile > kTile;
+  auto next_item = [&](Item it) {
+    it.base += kTile;
+    if (it.base >= thi) {
+      it.base = c0;
+      if (twice && it.h >= a.Hq && !it.second) {
+        it.second = true;
+      } else {
+        it.second = false;
+        it.h += step;
+      }
+    }
+    return it;
+  };
+  uint4* ring = smem + warp * 2 * kSlot;
+  const uint4* src = static_cast<const uint4*>(a.qkv) + static_cast<size_t>(b) * a.S * NH * LPR + j;
+  auto copy = [&](const Item& it, int slot) {  // one copy group per item, empty past the last
+    if (it.h < NH) {
+      const uint32_t dst = smem_addr(ring + slot * kSlot + lane);
+#pragma unroll
+      for (int i = 0; i < kTile / RPW; ++i) {
+        const int t = it.base + i * RPW + sub;
+        if (t >= tlo && t < thi) cp_async16(dst + i * 32 * 16, src + (static_cast<size_t>(t) * NH + it.h) * LPR, true);
+      }
+    }
+    cp_async_commit();
+  };
+  Item cur{static_cast<int>(blockIdx.y) * kWarps + warp, c0, false};
+  if (thi > tlo) copy(cur, 0);
+
+  const int hl = a.rot >> 4;  // chunks of half a rotation
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) w1[i / D][i % D] = 1.0f + __ldg((i < D ? a.qw : a.kw) + i % D);
   for (int i = threadIdx.x; i < (thi - tlo) * 8 * hl; i += kThreads) {  // pairs of the live rows
     const int r = i / (8 * hl), pair = i - r * 8 * hl;
@@ -186,107 +233,91 @@ __global__ void __launch_bounds__(kThreads, 2) append_kv_kernel(const AppendArgs
     dst[0] = cv;
     dst[2] = sv;
   }
-  // the tile's pages
-  const int page = (c + tlo) >> 7;  // of live rows; the tile lies in one page
+  // dense output of head h at row t, or null
+  auto dense_at = [&](int h, int t) -> uint4* {
+    const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
+    uint4* d = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
+    if (!d) return nullptr;
+    const int heads = isq ? a.Hq : a.Hkv, hh = isq ? h : (isv ? h - a.Hq - a.Hkv : h - a.Hq);
+    return d + ((static_cast<size_t>(b) * a.S + t) * heads + hh) * LPR + j;
+  };
+  const int tpad = min(a.S, t0 + a.tile);
+  if (max(thi, tlo) < tpad)  // padding rows: zeros in the dense outputs
+    for (int h = blockIdx.y * kWarps + warp; h < NH; h += step)
+      for (int t = max(thi, tlo) + sub; t < tpad; t += RPW)
+        if (uint4* d = dense_at(h, t)) *d = make_uint4(0, 0, 0, 0);
+  if (thi <= tlo) return;
+
+  // the tile's pages: it lies in one page of K and one of V
+  const int page = (c + tlo) >> 7;
   int pg[2] = {-1, -1};
-  if (thi > tlo) {
-    if (page < a.maxPagesPerSeq) {
-      const int32_t* pt = a.pageTable + static_cast<size_t>(b) * 2 * a.maxPagesPerSeq + page;
-      pg[0] = __ldg(pt);
-      pg[1] = __ldg(pt + a.maxPagesPerSeq);
-    }
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (static_cast<unsigned>(pg[i]) >= static_cast<unsigned>(a.numFlatPages)) {
-        pg[i] = -1;
-        bad = true;
-      }
-    if (bad && threadIdx.x == 0 && a.status) atomicOr(a.status, kErrBadPage);
+  if (page < a.maxPagesPerSeq) {
+    const int32_t* pt = a.pageTable + static_cast<size_t>(b) * 2 * a.maxPagesPerSeq + page;
+    pg[0] = __ldg(pt);
+    pg[1] = __ldg(pt + a.maxPagesPerSeq);
   }
+  bool badPage = false;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (static_cast<unsigned>(pg[i]) >= static_cast<unsigned>(a.numFlatPages)) {
+      pg[i] = -1;
+      badPage = true;
+    }
+  if (badPage && threadIdx.x == 0 && a.status) atomicOr(a.status, kErrBadPage);
   __syncthreads();
 
-  const int NH = a.Hq + 2 * a.Hkv;
   const int side = j < hl ? -1 : (j < 2 * hl ? 1 : 0);
-  const int partner = lane - side * hl;
-  const uint4* src = static_cast<const uint4*>(a.qkv) + static_cast<size_t>(b) * a.S * NH * LPR + j;
-  for (int h = blockIdx.y * kWarps + warp; h < NH; h += gridDim.y * kWarps) {
+  HeadWeights w;
+  int have = -1;        // whose weights w holds: 0 q heads, 1 k heads
+  float bm = 0.f;       // lanes 0..15, 8-bit: largest value of row `lane` (of the whole block, for blocks above 16)
+  float rowInv = 0.f;   // lanes 0..15, 8-bit: 1 / scale of row `lane`
+  for (int slot = 0; cur.h < NH; slot ^= 1) {
+    const Item nxt = next_item(cur);
+    copy(nxt, slot ^ 1);
+    cp_async_wait<1>();
+    __syncwarp();
+    const int h = cur.h, base = cur.base;
     const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
     const int hk = isq ? 0 : (isv ? h - a.Hq - a.Hkv : h - a.Hq);
-    HeadWeights w;
-    if (!isv) {
-      const int jp = j - side * hl;
+    const int pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
+    const uint4* rows = ring + slot * kSlot;
+    if (!isv && have != (isq ? 0 : 1)) {
+      have = isq ? 0 : 1;
+      const uint64_t flip = side < 0 ? 0x8000000080000000ull : 0ull;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        w.own[k] = *reinterpret_cast<const uint64_t*>(&w1[isq ? 0 : 1][8 * j + 2 * k]);
-        w.partner[k] = *reinterpret_cast<const uint64_t*>(&w1[isq ? 0 : 1][8 * jp + 2 * k]);
+        w.own[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * j + 2 * k]);
+        w.partner[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * (j - side * hl) + 2 * k]) ^ flip;
       }
     }
-    // dense output of this head: row t at dense + t * denseStride (16-byte chunks)
-    uint4* dense = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
-    const size_t denseStride = static_cast<size_t>(isq ? a.Hq : a.Hkv) * LPR;
-    if (dense) dense += static_cast<size_t>(b) * a.S * denseStride + static_cast<size_t>(isq ? h : hk) * LPR + j;
-    const int pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
-
-    uint4 raw[ITER];
-    float inv[ITER];
-    // Loads the rows base .. base + 15 and forms the norm's factors.
-    auto load = [&](int base) {
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int t = base + i * RPW + sub;
-        raw[i] = t >= tlo && t < thi ? __ldg(src + (static_cast<size_t>(t) * NH + h) * LPR) : make_uint4(0, 0, 0, 0);
-      }
-      if (isv) return;
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        uint64_t x[4];
-        unpack8<kBf16>(raw[i], x);
-        float m = mean_square<D>(x, 1.0f) + a.eps, back = 1.0f;
-        if (kBf16 && __any_sync(kFull, m == INFINITY)) {  // squares past fp32: the same on values scaled by 2^-64
-          const float ms = mean_square<D>(x, 0x1p-64f) + a.eps * 0x1p-128f;
-          back = m == INFINITY ? 0x1p-64f : 1.0f;
-          m = m == INFINITY ? ms : m;
-        }
-        const float r = rsqrtf(m);
-        inv[i] = back * r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
-      }
-    };
-    auto value = [&](int base, int i, uint64_t (&y)[4]) {
+    auto value = [&](int rr, uint64_t (&y)[4]) {  // rr: row of the chunk
       if (isv)
-        unpack8<kBf16>(raw[i], y);
+        unpack8<kBf16>(rows[rr * LPR + j], y);
       else
-        norm_rotate<D, kBf16>(raw[i], inv[i], w, partner, side,
-                              table + static_cast<size_t>(base - t0 + i * RPW + sub) * 4 * hl + (side > 0 ? j - hl : j),
-                              hl, y);
+        norm_rotate<D, kBf16>(rows + rr * LPR, j, side, hl, w, a.eps,
+                              table + (base - t0 + rr) * 4 * hl + (side > 0 ? j - hl : j), y);
     };
+    const int i0 = max(tlo - base, 0) / RPW, i1 = (min(thi - base, kTile) + RPW - 1) / RPW;  // accesses with live rows
 
-    float rowInv = 0.f;  // 8-bit K/V heads, lanes 0..15: 1 / scale of row `lane`
-    if constexpr (kKv8) {
-      if (!isq && thi > tlo) {
-        const int sb = 1 << a.blockShift, seg = min(sb, kTile);
-        float bm = 0.f;
-        for (int base = t0; base < t0 + a.tile; base += kTile) {
-          if (base + kTile <= tlo || base >= thi) continue;
-          load(base);
-          float rm = 0.f;  // of row `lane`
+    if (kKv8 && !isq && !cur.second) {  // the largest value of each row, then of each block
+      float rm = 0.f;
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) {
+        uint64_t y[4];
+        value(i * RPW + sub, y);
+        const int t = base + i * RPW + sub;
+        float m = t >= tlo && t < thi ? finite_max(y) : 0.f;
 #pragma unroll
-          for (int i = 0; i < ITER; ++i) {
-            uint64_t y[4];
-            value(base, i, y);
-            const int t = base + i * RPW + sub;
-            float m = t >= tlo && t < thi ? finite_max(y) : 0.f;
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            m = __shfl_sync(kFull, m, (lane % RPW) * LPR);
-            if (lane / RPW == i) rm = m;
-          }
-          for (int o = 1; o < seg; o <<= 1) rm = fmaxf(rm, __shfl_xor_sync(kFull, rm, o));
-          bm = fmaxf(bm, rm);
-        }
-        // the scale of this lane's block (lanes 0..15; the upper half only follows)
+        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        m = __shfl_sync(kFull, m, (lane % RPW) * LPR);
+        if (lane / RPW == i) rm = m;
+      }
+      const int sb = 1 << a.blockShift;
+      for (int o = 1; o < min(sb, kTile); o <<= 1) rm = fmaxf(rm, __shfl_xor_sync(kFull, rm, o));
+      bm = base == c0 ? rm : fmaxf(bm, rm);
+      if (base + kTile >= thi) {  // every row is in: the scale of this lane's block
         const int rr = lane & (kTile - 1);
-        const int tb = t0 + (sb > kTile ? 0 : rr & ~(sb - 1));  // row at the block's first position
+        const int tb = t0 + (twice ? 0 : rr & ~(sb - 1));  // row at the block's first position
         const bool fill = max(tb, tlo) < min(tb + sb, thi) && pageId >= 0;
         float* sp = a.scale +
                     ((static_cast<size_t>(fill ? pageId : 0) << (7 - a.blockShift)) +
@@ -308,58 +339,61 @@ __global__ void __launch_bounds__(kThreads, 2) append_kv_kernel(const AppendArgs
           }
         }
         __syncwarp();  // every lane of a block has read its scale
-        if (fill && (sb > kTile ? lane == 0 : lane < kTile && (rr & (sb - 1)) == 0)) *sp = now;
+        if (fill && (twice ? lane == 0 : lane < kTile && (rr & (sb - 1)) == 0)) *sp = now;
         rowInv = 1.0f / now;
         // older rows of the grown block (at most one block of the tile holds older tokens)
-        const float f = __shfl_sync(kFull, shrink, sb > kTile || t0 >= 0 ? 0 : (-t0) & ~(sb - 1));
-        if (t0 < 0 && f != 1.f && pageId >= 0) {
-          const int first = c & ~(sb - 1);
-          for (int p = first + sub; p < c; p += RPW) {
+        const float f = __shfl_sync(kFull, shrink, twice || t0 >= 0 ? 0 : (-t0) & ~(sb - 1));
+        if (t0 < 0 && f != 1.f && pageId >= 0)
+          for (int p = (c & ~(sb - 1)) + sub; p < c; p += RPW) {
             uint2* row = reinterpret_cast<uint2*>(
                              a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + (p & 127)) * a.Hkv + hk) *
                                           a.poolHeadDim) + j;
             *row = rescale8(*row, f);
           }
-        }
       }
     }
 
-    const bool held = kKv8 && !isq && a.tile == kTile;  // the amax pass left the rows in registers
-    for (int base = t0; base < t0 + a.tile; base += kTile) {
-      if (base + kTile <= tlo || base >= a.S) continue;
-      const bool any = base < thi;
-      if (any && !held) load(base);
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
+    if (!kKv8 || isq || !twice || cur.second) {
+      uint4* dense = dense_at(h, base + sub);
+      const size_t denseStep = static_cast<size_t>(isq ? a.Hq : a.Hkv) * LPR * RPW;
+      uint8_t* prow = nullptr;
+      const size_t poolStep = static_cast<size_t>(a.Hkv) * a.poolHeadDim * (kKv8 ? 1 : 2) * RPW;
+      if (pageId >= 0)
+        prow = a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + ((c + base + sub) & 127)) * a.Hkv + hk) *
+                            a.poolHeadDim * (kKv8 ? 1 : 2);
+#pragma unroll 2
+      for (int i = i0; i < i1; ++i) {
         const int rr = i * RPW + sub, t = base + rr;
         const bool live = t >= tlo && t < thi;
-        uint64_t y[4] = {0, 0, 0, 0};
-        if (any) value(base, i, y);
-        if (dense && t >= tlo && t < a.S && t < t0 + a.tile) {
-          uint4 out = make_uint4(0, 0, 0, 0);
-          if (live) out = isv ? raw[i] : pack8<kBf16>(y);
-          dense[static_cast<size_t>(t) * denseStride] = out;
-        }
-        if (isq) continue;
-        const float qs = kKv8 ? __shfl_sync(kFull, rowInv, rr) : 0.f;
-        if (live && pageId >= 0) {
-          const size_t row = (static_cast<size_t>(pageId) * kTokensPerPage + ((c + t) & 127)) * a.Hkv + hk;
+        uint64_t y[4];
+        value(rr, y);
+        const float qs = kKv8 && !isq ? __shfl_sync(kFull, rowInv, rr) : 0.f;
+        if (!live) continue;
+        const bool whole = dense || (!kKv8 && prow);
+        uint4 out;
+        if (whole) out = isv ? rows[rr * LPR + j] : pack8<kBf16>(y);
+        if (dense) dense[i * denseStep] = out;
+        if (prow) {
           if constexpr (kKv8)
-            *(reinterpret_cast<uint2*>(a.pool + row * a.poolHeadDim) + j) = quantise8(y, qs);
+            reinterpret_cast<uint2*>(prow + i * poolStep)[j] = quantise8(y, qs);
           else
-            *(reinterpret_cast<uint4*>(a.pool + row * a.poolHeadDim * 2) + j) = isv ? raw[i] : pack8<kBf16>(y);
+            reinterpret_cast<uint4*>(prow + i * poolStep)[j] = out;
         }
       }
     }
+    __syncwarp();  // every lane is done with the slot
+    cur = nxt;
   }
+  cp_async_wait<0>();  // the last groups are empty; nothing is in flight at exit
 }
 
 template <int D, bool kBf16, bool kKv8>
 cudaError_t append_go(const AppendArgs& a, int B, cudaStream_t st) {
   auto kernel = append_kv_kernel<D, kBf16, kKv8>;
-  const size_t smem = static_cast<size_t>(a.tile) * (a.rot / 2) * 8;  // at most 128 x 64 pairs: 64 KB
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokensPerPage * (D / 2) * 8);
+  // the warps' rings and the table: 32 or 64 KB, and 8 bytes per row and rotated pair (at most 64 KB)
+  const size_t smem = kWarps * 2 * kTile * (D * 2) + static_cast<size_t>(a.tile) * (a.rot / 2) * 8;
+  const cudaError_t attr =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (attr != cudaSuccess) return attr;
   // One CTA per tile when the tiles fill the GPU a few times over; otherwise the heads of a tile are dealt
   // out to several CTAs, down to one head per warp.
