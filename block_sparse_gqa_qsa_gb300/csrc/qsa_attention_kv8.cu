@@ -13,11 +13,13 @@
 //
 // One CTA of 4 warps takes a (row, KV head) pair; when there are few pairs a
 // cluster of up to 8 CTAs shares one.  The list is dealt out to the warps of
-// the pair in steps of 32 entries, and each warp runs by itself: lane i
-// resolves entry i of its step (list entry two steps ahead, page ids one step
-// ahead, so each dependent load has a step to arrive), then the warp gathers
-// the 32 K and V rows of 128 bytes with cp.async into its own two-slot ring
-// and computes on the step before: no CTA barrier inside the loop.
+// the pair in steps of 32 entries, and each warp runs by itself, with no CTA
+// barrier inside the loop: lane i resolves entry i of a step (list entry three
+// steps ahead, page ids two, scales one, so that each dependent load has a
+// step to arrive), and the warp gathers the 32 K and V rows of 128 bytes with
+// cp.async into its own K tile and V tile.  A step's K tile is free after its
+// first product, its V tile after the second, and the next step's rows start
+// then: one tile of each keeps half a step of copies in flight per warp.
 // S^T = C^K Q^T and O^T += (C^V)^T P^T are m16n8k16 MMAs with the head group as
 // N.  The summed dims of the first and the output dims of the second may be
 // permuted freely, so a lane reads its codes as whole 16-byte chunks and
@@ -35,10 +37,8 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kD = 128;
 constexpr int kStep = 32;                      // list entries of a warp's step
-constexpr int kSlotBytes = kStep * kD * 2;     // K and V rows of a step
-constexpr int kStages = 2;
-constexpr int kRingBytes = kStages * kSlotBytes;
-constexpr int kSmem = kWarps * kRingBytes;
+constexpr int kTileBytes = kStep * kD;         // K (or V) rows of a step
+constexpr int kWarpBytes = 2 * kTileBytes;     // one K tile, one V tile
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -93,7 +93,11 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
 // Byte offset of 16-byte chunk c of key row r in a step's K tile (a lane group reads chunks 0..3 or 4..7 of
 // two neighbouring rows) and V tile (chunks 0, 1 of rows 0, 2, 4, 6): each access covers all banks once.
 __device__ __forceinline__ uint32_t k_off(int r, int c) { return r * kD + ((c ^ ((r & 1) << 2)) << 4); }
-__device__ __forceinline__ uint32_t v_off(int r, int c) { return kStep * kD + r * kD + ((c ^ (r & 6)) << 4); }
+__device__ __forceinline__ uint32_t v_off(int r, int c) { return r * kD + ((c ^ (r & 6)) << 4); }
+
+__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
@@ -118,19 +122,18 @@ struct Entry {
   float iv;  // 1 / V scale; 0 for an entry that names nothing
 };
 
-template <int NT, bool kBf16>
-__device__ __forceinline__ void attend32(Acc<NT>& A, uint32_t slot, const uint32_t (&qf)[NT][8][2],
-                                         const float (&qs)[NT][2], const Entry& en) {
+// S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + g and + 8, heads 8 nt + 2 q and + 1.
+template <int NT>
+__device__ __forceinline__ void scores32(float (&s)[2][NT][4], uint32_t tile, const uint32_t (&qf)[NT][8][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  float s[2][NT][4];
 #pragma unroll
   for (int gk = 0; gk < 2; ++gk) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s[gk][nt][0] = s[gk][nt][1] = s[gk][nt][2] = s[gk][nt][3] = 0.f;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint4 r0 = lds16(slot + k_off(16 * gk + g, q + 4 * half));
-      const uint4 r1 = lds16(slot + k_off(16 * gk + g + 8, q + 4 * half));
+      const uint4 r0 = lds16(tile + k_off(16 * gk + g, q + 4 * half));
+      const uint4 r1 = lds16(tile + k_off(16 * gk + g + 8, q + 4 * half));
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a[4];
@@ -141,6 +144,17 @@ __device__ __forceinline__ void attend32(Acc<NT>& A, uint32_t slot, const uint32
       }
     }
   }
+}
+
+// Online softmax of a step: s becomes the weights relative to the running maximum, returned in fp16 as the B
+// fragments of the second product.  The maximum moves only when a weight would pass 2^kHeadroom (the weights
+// are relative numbers: nothing is lost by their being up to 256 instead of 1), so that O is hardly ever
+// rescaled after a warp's first step.
+template <int NT, bool kBf16>
+__device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], const float (&qs)[NT][2], const Entry& en,
+                                          uint32_t (&pb)[2][NT][2]) {
+  constexpr float kHeadroom = 8.f;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
   float ks[4], lv[4], iv[4];  // of keys g, g + 8, g + 16, g + 24
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -148,7 +162,8 @@ __device__ __forceinline__ void attend32(Acc<NT>& A, uint32_t slot, const uint32
     lv[i] = __shfl_sync(kFull, en.lv, g + 8 * i);
     iv[i] = __shfl_sync(kFull, en.iv, g + 8 * i);
   }
-  uint32_t pb[2][NT][2];
+  float mx[NT][2];
+  bool move = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -159,43 +174,63 @@ __device__ __forceinline__ void attend32(Acc<NT>& A, uint32_t slot, const uint32
         if constexpr (kBf16) x *= qs[nt][h];
         x = fmaf(x, ks[i], lv[i]);
       }
-    float al[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float mx = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+      mx[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-      const float mn = fmaxf(A.m[nt][h], mx);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      al[h] = ex2_ftz(A.m[nt][h] - mu);
-      A.m[nt][h] = mn;
-      float l = A.l[nt][h] * al[h];
+      for (int o = 4; o < 32; o <<= 1) mx[nt][h] = fmaxf(mx[nt][h], __shfl_xor_sync(kFull, mx[nt][h], o));
+      move |= mx[nt][h] > A.m[nt][h] + kHeadroom;
+    }
+  }
+  if (__any_sync(kFull, move)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float al[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float mn = fmaxf(A.m[nt][h], mx[nt][h]);
+        al[h] = ex2_ftz(A.m[nt][h] - (mn == -INFINITY ? 0.f : mn));
+        A.m[nt][h] = mn;
+        A.l[nt][h] *= al[h];
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        A.o[mt][nt][0] *= al[0];
+        A.o[mt][nt][1] *= al[1];
+        A.o[mt][nt][2] *= al[0];
+        A.o[mt][nt][3] *= al[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float mu = A.m[nt][h] == -INFINITY ? 0.f : A.m[nt][h];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float& x = s[i >> 1][nt][2 * (i & 1) + h];
         x = ex2_ftz(x - mu);
-        l = fmaf(x, iv[i], l);
+        A.l[nt][h] = fmaf(x, iv[i], A.l[nt][h]);
       }
-      A.l[nt][h] = l;
     }
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      A.o[mt][nt][0] *= al[0];
-      A.o[mt][nt][1] *= al[1];
-      A.o[mt][nt][2] *= al[0];
-      A.o[mt][nt][3] *= al[1];
-    }
-    // P in fp16: at most 1, off by 2^-11 of itself, which the output's own rounding hides
+    // the weights in fp16: off by 2^-11 of themselves, which the output's own rounding hides
 #pragma unroll
     for (int gk = 0; gk < 2; ++gk) {
       pb[gk][nt][0] = movmatrix_t(pack_half2(s[gk][nt][0], s[gk][nt][1]));
       pb[gk][nt][1] = movmatrix_t(pack_half2(s[gk][nt][2], s[gk][nt][3]));
     }
   }
+}
+
+// O^T += (C^V)^T P^T.
+template <int NT>
+__device__ __forceinline__ void values32(Acc<NT>& A, uint32_t tile, const uint32_t (&pb)[2][NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int gk = 0; gk < 2; ++gk) {
-    const uint4 va = lds16(slot + v_off(16 * gk + 2 * q, g)), vb = lds16(slot + v_off(16 * gk + 2 * q + 1, g));
-    const uint4 vc = lds16(slot + v_off(16 * gk + 2 * q + 8, g)), vd = lds16(slot + v_off(16 * gk + 2 * q + 9, g));
+    const uint4 va = lds16(tile + v_off(16 * gk + 2 * q, g)), vb = lds16(tile + v_off(16 * gk + 2 * q + 1, g));
+    const uint4 vc = lds16(tile + v_off(16 * gk + 2 * q + 8, g)), vd = lds16(tile + v_off(16 * gk + 2 * q + 9, g));
 #pragma unroll
     for (int w = 0; w < 4; ++w)
 #pragma unroll
@@ -254,8 +289,16 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
   }
 }
 
+// Resident CTAs per SM: the register budget (128 or 168 a thread) decides.
+template <int NT>
+constexpr int kCtasPerSm = NT == 1 ? 4 : 3;
+// The tiles, and later the merge buffers: the warps' O, m and l, then the CTA's.
+template <int NT>
+constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kD + 2) * 4 ? kWarps * kWarpBytes
+                                                                               : (kWarps + 1) * 8 * NT * (kD + 2) * 4;
+
 template <int NT, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 3) sparse_paged_kv8_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_kernel(const PagedArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x % a.split);
@@ -278,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_paged_kv8_kernel(const Pag
   const int32_t* ptV = ptK + a.maxPagesPerSeq;
   const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
   const int first = kStep * (rank * kWarps + warp) + lane;
-  const uint32_t ring = smem_addr(smem) + warp * kRingBytes;
-  const size_t rowBytes = static_cast<size_t>(a.Hkv) * a.poolHeadDim;
+  const uint32_t ktile = smem_addr(smem) + warp * kWarpBytes, vtile = ktile + kTileBytes;
+  const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
   const uint8_t* base = a.pool + static_cast<size_t>(kvh) * a.poolHeadDim + (lane & 7) * 16;
 
   int bad = 0;
@@ -298,37 +341,44 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_paged_kv8_kernel(const Pag
     }
     return p;
   };
-  // Gathers a step's rows into ring slot `stage` (one copy group, empty if the step names nothing).
-  auto gather = [&](const Pages& p, int stage, Entry& en) -> bool {
+  struct Rows {
+    int k, v;       // pool rows of lane's entry; -1: none
+    float ks, vs;   // their scales as stored
+    unsigned mask;  // lanes whose entry names a row
+  };
+  auto resolve = [&](const Pages& p) {
+    Rows r{-1, -1, 0.f, 0.f, 0u};
     const bool ok = p.j >= 0 && static_cast<unsigned>(p.k) < static_cast<unsigned>(a.numFlatPages) &&
                     static_cast<unsigned>(p.v) < static_cast<unsigned>(a.numFlatPages);
     if (p.j >= 0 && !ok) bad |= kErrBadPage;
-    const bool any = __any_sync(kFull, ok);
-    en = Entry{0.f, -INFINITY, 0.f};
-    if (any) {
-      const int in = p.j & 127;
-      const int krow = ok ? p.k * kTokensPerPage + in : -1, vrow = ok ? p.v * kTokensPerPage + in : -1;
-      float ks = 0.f, vs = 0.f;
-      if (ok) {
-        ks = __ldg(a.scale + static_cast<size_t>(krow >> a.blockShift) * a.Hkv + kvh);
-        vs = __ldg(a.scale + static_cast<size_t>(vrow >> a.blockShift) * a.Hkv + kvh);
-      }
-      const uint32_t dst = ring + stage * kSlotBytes;
+    if (ok) {
+      r.k = p.k * kTokensPerPage + (p.j & 127);
+      r.v = p.v * kTokensPerPage + (p.j & 127);
+      r.ks = __ldg(a.scale + static_cast<size_t>(r.k >> a.blockShift) * a.Hkv + kvh);
+      r.vs = __ldg(a.scale + static_cast<size_t>(r.v >> a.blockShift) * a.Hkv + kvh);
+    }
+    r.mask = __ballot_sync(kFull, ok);
+    return r;
+  };
+  // Gathers the 32 rows that the lanes hold into a tile, 8 lanes to a row of 128 bytes: one copy group.
+  auto gather = [&](int row, unsigned mask, auto dst) {
+    if (mask == kFull) {
 #pragma unroll
-      for (int i = 0; i < kStep / 4; ++i) {  // 8 lanes copy one 128-byte row
-        const int r = 4 * i + (lane >> 3), c = lane & 7;
-        const int kr = __shfl_sync(kFull, krow, r), vr = __shfl_sync(kFull, vrow, r);
-        cp_async16(dst + k_off(r, c), base + static_cast<size_t>(max(kr, 0)) * rowBytes, kr >= 0);
-        cp_async16(dst + v_off(r, c), base + static_cast<size_t>(max(vr, 0)) * rowBytes, vr >= 0);
-      }
-      if (ok) {
-        vs = read_scale(vs);
-        en = Entry{read_scale(ks) * a.sl2, __log2f(vs), 1.0f / vs};
+      for (int i = 0; i < kStep / 4; ++i)
+        cp_async16_all(dst(i), base + static_cast<uint64_t>(static_cast<uint32_t>(
+                                          __shfl_sync(kFull, row, 4 * i + (lane >> 3)))) * rowBytes);
+    } else if (mask) {  // rows that are not named are zeros
+#pragma unroll
+      for (int i = 0; i < kStep / 4; ++i) {
+        const int r = __shfl_sync(kFull, row, 4 * i + (lane >> 3));
+        cp_async16(dst(i), base + static_cast<uint64_t>(static_cast<uint32_t>(max(r, 0))) * rowBytes, r >= 0);
       }
     }
     cp_async_commit();
-    return any;
   };
+  const uint32_t kdst = ktile + k_off(lane >> 3, lane & 7), vdst = vtile + v_off(lane >> 3, lane & 7);
+  auto gather_k = [&](const Rows& r) { gather(r.k, r.mask, [&](int i) { return kdst + i * 4 * kD; }); };
+  auto gather_v = [&](const Rows& r) { gather(r.v, r.mask, [&](int i) { return (vdst ^ ((i & 1) << 6)) + i * 4 * kD; }); };
 
   Acc<NT> A;
 #pragma unroll
@@ -339,25 +389,37 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_paged_kv8_kernel(const Pag
     A.l[nt][0] = A.l[nt][1] = 0.f;
   }
   const int steps = max(0, (a.topK - (first - lane) + hop - 1) / hop);
-  int j2 = list_at(first + hop);
-  Pages p1 = pages_of(list_at(first));
+  Rows cur = resolve(pages_of(list_at(first)));
+  gather_k(cur);
+  gather_v(cur);
+  Pages p1 = pages_of(list_at(first + hop));
+  int j2 = list_at(first + 2 * hop);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
   load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + head0 * (kD / 8), a.G, qf, qs);
-  Entry now, next;
-  bool anyNow = gather(p1, 0, now), anyNext = false;
-  p1 = pages_of(j2);
-  j2 = list_at(first + 2 * hop);
   for (int i = 0; i < steps; ++i) {
-    __syncwarp();  // every lane is done with the slot of step i - 1
-    anyNext = gather(p1, (i + 1) & 1, next);
+    const Rows next = resolve(p1);
     p1 = pages_of(j2);
-    j2 = i + 3 < steps ? list_at(first + (i + 3) * hop) : -1;
-    cp_async_wait<1>();
+    j2 = list_at(first + (i + 3) * hop);
+    float s[2][NT][4];
+    uint32_t pb[2][NT][2];
+    cp_async_wait<1>();  // this lane's share of the K tile; the V tile may be in flight
     __syncwarp();
-    if (anyNow) attend32<NT, kBf16>(A, ring + (i & 1) * kSlotBytes, qf, qs, now);
-    now = next;
-    anyNow = anyNext;
+    if (cur.mask) scores32<NT>(s, ktile, qf);
+    __syncwarp();  // every lane is done with the K tile
+    gather_k(next);
+    if (cur.mask) {
+      const bool ok = cur.k >= 0;
+      const float vs = read_scale(cur.vs);
+      const Entry en{ok ? read_scale(cur.ks) * a.sl2 : 0.f, ok ? __log2f(vs) : -INFINITY, ok ? 1.0f / vs : 0.f};
+      softmax32<NT, kBf16>(A, s, qs, en, pb);
+    }
+    cp_async_wait<1>();  // the V tile; the next K tile may be in flight
+    __syncwarp();
+    if (cur.mask) values32<NT>(A, vtile, pb);
+    __syncwarp();
+    gather_v(next);
+    cur = next;
   }
   cp_async_wait<0>();
   bad = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
@@ -451,17 +513,17 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_paged_kv8_kernel(const Pag
 template <int NT, bool kBf16>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   auto kernel = sparse_paged_kv8_kernel<NT, kBf16>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<NT>);
   if (e != cudaSuccess) return e;
-  // As many CTAs per pair as stay resident at once (three per SM), at most one per 128 entries of the list.
-  const long long slots = 3LL * sm_count();
+  // As many CTAs per pair as stay resident at once, at most one per 128 entries of the list.
+  const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();
   const int most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
   a.split = static_cast<int>(std::max<long long>(1, std::min<long long>(most, slots / pairs)));
   if (pairs * a.split > 0x7fffffffLL) a.split = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.split));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = kSmem<NT>;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
