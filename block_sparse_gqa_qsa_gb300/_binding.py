@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -426,31 +427,64 @@ def sparse_decode_noalloc(q, pool, page_table, indices, ctx, out, *, D, scale, s
 
 
 # -------------------------------------------------------------- paged cache
-def _same_device(name: str, tensors) -> None:
-    """Every tensor on the current device: the kernels run there, on its current stream."""
-    cur = torch.cuda.current_device()
+# A decode step calls these once per layer, and its kernels take a few microseconds, so the host side is kept
+# short: one check per tensor, the params packed in one go (same layout as the ctypes structs above).
+_APPEND_PACK = struct.Struct("@12P10i2fP")
+_PAGED_PACK = struct.Struct("@8P10ifPP")
+_packed_calls = {}
+
+
+def _packed(name: str):
+    """The entry point as a function of packed params bytes."""
+    f = _packed_calls.get(name)
+    if f is None:
+        f = lib()._FuncPtr((name, lib()))
+        f.argtypes = [_vp]
+        f.restype = ctypes.c_int
+        _packed_calls[name] = f
+    return f
+
+
+def _arg(t: torch.Tensor | None, dtype, name: str, device: int) -> int:
+    """The address of a contiguous tensor of `dtype` on the current device (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _ptr(t, dtype, name)
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
+def _current_device(*tensors) -> int:
+    """The current CUDA device; refuses CPU tensors before anything touches CUDA."""
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"{name}: a tensor is on {t.device}, the current device is cuda:{cur}")
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+    return torch.cuda.current_device()
 
 
 def _append(name, qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
             v_out, status, stream):
     et = qkv.dtype
-    if et not in (torch.float16, torch.bfloat16):
+    bf16 = et is torch.bfloat16
+    if not bf16 and et is not torch.float16:
         raise ValueError(f"{name}: qkv must be float16 or bfloat16")
     if qkv.dim() != 4 or pool.dim() != 4 or page_table.dim() != 3:
         raise ValueError(f"{name}: qkv and pool have 4 dimensions, page_table 3")
     B, S, NH, D = qkv.shape
     nflat, tpp, ph, phd = pool.shape
-    if NH != Hq + 2 * Hkv or tuple(q_out.shape) != (B, S, Hq, D) or tuple(wq.shape) != (D,) or \
-            tuple(wk.shape) != (D,) or tuple(ctx.shape) != (B,) or tpp != 128 or ph != Hkv or \
-            tuple(page_table.shape[:2]) != (B, 2):
+    ptb, two, pages = page_table.shape
+    if NH != Hq + 2 * Hkv or q_out.shape != (B, S, Hq, D) or wq.shape != (D,) or wk.shape != (D,) or \
+            ctx.shape != (B,) or tpp != 128 or ph != Hkv or ptb != B or two != 2:
         raise ValueError(f"{name}: shape mismatch")
     for t in (k_out, v_out):
-        if t is not None and tuple(t.shape) != (B, S, Hkv, D):
+        if t is not None and t.shape != (B, S, Hkv, D):
             raise ValueError(f"{name}: k_out/v_out shape mismatch")
-    if new_lengths is not None and tuple(new_lengths.shape) != (B,):
+    if new_lengths is not None and new_lengths.shape != (B,):
         raise ValueError(f"{name}: new_lengths must have shape ({B},)")
     block = 0
     if scale is not None:
@@ -458,18 +492,22 @@ def _append(name, qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot
                 128 % scale.shape[1]:
             raise ValueError(f"{name}: scale must be [{nflat}, 128 / block, {Hkv}]")
         block = 128 // scale.shape[1]
-    p = QsaAppendKvParams(
-        qkv=_ptr(qkv, et, "qkv"), qNormW=_ptr(wq, torch.float32, "qNormW"), kNormW=_ptr(wk, torch.float32, "kNormW"),
-        contextLengths=_ptr(ctx, torch.int32, "contextLengths"),
-        newLengths=_ptr(new_lengths, torch.int32, "new_lengths"), qOut=_ptr(q_out, et, "q_out"),
-        kOut=_ptr(k_out, et, "k_out"), vOut=_ptr(v_out, et, "v_out"),
-        kvPool=_ptr(pool, et if scale is None else torch.float8_e4m3fn, "pool"),
-        kvScale=_ptr(scale, torch.float32, "scale"), pageTable=_ptr(page_table, torch.int32, "pageTable"),
-        status=_ptr(status, torch.int32, "status"), batchSize=B, seqLen=S, numQHeads=Hq, numKVHeads=Hkv, headDim=D,
-        rotDim=rot, poolHeadDim=phd, numFlatPages=nflat, maxPagesPerSeq=page_table.shape[-1], scaleBlock=block,
-        ropeTheta=theta, rmsNormEps=eps, stream=_stream(stream))
-    _same_device(name, (qkv, wq, wk, ctx, new_lengths, q_out, k_out, v_out, pool, scale, page_table, status))
-    _check(getattr(lib(), "qsa_" + name + ("_bf16" if et == torch.bfloat16 else ""))(ctypes.byref(p)))
+    dev = _current_device(qkv)
+    f32, i32 = torch.float32, torch.int32
+    packed = _APPEND_PACK.pack(
+        _arg(qkv, et, "qkv", dev), _arg(wq, f32, "qNormW", dev), _arg(wk, f32, "kNormW", dev),
+        _arg(ctx, i32, "contextLengths", dev), _arg(new_lengths, i32, "new_lengths", dev),
+        _arg(q_out, et, "q_out", dev), _arg(k_out, et, "k_out", dev), _arg(v_out, et, "v_out", dev),
+        _arg(pool, et if scale is None else torch.float8_e4m3fn, "pool", dev), _arg(scale, f32, "scale", dev),
+        _arg(page_table, i32, "pageTable", dev), _arg(status, i32, "status", dev), B, S, Hq, Hkv, D, rot, phd, nflat,
+        pages, block, theta, eps, _raw_stream(stream, dev))
+    r = _packed(_APPEND_NAMES[name, bf16])(packed)
+    if r:
+        _check(r)
+
+
+_APPEND_NAMES = {(n, b): "qsa_" + n + ("_bf16" if b else "") for n in ("append_kv", "append_kv8")
+                 for b in (False, True)}
 
 
 def append_kv(qkv, wq, wk, ctx, q_out, pool, page_table, *, Hq, Hkv, rot, theta, eps, new_lengths=None, k_out=None,
@@ -498,25 +536,28 @@ def sparse_paged_kv8(q, pool, kv_scale, page_table, indices, ctx, out, *, scale,
     [numFlat,128,Hkv,poolHeadDim], kv_scale float32 [numFlat,128/block,Hkv], indices int32 [B,S,topK], ctx int32 [B]
     total lengths, new_lengths int32 [B] query rows (None: min(S, ctx)); scale multiplies q . k."""
     et = q.dtype
-    if et not in (torch.float16, torch.bfloat16):
+    bf16 = et is torch.bfloat16
+    if not bf16 and et is not torch.float16:
         raise ValueError("sparse_paged_kv8: q must be float16 or bfloat16")
     if q.dim() != 4 or pool.dim() != 4 or kv_scale.dim() != 3 or page_table.dim() != 3 or indices.dim() != 3:
         raise ValueError("sparse_paged_kv8: q and pool have 4 dimensions, kv_scale, page_table and indices 3")
     B, S, Hq, D = q.shape
     nflat, tpp, Hkv, phd = pool.shape
-    nblk = kv_scale.shape[1]
-    if tuple(out.shape) != (B, S, Hq, D) or tpp != 128 or tuple(page_table.shape[:2]) != (B, 2) or \
-            tuple(indices.shape[:2]) != (B, S) or tuple(ctx.shape) != (B,) or \
-            tuple(kv_scale.shape) != (nflat, nblk, Hkv) or nblk < 1 or 128 % nblk or \
-            (new_lengths is not None and tuple(new_lengths.shape) != (B,)):
+    sf, nblk, sh = kv_scale.shape
+    ptb, two, pages = page_table.shape
+    ib, is_, topK = indices.shape
+    if out.shape != (B, S, Hq, D) or tpp != 128 or ptb != B or two != 2 or ib != B or is_ != S or ctx.shape != (B,) or \
+            sf != nflat or sh != Hkv or nblk < 1 or 128 % nblk or \
+            (new_lengths is not None and new_lengths.shape != (B,)):
         raise ValueError("sparse_paged_kv8: shape mismatch")
-    p = QsaSparsePagedKv8Params(
-        qPtr=_ptr(q, et, "q"), kvPool=_ptr(pool, torch.float8_e4m3fn, "pool"),
-        kvScale=_ptr(kv_scale, torch.float32, "kv_scale"), pageTable=_ptr(page_table, torch.int32, "pageTable"),
-        indices=_ptr(indices, torch.int32, "indices"), contextLengths=_ptr(ctx, torch.int32, "contextLengths"),
-        newLengths=_ptr(new_lengths, torch.int32, "new_lengths"), oPtr=_ptr(out, et, "out"), batchSize=B, seqLen=S,
-        numQHeads=Hq, numKVHeads=Hkv, headDim=D, poolHeadDim=phd, numFlatPages=nflat,
-        maxPagesPerSeq=page_table.shape[-1], topK=indices.shape[-1], scaleBlock=128 // nblk, attentionScale=scale,
-        stream=_stream(stream), status=_ptr(status, torch.int32, "status"))
-    _same_device("sparse_paged_kv8", (q, pool, kv_scale, page_table, indices, ctx, new_lengths, out, status))
-    _check(getattr(lib(), "qsa_sparse_paged_kv8" + ("_bf16" if et == torch.bfloat16 else ""))(ctypes.byref(p)))
+    dev = _current_device(q)
+    f32, i32 = torch.float32, torch.int32
+    packed = _PAGED_PACK.pack(
+        _arg(q, et, "q", dev), _arg(pool, torch.float8_e4m3fn, "pool", dev), _arg(kv_scale, f32, "kv_scale", dev),
+        _arg(page_table, i32, "pageTable", dev), _arg(indices, i32, "indices", dev),
+        _arg(ctx, i32, "contextLengths", dev), _arg(new_lengths, i32, "new_lengths", dev), _arg(out, et, "out", dev), B,
+        S, Hq, Hkv, D, phd, nflat, pages, topK, 128 // nblk, scale, _raw_stream(stream, dev),
+        _arg(status, i32, "status", dev))
+    r = _packed("qsa_sparse_paged_kv8_bf16" if bf16 else "qsa_sparse_paged_kv8")(packed)
+    if r:
+        _check(r)

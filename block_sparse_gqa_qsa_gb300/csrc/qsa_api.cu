@@ -59,6 +59,20 @@ qsa::RopeFreqs rope_freqs(float theta, int rot) {
   return r;
 }
 
+// rope_freqs of the calling thread's last (theta, rot): the table is a function of the two alone, and a decode step
+// asks for the same one in every layer.
+const qsa::RopeFreqs& last_rope_freqs(float theta, int rot) {
+  thread_local qsa::RopeFreqs r;
+  thread_local float of_theta = 0.f;  // no valid theta
+  thread_local int of_rot = 0;
+  if (of_theta != theta || of_rot != rot) {
+    r = rope_freqs(theta, rot);
+    of_theta = theta;
+    of_rot = rot;
+  }
+  return r;
+}
+
 constexpr int kMaxAttnListWidth = 16384;  // attention stages one list (or slice) in shared memory
 
 // Indexer arguments shared by both indexers ("Qsa Attention Plugin" constructor
@@ -184,7 +198,7 @@ qsa_status_t append_kv_entry(const QsaAppendKvParams* p, const char* fn, bool bf
       static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
       static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL)
     return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen, maxPagesPerSeq or numFlatPages too large", fn);
-  const cudaError_t e = qsa::launch_append_kv(*p, rope_freqs(p->ropeTheta, p->rotDim), bf16, kv8);
+  const cudaError_t e = qsa::launch_append_kv(*p, last_rope_freqs(p->ropeTheta, p->rotDim), bf16, kv8);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
@@ -211,9 +225,10 @@ qsa_status_t sparse_paged_kv8_entry(const QsaSparsePagedKv8Params* p, const char
   if (static_cast<long long>(p->batchSize) * p->seqLen > 0x7fffffffLL ||
       static_cast<long long>(p->batchSize) * p->seqLen * p->numKVHeads > 0x7fffffffLL ||
       static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
-      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL)
-    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen * numKVHeads, maxPagesPerSeq or numFlatPages too large",
-                fn);
+      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numKVHeads) * p->poolHeadDim > 0x7fffffffLL)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen * numKVHeads, maxPagesPerSeq, numFlatPages or a pool row "
+                                     "too large", fn);
   const cudaError_t e = qsa::launch_sparse_paged_kv8(*p, bf16);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }

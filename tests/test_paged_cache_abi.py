@@ -122,9 +122,9 @@ def test_binding_refuses(qb):
     pool8, scale = torch.zeros(4, 128, 1, 128).to(torch.float8_e4m3fn), torch.ones(4, 8, 1)
     pt = torch.zeros(2, 2, 2, dtype=torch.int32)
     kw = dict(Hq=2, Hkv=1, rot=32, theta=1e4, eps=1e-6)
-    with pytest.raises(ValueError, match="CUDA"):
+    with pytest.raises(ValueError, match="CUDA tensor"):
         qb.append_kv(qkv, w, w, i, q, pool16, pt, **kw)
-    with pytest.raises(ValueError, match="CUDA"):
+    with pytest.raises(ValueError, match="CUDA tensor"):
         qb.append_kv8(qkv, w, w, i, q, pool8, scale, pt, **kw)
     with pytest.raises(ValueError, match="scale"):
         qb.append_kv8(qkv, w, w, i, q, pool8, None, pt, **kw)
@@ -141,7 +141,7 @@ def test_binding_refuses(qb):
     with pytest.raises(ValueError, match="k_out"):
         qb.append_kv(qkv, w, w, i, q, pool16, pt, k_out=q, **kw)
     lists = torch.zeros(2, 3, 5, dtype=torch.int32)
-    with pytest.raises(ValueError, match="CUDA"):
+    with pytest.raises(ValueError, match="CUDA tensor"):
         qb.sparse_paged_kv8(q, pool8, scale, pt, lists, i, q.clone(), scale=0.1)
     with pytest.raises(ValueError, match="float16 or bfloat16"):
         qb.sparse_paged_kv8(q.float(), pool8, scale, pt, lists, i, q.clone(), scale=0.1)
@@ -151,3 +151,11 @@ def test_binding_refuses(qb):
         qb.sparse_paged_kv8(q, pool8, scale[:, :5], pt, lists, i, q.clone(), scale=0.1)
     with pytest.raises(ValueError, match="dimensions"):
         qb.sparse_paged_kv8(q, pool8, scale, pt, lists[0], i, q.clone(), scale=0.1)
+
+
+def test_packed_params_are_the_structs(qb):
+    """The binding packs the params in one go: field for field what the ctypes structs (checked against C above) hold."""
+    for pack, cls in ((qb._APPEND_PACK, qb.QsaAppendKvParams), (qb._PAGED_PACK, qb.QsaSparsePagedKv8Params)):
+        values = [i + 1 for i in range(len(cls._fields_))]
+        got = cls.from_buffer_copy(pack.pack(*values))
+        assert pack.size == ctypes.sizeof(cls) and [getattr(got, f) for f, _ in cls._fields_] == values
