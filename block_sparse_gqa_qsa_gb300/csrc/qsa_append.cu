@@ -12,13 +12,13 @@
 // scales lies in one tile, so one warp owns a block and no atomics are needed.
 // A warp takes one head of up to 16 of the tile's rows at a time, copied by
 // cp.async into its own two-slot ring in shared memory: the next head's rows
-// travel while this one is computed, whatever the registers hold.  A lane
-// works on 8 values (16 bytes); the D/8 lanes of a row reduce its sum of
-// squares with shuffles, and because rotDim is a multiple of 16 a chunk's
-// rotation partner is a whole chunk of the same row, read from shared memory.
-// For an 8-bit pool a K or V head is passed over twice in shared memory: its
-// blocks' largest values first, then the codes.  Blocks of more than 16 tokens
-// are copied twice (the second time from L2).
+// travel while this one is computed.  rotDim is a multiple of 16, so a row's
+// 16-byte chunks of 8 values are whole rotation halves; a lane takes a chunk
+// of a first half and its partner chunk (or two chunks past rotDim), so the
+// rotation needs no exchange, and the D/16 lanes of a row reduce its sum of
+// squares with shuffles.  For an 8-bit pool a K or V head is passed over twice
+// in shared memory: its blocks' largest values first, then the codes.  Blocks
+// of more than 16 tokens are copied twice (the second time from L2).
 #include <algorithm>
 
 #include "qsa_internal.h"
@@ -29,8 +29,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 16;  // rows of a ring slot
-constexpr int kCtasPerSm = 3;
+constexpr int kTile = 16;  // most rows of a ring slot
+constexpr int kCtasPerSm = 2;
 
 struct AppendArgs {
   const void* qkv;
@@ -49,6 +49,7 @@ struct AppendArgs {
   int blockShift;        // log2(scaleBlock)
   int tile;              // positions per CTA: max(kTile, scaleBlock)
   int tiles;             // tiles per sequence
+  int slotRows;          // rows of a ring slot: min(kTile, S)
   float eps;
   unsigned long long turn[64];  // inv_freq of pair i as a 64-bit fixed-point fraction of a turn
 };
@@ -76,36 +77,39 @@ __device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Mean square of a row; x: this lane's 8 of its D values, as pairs.
+// Two chunks of a row, as pairs of values.
+struct Chunks {
+  uint64_t a[4], b[4];
+};
+
+// Mean square of a row whose D values the D/16 lanes of a group hold.
 template <int D>
-__device__ __forceinline__ float mean_square(const uint64_t (&x)[4]) {
-  uint64_t acc = fmul2(x[0], x[0]);
+__device__ __forceinline__ float mean_square(const Chunks& x) {
+  uint64_t p = fmul2(x.a[0], x.a[0]), q = fmul2(x.b[0], x.b[0]);
 #pragma unroll
-  for (int k = 1; k < 4; ++k) acc = ffma2(x[k], x[k], acc);
-  float ss = lo_f2(acc) + hi_f2(acc);
+  for (int k = 1; k < 4; ++k) {
+    p = ffma2(x.a[k], x.a[k], p);
+    q = ffma2(x.b[k], x.b[k], q);
+  }
+  float ss = (lo_f2(p) + hi_f2(p)) + (lo_f2(q) + hi_f2(q));
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+  for (int o = D / 32; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
   return ss * (1.0f / D);
 }
 
-// What a lane keeps of a head's norm and rotation: (1 + w) of its chunk, and of its partner chunk with the
-// rotation's sign (- for the first half of a pair).
-struct HeadWeights {
-  uint64_t own[4], partner[4];
-};
-
-// The 8 values of a lane's chunk after norm and rotation: with u = x (1 + w) and the partner chunk's u',
-// y = (u cos -+ u' sin) / sqrt(mean(x^2) + eps).  row: the 16-byte chunks of the head's row in shared memory;
-// cs: the row's table at this lane's chunk, `stride` apart (not read by lanes past rotDim).
+// x (1 + w) / sqrt(mean(x^2) + eps), and for lanes that hold rotated chunks (`rotated`) the rotation of (a, b) by the
+// row's table at this lane's chunk: (cos, cos), (sin, sin) of elements 2k, 2k + 1, hl apart.
 template <int D, bool kBf16>
-__device__ __forceinline__ void norm_rotate(const uint4* row, int j, int side, int hl, const HeadWeights& w, float eps,
-                                            const ulonglong2* cs, uint64_t (&y)[4]) {
-  unpack8<kBf16>(row[j], y);
-  float m = mean_square<D>(y) + eps, back = 1.0f;
+__device__ __forceinline__ void norm_rotate(Chunks& x, const Chunks& w, float eps, bool rotated, const ulonglong2* cs,
+                                            int hl) {
+  float m = mean_square<D>(x) + eps, back = 1.0f;
   if (kBf16 && __any_sync(kFull, m == INFINITY)) {  // squares past fp32: the same on values scaled by 2^-64
-    uint64_t z[4];
+    Chunks z;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) z[k] = fmul2(y[k], pack_f2(0x1p-64f, 0x1p-64f));
+    for (int k = 0; k < 4; ++k) {
+      z.a[k] = fmul2(x.a[k], pack_f2(0x1p-64f, 0x1p-64f));
+      z.b[k] = fmul2(x.b[k], pack_f2(0x1p-64f, 0x1p-64f));
+    }
     const float ms = mean_square<D>(z);  // eps is nothing beside squares of 2^128
     back = m == INFINITY ? 0x1p-64f : 1.0f;
     m = m == INFINITY ? ms : m;
@@ -113,18 +117,25 @@ __device__ __forceinline__ void norm_rotate(const uint4* row, int j, int side, i
   const float r = rsqrtf(m);
   const float inv = back * r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
 #pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], w.own[k]);
-  if (side) {
-    uint64_t u[4];
-    unpack8<kBf16>(row[j - side * hl], u);
+  for (int k = 0; k < 4; ++k) {
+    x.a[k] = fmul2(x.a[k], w.a[k]);
+    x.b[k] = fmul2(x.b[k], w.b[k]);
+  }
+  if (rotated) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const ulonglong2 t = cs[k * hl];  // (cos, cos), (sin, sin) of elements 2k, 2k + 1
-      y[k] = ffma2(fmul2(u[k], w.partner[k]), t.y, fmul2(y[k], t.x));
+      const ulonglong2 t = cs[k * hl];
+      const uint64_t u = fmul2(x.a[k], t.x);
+      const uint64_t v = ffma2(x.a[k], t.y, fmul2(x.b[k], t.x));
+      x.a[k] = pack_f2(fmaf(-lo_f2(x.b[k]), lo_f2(t.y), lo_f2(u)), fmaf(-hi_f2(x.b[k]), hi_f2(t.y), hi_f2(u)));
+      x.b[k] = v;
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] = fmul2(y[k], pack_f2(inv, inv));
+  for (int k = 0; k < 4; ++k) {
+    x.a[k] = fmul2(x.a[k], pack_f2(inv, inv));
+    x.b[k] = fmul2(x.b[k], pack_f2(inv, inv));
+  }
 }
 
 // Largest finite magnitude of 8 values (0 for none).
@@ -164,16 +175,24 @@ __device__ __forceinline__ uint2 rescale8(const uint2 c, float f) {
   return make_uint2(r[0], r[1]);
 }
 
+// Place of chunk c of ring row r: the lanes of a row read chunks 0 .. hl - 1 and 2 hl .. , or the others, at once, and
+// for the usual hl those lie in different banks.
+template <int D>
+__device__ __forceinline__ int place(int r, int c) {
+  return r * (D / 8) + (D == 128 ? c ^ ((c >> 3) << 2) : c ^ ((r & 1) << 2));
+}
+
 template <int D, bool kBf16, bool kKv8>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const AppendArgs a) {
-  constexpr int LPR = D / 8;              // lanes (16-byte chunks) per row
-  constexpr int RPW = 32 / LPR;           // rows of a warp-wide access
-  constexpr int kSlot = kTile * LPR;      // chunks of a ring slot
-  extern __shared__ __align__(16) uint4 smem[];  // [kWarps][2][kTile][LPR] rows, then the cos/sin table
+  constexpr int LPR = D / 8;    // chunks per row, lanes that copy one
+  constexpr int RPW = 32 / LPR; // rows of a warp-wide copy
+  constexpr int CPR = D / 16;   // lanes that compute a row, two chunks each
+  constexpr int RPI = 32 / CPR; // rows a warp computes at once
+  extern __shared__ __align__(16) uint4 smem[];  // [kWarps][2][slotRows][LPR] rows, then the cos/sin table
   __shared__ __align__(16) float w1[2][D];       // 1 + w of q and k heads
-  ulonglong2* table = reinterpret_cast<ulonglong2*>(smem + kWarps * 2 * kSlot);  // [row of the tile][4][rot / 16]
+  const int slotChunks = a.slotRows * LPR;
+  ulonglong2* table = reinterpret_cast<ulonglong2*>(smem + kWarps * 2 * slotChunks);  // [live row][4][rot / 16]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j = lane & (LPR - 1), sub = lane / LPR;
   const int b = blockIdx.x / a.tiles, tileIdx = blockIdx.x - b * a.tiles;
   const int L = max(a.ctx[b], 0);
   const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   // A warp's work: its heads in turn; for a K or V head of an 8-bit pool with blocks above kTile, all of the
   // tile's chunks of kTile rows for the largest values and once more for the codes; else each chunk once.
   struct Item {
-    int h, base;  // head, first row of the chunk
+    int h, base;  // head, row at the chunk's first position
     bool second;
   };
   const int c0 = t0 < tlo ? t0 + (tlo - t0) / kTile * kTile : t0;  // first chunk with a row of the CTA
@@ -197,24 +216,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     it.base += kTile;
     if (it.base >= thi) {
       it.base = c0;
-      if (twice && it.h >= a.Hq && !it.second) {
-        it.second = true;
-      } else {
-        it.second = false;
-        it.h += step;
-      }
+      const bool again = twice && it.h >= a.Hq && !it.second;
+      it.second = again;
+      it.h += again ? 0 : step;
     }
     return it;
   };
-  uint4* ring = smem + warp * 2 * kSlot;
-  const uint4* src = static_cast<const uint4*>(a.qkv) + static_cast<size_t>(b) * a.S * NH * LPR + j;
+  uint4* ring = smem + warp * 2 * slotChunks;
+  const uint4* src = static_cast<const uint4*>(a.qkv) + static_cast<size_t>(b) * a.S * NH * LPR + lane % LPR;
   auto copy = [&](const Item& it, int slot) {  // one copy group per item, empty past the last
     if (it.h < NH) {
-      const uint32_t dst = smem_addr(ring + slot * kSlot + lane);
+      const int first = max(it.base, tlo), rows = min(thi, it.base + kTile) - first;
+      const uint4* g = src + (static_cast<size_t>(first + lane / LPR) * NH + it.h) * LPR;
+      const size_t hop = static_cast<size_t>(RPW) * NH * LPR;
+      uint4* d = ring + slot * slotChunks;
+      if (rows == kTile) {
 #pragma unroll
-      for (int i = 0; i < kTile / RPW; ++i) {
-        const int t = it.base + i * RPW + sub;
-        if (t >= tlo && t < thi) cp_async16(dst + i * 32 * 16, src + (static_cast<size_t>(t) * NH + it.h) * LPR, true);
+        for (int i = 0; i < kTile / RPW; ++i)
+          cp_async16(smem_addr(d + place<D>(i * RPW + lane / LPR, lane % LPR)), g + i * hop, true);
+      } else {
+        for (int r = lane / LPR; r < rows; r += RPW, g += hop) cp_async16(smem_addr(d + place<D>(r, lane % LPR)), g, true);
       }
     }
     cp_async_commit();
@@ -229,23 +250,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     float cv, sv;
     rope_cos_sin_turns(static_cast<unsigned>(c + tlo + r), a.turn[pair], cv, sv);
     const int e = pair & 7;
-    float* dst = reinterpret_cast<float*>(table + ((tlo - t0 + r) * 4 + (e >> 1)) * hl + (pair >> 3)) + (e & 1);
+    float* dst = reinterpret_cast<float*>(table + (r * 4 + (e >> 1)) * hl + (pair >> 3)) + (e & 1);
     dst[0] = cv;
     dst[2] = sv;
   }
-  // dense output of head h at row t, or null
-  auto dense_at = [&](int h, int t) -> uint4* {
-    const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
-    uint4* d = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
-    if (!d) return nullptr;
-    const int heads = isq ? a.Hq : a.Hkv, hh = isq ? h : (isv ? h - a.Hq - a.Hkv : h - a.Hq);
-    return d + ((static_cast<size_t>(b) * a.S + t) * heads + hh) * LPR + j;
-  };
-  const int tpad = min(a.S, t0 + a.tile);
-  if (max(thi, tlo) < tpad)  // padding rows: zeros in the dense outputs
-    for (int h = blockIdx.y * kWarps + warp; h < NH; h += step)
-      for (int t = max(thi, tlo) + sub; t < tpad; t += RPW)
-        if (uint4* d = dense_at(h, t)) *d = make_uint4(0, 0, 0, 0);
+  // padding rows: zeros in the dense outputs, where the tile's lie together
+  const int tpad = min(a.S, t0 + a.tile), tfirst = max(thi, tlo);
+  if (tfirst < tpad) {
+    auto zero = [&](void* out, int heads) {
+      if (!out) return;
+      uint4* d = static_cast<uint4*>(out) + (static_cast<size_t>(b) * a.S + tfirst) * heads * LPR;
+      const int chunks = (tpad - tfirst) * heads * LPR;
+      for (int i = blockIdx.y * kThreads + threadIdx.x; i < chunks; i += gridDim.y * kThreads) d[i] = make_uint4(0, 0, 0, 0);
+    };
+    zero(a.qout, a.Hq);
+    zero(a.kout, a.Hkv);
+    zero(a.vout, a.Hkv);
+  }
   if (thi <= tlo) return;
 
   // the tile's pages: it lies in one page of K and one of V
@@ -266,51 +287,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   if (badPage && threadIdx.x == 0 && a.status) atomicOr(a.status, kErrBadPage);
   __syncthreads();
 
-  const int side = j < hl ? -1 : (j < 2 * hl ? 1 : 0);
-  HeadWeights w;
+  const int l = lane & (CPR - 1), sub = lane / CPR;
+  const bool rotated = l < hl;
+  const int ca = rotated ? l : hl + l, cb = rotated ? l + hl : l + CPR;  // this lane's chunks
+  Chunks w;
   int have = -1;        // whose weights w holds: 0 q heads, 1 k heads
-  float bm = 0.f;       // lanes 0..15, 8-bit: largest value of row `lane` (of the whole block, for blocks above 16)
-  float rowInv = 0.f;   // lanes 0..15, 8-bit: 1 / scale of row `lane`
+  float bm = 0.f;       // lanes 0..15, 8-bit: largest value of chunk position `lane` (of the whole block, above 16)
+  float rowInv = 0.f;   // lanes 0..15, 8-bit: 1 / scale at chunk position `lane`
   for (int slot = 0; cur.h < NH; slot ^= 1) {
     const Item nxt = next_item(cur);
     copy(nxt, slot ^ 1);
     cp_async_wait<1>();
     __syncwarp();
     const int h = cur.h, base = cur.base;
+    const int first = max(base, tlo), rows = min(thi, base + kTile) - first, off = first - base;
     const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
-    const int hk = isq ? 0 : (isv ? h - a.Hq - a.Hkv : h - a.Hq);
+    const int hk = isq ? h : (isv ? h - a.Hq - a.Hkv : h - a.Hq);  // among the q, k or v heads
     const int pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
-    const uint4* rows = ring + slot * kSlot;
+    const uint4* buf = ring + slot * slotChunks;
     if (!isv && have != (isq ? 0 : 1)) {
       have = isq ? 0 : 1;
-      const uint64_t flip = side < 0 ? 0x8000000080000000ull : 0ull;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        w.own[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * j + 2 * k]);
-        w.partner[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * (j - side * hl) + 2 * k]) ^ flip;
+        w.a[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * ca + 2 * k]);
+        w.b[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * cb + 2 * k]);
       }
     }
-    auto value = [&](int rr, uint64_t (&y)[4]) {  // rr: row of the chunk
-      if (isv)
-        unpack8<kBf16>(rows[rr * LPR + j], y);
-      else
-        norm_rotate<D, kBf16>(rows + rr * LPR, j, side, hl, w, a.eps,
-                              table + (base - t0 + rr) * 4 * hl + (side > 0 ? j - hl : j), y);
+    // The lane's values of the chunk's r-th live row (r past the last: no row, anything).
+    auto value = [&](int r, uint4& rawa, uint4& rawb, Chunks& y) {
+      const int rc = min(r, rows - 1);
+      rawa = buf[place<D>(rc, ca)];
+      rawb = buf[place<D>(rc, cb)];
+      unpack8<kBf16>(rawa, y.a);
+      unpack8<kBf16>(rawb, y.b);
+      if (!isv) norm_rotate<D, kBf16>(y, w, a.eps, rotated, table + (first - tlo + rc) * 4 * hl + l, hl);
     };
-    const int i0 = max(tlo - base, 0) / RPW, i1 = (min(thi - base, kTile) + RPW - 1) / RPW;  // accesses with live rows
 
     if (kKv8 && !isq && !cur.second) {  // the largest value of each row, then of each block
       float rm = 0.f;
-#pragma unroll 1
-      for (int i = i0; i < i1; ++i) {
-        uint64_t y[4];
-        value(i * RPW + sub, y);
-        const int t = base + i * RPW + sub;
-        float m = t >= tlo && t < thi ? finite_max(y) : 0.f;
+      for (int i = 0; i * RPI < rows; ++i) {
+        uint4 ra, rb;
+        Chunks y;
+        value(i * RPI + sub, ra, rb, y);
+        float m = fmaxf(finite_max(y.a), finite_max(y.b));
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        m = __shfl_sync(kFull, m, (lane % RPW) * LPR);
-        if (lane / RPW == i) rm = m;
+        for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        const int r = lane - off - i * RPI;  // lane's row among these
+        m = __shfl_sync(kFull, m, (r & (RPI - 1)) * CPR);
+        if (r >= 0 && r < RPI && lane - off < rows) rm = m;
       }
       const int sb = 1 << a.blockShift;
       for (int o = 1; o < min(sb, kTile); o <<= 1) rm = fmaxf(rm, __shfl_xor_sync(kFull, rm, o));
@@ -344,41 +368,52 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
         // older rows of the grown block (at most one block of the tile holds older tokens)
         const float f = __shfl_sync(kFull, shrink, twice || t0 >= 0 ? 0 : (-t0) & ~(sb - 1));
         if (t0 < 0 && f != 1.f && pageId >= 0)
-          for (int p = (c & ~(sb - 1)) + sub; p < c; p += RPW) {
+          for (int p = (c & ~(sb - 1)) + lane / LPR; p < c; p += RPW) {
             uint2* row = reinterpret_cast<uint2*>(
                              a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + (p & 127)) * a.Hkv + hk) *
-                                          a.poolHeadDim) + j;
+                                          a.poolHeadDim) + lane % LPR;
             *row = rescale8(*row, f);
           }
       }
     }
 
     if (!kKv8 || isq || !twice || cur.second) {
-      uint4* dense = dense_at(h, base + sub);
-      const size_t denseStep = static_cast<size_t>(isq ? a.Hq : a.Hkv) * LPR * RPW;
-      uint8_t* prow = nullptr;
-      const size_t poolStep = static_cast<size_t>(a.Hkv) * a.poolHeadDim * (kKv8 ? 1 : 2) * RPW;
-      if (pageId >= 0)
-        prow = a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + ((c + base + sub) & 127)) * a.Hkv + hk) *
-                            a.poolHeadDim * (kKv8 ? 1 : 2);
+      uint4* dense = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
+      const int heads = isq ? a.Hq : a.Hkv;
+      if (dense) dense += ((static_cast<size_t>(b) * a.S + first + sub) * heads + hk) * LPR;
+      constexpr int kElem = kKv8 ? 1 : 2;
+      const size_t rowBytes = static_cast<size_t>(a.Hkv) * a.poolHeadDim * kElem;
+      uint8_t* prow = pageId < 0 ? nullptr
+                                 : a.pool + (static_cast<size_t>(pageId) * kTokensPerPage + ((c + first) & 127) + sub) * rowBytes +
+                                       static_cast<size_t>(hk) * a.poolHeadDim * kElem;
 #pragma unroll 2
-      for (int i = i0; i < i1; ++i) {
-        const int rr = i * RPW + sub, t = base + rr;
-        const bool live = t >= tlo && t < thi;
-        uint64_t y[4];
-        value(rr, y);
-        const float qs = kKv8 && !isq ? __shfl_sync(kFull, rowInv, rr) : 0.f;
-        if (!live) continue;
-        const bool whole = dense || (!kKv8 && prow);
-        uint4 out;
-        if (whole) out = isv ? rows[rr * LPR + j] : pack8<kBf16>(y);
-        if (dense) dense[i * denseStep] = out;
-        if (prow) {
-          if constexpr (kKv8)
-            reinterpret_cast<uint2*>(prow + i * poolStep)[j] = quantise8(y, qs);
-          else
-            reinterpret_cast<uint4*>(prow + i * poolStep)[j] = out;
+      for (int i = 0; i * RPI < rows; ++i) {
+        const int r = i * RPI + sub;
+        uint4 ra, rb;
+        Chunks y;
+        value(r, ra, rb, y);
+        const float qs = kKv8 && !isq ? __shfl_sync(kFull, rowInv, (off + r) & (kTile - 1)) : 0.f;
+        if (r < rows) {
+          if (!isv && (dense || !kKv8)) {
+            ra = pack8<kBf16>(y.a);
+            rb = pack8<kBf16>(y.b);
+          }
+          if (dense) {
+            dense[ca] = ra;
+            dense[cb] = rb;
+          }
+          if (prow) {
+            if constexpr (kKv8) {
+              reinterpret_cast<uint2*>(prow)[ca] = quantise8(y.a, qs);
+              reinterpret_cast<uint2*>(prow)[cb] = quantise8(y.b, qs);
+            } else {
+              reinterpret_cast<uint4*>(prow)[ca] = ra;
+              reinterpret_cast<uint4*>(prow)[cb] = rb;
+            }
+          }
         }
+        if (dense) dense += static_cast<size_t>(RPI) * heads * LPR;
+        if (prow) prow += RPI * rowBytes;
       }
     }
     __syncwarp();  // every lane is done with the slot
@@ -390,11 +425,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
 template <int D, bool kBf16, bool kKv8>
 cudaError_t append_go(const AppendArgs& a, int B, cudaStream_t st) {
   auto kernel = append_kv_kernel<D, kBf16, kKv8>;
-  // the warps' rings and the table: 32 or 64 KB, and 8 bytes per row and rotated pair (at most 64 KB)
-  const size_t smem = kWarps * 2 * kTile * (D * 2) + static_cast<size_t>(a.tile) * (a.rot / 2) * 8;
-  const cudaError_t attr =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (attr != cudaSuccess) return attr;
+  // the warps' rings, and the table of 8 bytes per row and rotated pair: at most 64 KB each
+  const size_t smem = kWarps * 2 * static_cast<size_t>(a.slotRows) * (D * 2) +
+                      static_cast<size_t>(std::min(a.tile, a.S)) * (a.rot / 2) * 8;
+  if (smem > 40 * 1024) {  // past what a kernel may have without asking (48 KB, w1 among it)
+    const cudaError_t attr =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (attr != cudaSuccess) return attr;
+  }
   // One CTA per tile when the tiles fill the GPU a few times over; otherwise the heads of a tile are dealt
   // out to several CTAs, down to one head per warp.
   const long long tiles = static_cast<long long>(B) * a.tiles;
@@ -439,6 +477,7 @@ cudaError_t launch_append_kv(const QsaAppendKvParams& p, const RopeFreqs& rf, bo
   a.tile = std::max(kTile, p.scaleBlock);
   // the most aligned tiles that seqLen consecutive positions touch
   a.tiles = static_cast<int>((static_cast<long long>(p.seqLen) + a.tile - 2) / a.tile + 1);
+  a.slotRows = std::min(kTile, p.seqLen);
   a.eps = p.rmsNormEps;
   for (int i = 0; i < 64; ++i) a.turn[i] = rf.turn[i];
   cudaStream_t st = static_cast<cudaStream_t>(p.stream);

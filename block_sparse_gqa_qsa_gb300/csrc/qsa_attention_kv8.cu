@@ -26,6 +26,8 @@
 // converts them to fp16 pairs in registers (exact), for V after interleaving
 // the bytes of two keys.
 #include <algorithm>
+#include <cfloat>
+#include <utility>
 
 #include "qsa_internal.h"
 #include "qsa_kv8.cuh"
@@ -38,7 +40,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kD = 128;
 constexpr int kStep = 32;                      // list entries of a warp's step
 constexpr int kTileBytes = kStep * kD;         // K (or V) rows of a step
-constexpr int kWarpBytes = 2 * kTileBytes;     // one K tile, one V tile
+// A warp's shared memory: a K tile, a V tile, the pool rows of two steps' entries (K then V), a step's Entry values.
+constexpr int kRowsAt = 2 * kTileBytes;
+constexpr int kEntriesAt = kRowsAt + 2 * 2 * kStep * 4;
+constexpr int kWarpBytes = kEntriesAt + kStep * 16;
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -95,8 +100,39 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
 __device__ __forceinline__ uint32_t k_off(int r, int c) { return r * kD + ((c ^ ((r & 1) << 2)) << 4); }
 __device__ __forceinline__ uint32_t v_off(int r, int c) { return r * kD + ((c ^ (r & 6)) << 4); }
 
-__device__ __forceinline__ void cp_async16_all(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+// 16-byte copy to dst + kOff.
+template <int kOff>
+__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;\n" ::"r"(dst), "l"(src), "n"(kOff) : "memory");
+}
+template <int kOff>
+__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src, bool pred) {
+  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(pred ? 16 : 0), "n"(kOff)
+               : "memory");
+}
+__device__ __forceinline__ float lg2_ftz(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One lane's eight 16-byte copies of a gather: rows 4 i + (lane >> 3), i = 0..7, each at dst[i & 1] + 512 i.
+// base: the lane's chunk of pool row 0.  kAll: every row is named (row >= 0); otherwise the others are zeros.
+template <bool kAll, size_t... I>
+__device__ __forceinline__ void copy_rows(const int (&row)[8], const uint32_t (&dst)[2], const uint8_t* base,
+                                          uint32_t rowBytes, std::index_sequence<I...>) {
+  if constexpr (kAll) {
+    (cp_async16_to<4 * kD * I>(dst[I & 1], base + static_cast<uint64_t>(static_cast<uint32_t>(row[I])) * rowBytes), ...);
+  } else {
+    (cp_async16_to<4 * kD * I>(dst[I & 1], base + static_cast<uint64_t>(static_cast<uint32_t>(max(row[I], 0))) * rowBytes,
+                               row[I] >= 0),
+     ...);
+  }
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
@@ -113,13 +149,6 @@ struct Acc {
   float o[8][NT][4];
   float m[NT][2];
   float l[NT][2];
-};
-
-// What lane i knows of entry i of a step.
-struct Entry {
-  float ks;  // K scale * attentionScale * log2(e); 0 for an entry that names nothing
-  float lv;  // log2(V scale); -inf for an entry that names nothing
-  float iv;  // 1 / V scale; 0 for an entry that names nothing
 };
 
 // S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + g and + 8, heads 8 nt + 2 q and + 1.
@@ -149,18 +178,21 @@ __device__ __forceinline__ void scores32(float (&s)[2][NT][4], uint32_t tile, co
 // Online softmax of a step: s becomes the weights relative to the running maximum, returned in fp16 as the B
 // fragments of the second product.  The maximum moves only when a weight would pass 2^kHeadroom (the weights
 // are relative numbers: nothing is lost by their being up to 256 instead of 1), so that O is hardly ever
-// rescaled after a warp's first step.
+// rescaled after a warp's first step.  It starts at the lowest finite number, so that an entry that names nothing
+// (-inf) weighs 0 even before the first that does.  entries[i], of key i: x = K scale * attentionScale * log2(e),
+// y = log2(V scale), z = 1 / V scale; (0, -inf, 0) for an entry that names nothing.
 template <int NT, bool kBf16>
-__device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], const float (&qs)[NT][2], const Entry& en,
-                                          uint32_t (&pb)[2][NT][2]) {
+__device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], const float (&qs)[NT][2],
+                                          const float4* entries, uint32_t (&pb)[2][NT][2]) {
   constexpr float kHeadroom = 8.f;
   const int lane = threadIdx.x & 31, g = lane >> 2;
   float ks[4], lv[4], iv[4];  // of keys g, g + 8, g + 16, g + 24
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    ks[i] = __shfl_sync(kFull, en.ks, g + 8 * i);
-    lv[i] = __shfl_sync(kFull, en.lv, g + 8 * i);
-    iv[i] = __shfl_sync(kFull, en.iv, g + 8 * i);
+    const float4 e = entries[g + 8 * i];
+    ks[i] = e.x;
+    lv[i] = e.y;
+    iv[i] = e.z;
   }
   float mx[NT][2];
   bool move = false;
@@ -189,7 +221,7 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float mn = fmaxf(A.m[nt][h], mx[nt][h]);
-        al[h] = ex2_ftz(A.m[nt][h] - (mn == -INFINITY ? 0.f : mn));
+        al[h] = ex2_ftz(A.m[nt][h] - mn);
         A.m[nt][h] = mn;
         A.l[nt][h] *= al[h];
       }
@@ -206,11 +238,10 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float mu = A.m[nt][h] == -INFINITY ? 0.f : A.m[nt][h];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float& x = s[i >> 1][nt][2 * (i & 1) + h];
-        x = ex2_ftz(x - mu);
+        x = ex2_ftz(x - A.m[nt][h]);
         A.l[nt][h] = fmaf(x, iv[i], A.l[nt][h]);
       }
     }
@@ -321,104 +352,108 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
   const int32_t* ptV = ptK + a.maxPagesPerSeq;
   const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
   const int first = kStep * (rank * kWarps + warp) + lane;
-  const uint32_t ktile = smem_addr(smem) + warp * kWarpBytes, vtile = ktile + kTileBytes;
+  uint8_t* mine = smem + warp * kWarpBytes;
+  const uint32_t ktile = smem_addr(mine), vtile = ktile + kTileBytes;
+  int* rows = reinterpret_cast<int*>(mine + kRowsAt);  // [step & 1][K, V][row & 3][row >> 2]
+  float4* entries = reinterpret_cast<float4*>(mine + kEntriesAt);
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
   const uint8_t* base = a.pool + static_cast<size_t>(kvh) * a.poolHeadDim + (lane & 7) * 16;
 
+  // Resolving an entry is free of branches: what an entry cannot name is looked up at 0 and dropped.
   int bad = 0;
   auto list_at = [&](int slot) { return slot < a.topK ? __ldg(lst + slot) : -1; };
   struct Pages {
     int j, k, v;  // entry (-1: none), its page ids
   };
   auto pages_of = [&](int j) {
-    Pages p{-1, -1, -1};
-    if (static_cast<unsigned>(j) < static_cast<unsigned>(L)) {
-      p.j = j;
-      p.k = __ldg(ptK + (j >> 7));
-      p.v = __ldg(ptV + (j >> 7));
-    } else if (j != -1) {
-      bad |= kErrBadIndex;
-    }
-    return p;
+    const bool in = static_cast<unsigned>(j) < static_cast<unsigned>(L);
+    bad |= !in && j != -1 ? kErrBadIndex : 0;
+    const int at = in ? j >> 7 : 0;
+    return Pages{in ? j : -1, __ldg(ptK + at), __ldg(ptV + at)};
   };
   struct Rows {
-    int k, v;       // pool rows of lane's entry; -1: none
-    float ks, vs;   // their scales as stored
-    unsigned mask;  // lanes whose entry names a row
+    bool ok;        // the lane's entry names a row
+    float ks, vs;   // its scales as stored
+    unsigned mask;  // lanes whose entry does
   };
-  auto resolve = [&](const Pages& p) {
-    Rows r{-1, -1, 0.f, 0.f, 0u};
-    const bool ok = p.j >= 0 && static_cast<unsigned>(p.k) < static_cast<unsigned>(a.numFlatPages) &&
-                    static_cast<unsigned>(p.v) < static_cast<unsigned>(a.numFlatPages);
-    if (p.j >= 0 && !ok) bad |= kErrBadPage;
-    if (ok) {
-      r.k = p.k * kTokensPerPage + (p.j & 127);
-      r.v = p.v * kTokensPerPage + (p.j & 127);
-      r.ks = __ldg(a.scale + static_cast<size_t>(r.k >> a.blockShift) * a.Hkv + kvh);
-      r.vs = __ldg(a.scale + static_cast<size_t>(r.v >> a.blockShift) * a.Hkv + kvh);
-    }
-    r.mask = __ballot_sync(kFull, ok);
+  auto resolve = [&](const Pages& p, int parity) {
+    Rows r;
+    const bool pages = static_cast<unsigned>(p.k) < static_cast<unsigned>(a.numFlatPages) &&
+                       static_cast<unsigned>(p.v) < static_cast<unsigned>(a.numFlatPages);
+    r.ok = p.j >= 0 && pages;
+    bad |= p.j >= 0 && !pages ? kErrBadPage : 0;
+    const int krow = r.ok ? p.k * kTokensPerPage + (p.j & 127) : 0;
+    const int vrow = r.ok ? p.v * kTokensPerPage + (p.j & 127) : 0;
+    r.ks = __ldg(a.scale + static_cast<size_t>(krow >> a.blockShift) * a.Hkv + kvh);
+    r.vs = __ldg(a.scale + static_cast<size_t>(vrow >> a.blockShift) * a.Hkv + kvh);
+    r.mask = __ballot_sync(kFull, r.ok);
+    int* at = rows + parity * 2 * kStep + (lane & 3) * (kStep / 4) + (lane >> 2);
+    at[0] = r.ok ? krow : -1;
+    at[kStep] = r.ok ? vrow : -1;
     return r;
   };
-  // Gathers the 32 rows that the lanes hold into a tile, 8 lanes to a row of 128 bytes: one copy group.
-  auto gather = [&](int row, unsigned mask, auto dst) {
-    if (mask == kFull) {
-#pragma unroll
-      for (int i = 0; i < kStep / 4; ++i)
-        cp_async16_all(dst(i), base + static_cast<uint64_t>(static_cast<uint32_t>(
-                                          __shfl_sync(kFull, row, 4 * i + (lane >> 3)))) * rowBytes);
-    } else if (mask) {  // rows that are not named are zeros
-#pragma unroll
-      for (int i = 0; i < kStep / 4; ++i) {
-        const int r = __shfl_sync(kFull, row, 4 * i + (lane >> 3));
-        cp_async16(dst(i), base + static_cast<uint64_t>(static_cast<uint32_t>(max(r, 0))) * rowBytes, r >= 0);
-      }
+  // Gathers a step's K (plane 0) or V (1) rows into the tile, 8 lanes to a row of 128 bytes: one copy group.
+  const uint32_t kdst[2] = {ktile + k_off(lane >> 3, lane & 7), ktile + k_off(lane >> 3, lane & 7)};
+  const uint32_t v0 = vtile + v_off(lane >> 3, lane & 7), vdst[2] = {v0, v0 ^ 64};  // rows 4 i: bit 2 flips with i
+  auto gather = [&](int parity, int plane, unsigned mask, const uint32_t (&dst)[2]) {
+    const int4* at = reinterpret_cast<const int4*>(rows + (parity * 2 + plane) * kStep + (lane >> 3) * (kStep / 4));
+    if (mask) {
+      const int4 x = at[0], y = at[1];
+      const int row[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (mask == kFull)
+        copy_rows<true>(row, dst, base, rowBytes, std::make_index_sequence<8>{});
+      else
+        copy_rows<false>(row, dst, base, rowBytes, std::make_index_sequence<8>{});
     }
     cp_async_commit();
   };
-  const uint32_t kdst = ktile + k_off(lane >> 3, lane & 7), vdst = vtile + v_off(lane >> 3, lane & 7);
-  auto gather_k = [&](const Rows& r) { gather(r.k, r.mask, [&](int i) { return kdst + i * 4 * kD; }); };
-  auto gather_v = [&](const Rows& r) { gather(r.v, r.mask, [&](int i) { return (vdst ^ ((i & 1) << 6)) + i * 4 * kD; }); };
 
   Acc<NT> A;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) A.o[mt][nt][0] = A.o[mt][nt][1] = A.o[mt][nt][2] = A.o[mt][nt][3] = 0.f;
-    A.m[nt][0] = A.m[nt][1] = -INFINITY;
+    A.m[nt][0] = A.m[nt][1] = -FLT_MAX;
     A.l[nt][0] = A.l[nt][1] = 0.f;
   }
   const int steps = max(0, (a.topK - (first - lane) + hop - 1) / hop);
-  Rows cur = resolve(pages_of(list_at(first)));
-  gather_k(cur);
-  gather_v(cur);
+  Rows cur = resolve(pages_of(list_at(first)), 0);
+  __syncwarp();
+  gather(0, 0, cur.mask, kdst);
+  gather(0, 1, cur.mask, vdst);
   Pages p1 = pages_of(list_at(first + hop));
-  int j2 = list_at(first + 2 * hop);
+  int slot = first + 2 * hop, j2 = list_at(slot);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
   load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + head0 * (kD / 8), a.G, qf, qs);
   for (int i = 0; i < steps; ++i) {
-    const Rows next = resolve(p1);
+    const int par = (i + 1) & 1;
+    const Rows next = resolve(p1, par);
     p1 = pages_of(j2);
-    j2 = list_at(first + (i + 3) * hop);
-    float s[2][NT][4];
-    uint32_t pb[2][NT][2];
-    cp_async_wait<1>();  // this lane's share of the K tile; the V tile may be in flight
-    __syncwarp();
-    if (cur.mask) scores32<NT>(s, ktile, qf);
-    __syncwarp();  // every lane is done with the K tile
-    gather_k(next);
+    slot += hop;
+    j2 = list_at(slot);
     if (cur.mask) {
-      const bool ok = cur.k >= 0;
       const float vs = read_scale(cur.vs);
-      const Entry en{ok ? read_scale(cur.ks) * a.sl2 : 0.f, ok ? __log2f(vs) : -INFINITY, ok ? 1.0f / vs : 0.f};
-      softmax32<NT, kBf16>(A, s, qs, en, pb);
+      entries[lane] = cur.ok ? make_float4(read_scale(cur.ks) * a.sl2, lg2_ftz(vs), rcp_ftz(vs), 0.f)
+                             : make_float4(0.f, -INFINITY, 0.f, 0.f);
+      float s[2][NT][4];
+      uint32_t pb[2][NT][2];
+      cp_async_wait<1>();  // this lane's share of the K tile; the V tile may be in flight
+      __syncwarp();
+      scores32<NT>(s, ktile, qf);
+      __syncwarp();  // every lane is done with the K tile
+      gather(par, 0, next.mask, kdst);
+      softmax32<NT, kBf16>(A, s, qs, entries, pb);
+      cp_async_wait<1>();  // the V tile; the next K tile may be in flight
+      __syncwarp();
+      values32<NT>(A, vtile, pb);
+      __syncwarp();  // every lane is done with the V tile
+      gather(par, 1, next.mask, vdst);
+    } else {  // nothing was copied for this step
+      __syncwarp();
+      gather(par, 0, next.mask, kdst);
+      gather(par, 1, next.mask, vdst);
     }
-    cp_async_wait<1>();  // the V tile; the next K tile may be in flight
-    __syncwarp();
-    if (cur.mask) values32<NT>(A, vtile, pb);
-    __syncwarp();
-    gather_v(next);
     cur = next;
   }
   cp_async_wait<0>();
@@ -456,13 +491,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
     }
   __syncthreads();
   for (int h = warp; h < a.G; h += kWarps) {
-    float M = -INFINITY, l = 0.f;
+    float M = -FLT_MAX, l = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mw[w * H + h]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float m = mw[w * H + h], f = m == -INFINITY ? 0.f : exp2f(m - M);
+      const float f = exp2f(mw[w * H + h] - M);
       const float4 x = ow[(w * H + h) * 32 + (lane ^ ((h >> 1) & 3))];
       l += f * lw[w * H + h];
       o.x += f * x.x;
@@ -487,16 +522,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
   const uint32_t ocAddr = smem_addr(oc), mcAddr = smem_addr(mc);
   for (int h = rank * kWarps + warp; h < a.G; h += a.split * kWarps) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ms[kMaxCluster], M = -INFINITY, l = 0.f;
+    float ms[kMaxCluster], M = -FLT_MAX, l = 0.f;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
-      ms[r] = r < a.split ? cluster_ld(cluster_addr(mcAddr + h * 4, r)) : -INFINITY;
+      ms[r] = r < a.split ? cluster_ld(cluster_addr(mcAddr + h * 4, r)) : -FLT_MAX;
       M = fmaxf(M, ms[r]);
     }
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
       if (r < a.split) {
-        const float f = ms[r] == -INFINITY ? 0.f : exp2f(ms[r] - M);
+        const float f = exp2f(ms[r] - M);
         const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * 32 + lane) * 16, r));
         l += f * cluster_ld(cluster_addr(mcAddr + (H + h) * 4, r));
         o.x += f * x.x;
