@@ -20,6 +20,7 @@
 // in shared memory: its blocks' largest values first, then the codes.  Blocks
 // of more than 16 tokens are copied twice (the second time from L2).
 #include <algorithm>
+#include <type_traits>
 
 #include "qsa_internal.h"
 #include "qsa_kv8.cuh"
@@ -30,7 +31,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;  // most rows of a ring slot
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxWideHeads = 512;  // K and V heads of a CTA whose tile is one block of more than kTile tokens
 
 struct AppendArgs {
   const void* qkv;
@@ -49,7 +51,9 @@ struct AppendArgs {
   int blockShift;        // log2(scaleBlock)
   int tile;              // positions per CTA: max(kTile, scaleBlock)
   int tiles;             // tiles per sequence
-  int slotRows;          // rows of a ring slot: min(kTile, S)
+  int slotRows;          // rows of a ring slot
+  int group;             // rows of a q head's item (any head's, for a 16-bit pool)
+  int headsPerCta;
   float eps;
   unsigned long long turn[64];  // inv_freq of pair i as a 64-bit fixed-point fraction of a turn
 };
@@ -97,11 +101,10 @@ __device__ __forceinline__ float mean_square(const Chunks& x) {
   return ss * (1.0f / D);
 }
 
-// x (1 + w) / sqrt(mean(x^2) + eps), and for lanes that hold rotated chunks (`rotated`) the rotation of (a, b) by the
-// row's table at this lane's chunk: (cos, cos), (sin, sin) of elements 2k, 2k + 1, hl apart.
+// x (1 + w) / sqrt(mean(x^2) + eps), then the rotation of (a, b) by the table entries cs, `hop` apart: (cos, cos),
+// (sin, sin) of elements 2k, 2k + 1 (lanes past rotDim get (1, 1), (0, 0)).
 template <int D, bool kBf16>
-__device__ __forceinline__ void norm_rotate(Chunks& x, const Chunks& w, float eps, bool rotated, const ulonglong2* cs,
-                                            int hl) {
+__device__ __forceinline__ void norm_rotate(Chunks& x, const Chunks& w, float eps, const ulonglong2* cs, int hop) {
   float m = mean_square<D>(x) + eps, back = 1.0f;
   if (kBf16 && __any_sync(kFull, m == INFINITY)) {  // squares past fp32: the same on values scaled by 2^-64
     Chunks z;
@@ -116,25 +119,14 @@ __device__ __forceinline__ void norm_rotate(Chunks& x, const Chunks& w, float ep
   }
   const float r = rsqrtf(m);
   const float inv = back * r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
+  const uint64_t inv2 = pack_f2(inv, inv);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    x.a[k] = fmul2(x.a[k], w.a[k]);
-    x.b[k] = fmul2(x.b[k], w.b[k]);
-  }
-  if (rotated) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const ulonglong2 t = cs[k * hl];
-      const uint64_t u = fmul2(x.a[k], t.x);
-      const uint64_t v = ffma2(x.a[k], t.y, fmul2(x.b[k], t.x));
-      x.a[k] = pack_f2(fmaf(-lo_f2(x.b[k]), lo_f2(t.y), lo_f2(u)), fmaf(-hi_f2(x.b[k]), hi_f2(t.y), hi_f2(u)));
-      x.b[k] = v;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x.a[k] = fmul2(x.a[k], pack_f2(inv, inv));
-    x.b[k] = fmul2(x.b[k], pack_f2(inv, inv));
+    const ulonglong2 t = cs[k * hop];
+    const uint64_t p = fmul2(x.a[k], w.a[k]), q = fmul2(x.b[k], w.b[k]), u = fmul2(p, t.x);
+    const uint64_t v = pack_f2(fmaf(-lo_f2(q), lo_f2(t.y), lo_f2(u)), fmaf(-hi_f2(q), hi_f2(t.y), hi_f2(u)));
+    x.a[k] = fmul2(v, inv2);
+    x.b[k] = fmul2(ffma2(p, t.y, fmul2(q, t.x)), inv2);
   }
 }
 
@@ -190,6 +182,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   constexpr int RPI = 32 / CPR; // rows a warp computes at once
   extern __shared__ __align__(16) uint4 smem[];  // [kWarps][2][slotRows][LPR] rows, then the cos/sin table
   __shared__ __align__(16) float w1[2][D];       // 1 + w of q and k heads
+  __shared__ ulonglong2 identity;                // the table entry of lanes past rotDim
+  __shared__ int blockMax[kMaxWideHeads];        // blocks above kTile: largest value of each K/V head, as float bits
+  __shared__ float blockInv[kMaxWideHeads];      // and 1 / their scale
   const int slotChunks = a.slotRows * LPR;
   ulonglong2* table = reinterpret_cast<ulonglong2*>(smem + kWarps * 2 * slotChunks);  // [live row][4][rot / 16]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,63 +192,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   const int L = max(a.ctx[b], 0);
   const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
   const int c = L - n;                            // position of row 0
-  const int t0 = tileIdx * a.tile - c % a.tile;   // row at the tile's first position
+  const int t0 = tileIdx * a.tile - (c & (a.tile - 1));   // row at the tile's first position
   if (t0 >= a.S) return;
   const int tlo = max(t0, 0);                     // first row of this CTA
   const int thi = min(min(a.S, n), t0 + a.tile);  // past its last live row; the tile's later rows are padding
   const int NH = a.Hq + 2 * a.Hkv;
-  const int step = gridDim.y * kWarps;
+  const int h0 = blockIdx.y * a.headsPerCta, h1 = min(NH, h0 + a.headsPerCta);
+  const bool wide = kKv8 && a.tile > kTile;       // the tile is one block of more than kTile tokens
 
-  // A warp's work: its heads in turn; for a K or V head of an 8-bit pool with blocks above kTile, all of the
-  // tile's chunks of kTile rows for the largest values and once more for the codes; else each chunk once.
-  struct Item {
-    int h, base;  // head, row at the chunk's first position
-    bool second;
-  };
-  const int c0 = t0 < tlo ? t0 + (tlo - t0) / kTile * kTile : t0;  // first chunk with a row of the CTA
-  const bool twice = kKv8 && a.tile > kTile;
-  auto next_item = [&](Item it) {
-    it.base += kTile;
-    if (it.base >= thi) {
-      it.base = c0;
-      const bool again = twice && it.h >= a.Hq && !it.second;
-      it.second = again;
-      it.h += again ? 0 : step;
-    }
-    return it;
-  };
-  uint4* ring = smem + warp * 2 * slotChunks;
-  const uint4* src = static_cast<const uint4*>(a.qkv) + static_cast<size_t>(b) * a.S * NH * LPR + lane % LPR;
-  auto copy = [&](const Item& it, int slot) {  // one copy group per item, empty past the last
-    if (it.h < NH) {
-      const int first = max(it.base, tlo), rows = min(thi, it.base + kTile) - first;
-      const uint4* g = src + (static_cast<size_t>(first + lane / LPR) * NH + it.h) * LPR;
-      const size_t hop = static_cast<size_t>(RPW) * NH * LPR;
-      uint4* d = ring + slot * slotChunks;
-      if (rows == kTile) {
-#pragma unroll
-        for (int i = 0; i < kTile / RPW; ++i)
-          cp_async16(smem_addr(d + place<D>(i * RPW + lane / LPR, lane % LPR)), g + i * hop, true);
-      } else {
-        for (int r = lane / LPR; r < rows; r += RPW, g += hop) cp_async16(smem_addr(d + place<D>(r, lane % LPR)), g, true);
-      }
-    }
-    cp_async_commit();
-  };
-  Item cur{static_cast<int>(blockIdx.y) * kWarps + warp, c0, false};
-  if (thi > tlo) copy(cur, 0);
-
-  const int hl = a.rot >> 4;  // chunks of half a rotation
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) w1[i / D][i % D] = 1.0f + __ldg((i < D ? a.qw : a.kw) + i % D);
-  for (int i = threadIdx.x; i < (thi - tlo) * 8 * hl; i += kThreads) {  // pairs of the live rows
-    const int r = i / (8 * hl), pair = i - r * 8 * hl;
-    float cv, sv;
-    rope_cos_sin_turns(static_cast<unsigned>(c + tlo + r), a.turn[pair], cv, sv);
-    const int e = pair & 7;
-    float* dst = reinterpret_cast<float*>(table + (r * 4 + (e >> 1)) * hl + (pair >> 3)) + (e & 1);
-    dst[0] = cv;
-    dst[2] = sv;
-  }
   // padding rows: zeros in the dense outputs, where the tile's lie together
   const int tpad = min(a.S, t0 + a.tile), tfirst = max(thi, tlo);
   if (tfirst < tpad) {
@@ -277,7 +223,64 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     pg[0] = __ldg(pt);
     pg[1] = __ldg(pt + a.maxPagesPerSeq);
   }
-  bool badPage = false;
+
+  // The work of a CTA, dealt to its warps one item at a time: a head and a group of its rows, `group` rows for a q head
+  // (any head of a 16-bit pool), kTile for a K or V head of an 8-bit pool.  Groups start at the tile's first position.
+  struct Item {
+    int h, first, rows;  // head, first live row, live rows
+  };
+  const int hs = kKv8 ? max(h0, min(a.Hq, h1)) : h1;  // heads [h0, hs) take groups of `group` rows, [hs, h1) of kTile
+  const int gq0 = (tlo - t0) / a.group, gq = (thi - t0 + a.group - 1) / a.group - gq0;
+  const int gk0 = (tlo - t0) / kTile, gk = (thi - t0 + kTile - 1) / kTile - gk0;
+  const int nq = (hs - h0) * gq, items = nq + (h1 - hs) * gk;
+  auto item_at = [&](int i) {
+    const bool q = i < nq;
+    const int per = q ? gq : gk, size = q ? a.group : kTile, k = q ? i : i - nq, h = k / per;
+    const int base = t0 + (k - h * per + (q ? gq0 : gk0)) * size, first = max(base, tlo);
+    return Item{(q ? h0 : hs) + h, first, min(thi, base + size) - first};
+  };
+  uint4* ring = smem + warp * 2 * slotChunks;
+  const uint4* src = static_cast<const uint4*>(a.qkv) +
+                     (static_cast<size_t>(b) * a.S + lane / LPR) * NH * LPR + lane % LPR;
+  auto copy = [&](const Item& it, int slot) {  // one copy group
+    const uint4* g = src + (static_cast<size_t>(it.first) * NH + it.h) * LPR;
+    const size_t hop = static_cast<size_t>(RPW) * NH * LPR;
+    uint4* d = ring + slot * slotChunks;
+    if (it.rows == kTile) {
+#pragma unroll
+      for (int i = 0; i < kTile / RPW; ++i)
+        cp_async16(smem_addr(d + place<D>(i * RPW + lane / LPR, lane % LPR)), g + i * hop, true);
+    } else {
+#pragma unroll 2
+      for (int r = lane / LPR; r < it.rows; r += RPW, g += hop)
+        cp_async16(smem_addr(d + place<D>(r, lane % LPR)), g, true);
+    }
+  };
+  const int begin = wide ? nq : 0;  // wide blocks: the K and V heads twice, first for their largest values
+  Item next{0, 0, 0};  // the item whose rows are in, or on their way to, ring slot `slot`
+  int slot = 0;
+  if (begin + warp < items) copy(next = item_at(begin + warp), 0);
+  cp_async_commit();
+
+  const int hl = a.rot >> 4;  // chunks of half a rotation
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) w1[i / D][i % D] = 1.0f + __ldg((i < D ? a.qw : a.kw) + i % D);
+  if (threadIdx.x == 0) identity = make_ulonglong2(pack_f2(1.f, 1.f), 0);
+  if (wide)
+    for (int i = threadIdx.x; i < h1 - hs; i += kThreads) blockMax[i] = 0;
+  if (h0 < a.Hq + a.Hkv)  // V heads need no table
+    for (int r = warp; r < thi - tlo; r += kWarps)
+      for (int pair = lane; pair < 8 * hl; pair += 32) {
+        // pos * turn mod 2^64 is the angle as an exact fraction of a turn; its top 32 bits, signed, are half turns * 2^31
+        const unsigned long long t = a.turn[pair] * static_cast<unsigned>(c + tlo + r);
+        float cv, sv;
+        sincospif(static_cast<float>(static_cast<int>(static_cast<unsigned>(t >> 32))) * 0x1p-31f, &sv, &cv);
+        const int e = pair & 7;
+        float* dst = reinterpret_cast<float*>(table + (r * 4 + (e >> 1)) * hl + (pair >> 3)) + (e & 1);
+        dst[0] = cv;
+        dst[2] = sv;
+      }
+
+  bool badPage = false;  // an id outside the pool: -1
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     if (static_cast<unsigned>(pg[i]) >= static_cast<unsigned>(a.numFlatPages)) {
@@ -290,155 +293,231 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   const int l = lane & (CPR - 1), sub = lane / CPR;
   const bool rotated = l < hl;
   const int ca = rotated ? l : hl + l, cb = rotated ? l + hl : l + CPR;  // this lane's chunks
+  const int csHop = rotated ? hl : 0;
   Chunks w;
-  int have = -1;        // whose weights w holds: 0 q heads, 1 k heads
-  float bm = 0.f;       // lanes 0..15, 8-bit: largest value of chunk position `lane` (of the whole block, above 16)
-  float rowInv = 0.f;   // lanes 0..15, 8-bit: 1 / scale at chunk position `lane`
-  for (int slot = 0; cur.h < NH; slot ^= 1) {
-    const Item nxt = next_item(cur);
-    copy(nxt, slot ^ 1);
-    cp_async_wait<1>();
-    __syncwarp();
-    const int h = cur.h, base = cur.base;
-    const int first = max(base, tlo), rows = min(thi, base + kTile) - first, off = first - base;
-    const bool isq = h < a.Hq, isv = h >= a.Hq + a.Hkv;
-    const int hk = isq ? h : (isv ? h - a.Hq - a.Hkv : h - a.Hq);  // among the q, k or v heads
-    const int pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
-    const uint4* buf = ring + slot * slotChunks;
-    if (!isv && have != (isq ? 0 : 1)) {
-      have = isq ? 0 : 1;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w.a[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * ca + 2 * k]);
-        w.b[k] = *reinterpret_cast<const uint64_t*>(&w1[have][8 * cb + 2 * k]);
-      }
+  int have = -1;  // whose weights w holds: 0 q heads, 1 k heads
+  // Calls f(r, raw chunks, values) for the lane's rows r of an item in a ring slot, all lanes alike (r past the last: no
+  // row, any values).
+  auto each_row = [&](const Item& it, int slot, auto norm, auto&& f) {
+    const uint4* pa = ring + slot * slotChunks + place<D>(sub, ca);  // RPI is even: the place moves evenly
+    const uint4* pb = ring + slot * slotChunks + place<D>(sub, cb);
+    const ulonglong2* cs = rotated ? table + (it.first - tlo + sub) * 4 * hl + l : &identity;
+    for (int r = sub; r - sub < it.rows; r += RPI, pa += RPI * LPR, pb += RPI * LPR, cs += RPI * 4 * csHop) {
+      const uint4 ra = *pa, rb = *pb;
+      Chunks y;
+      unpack8<kBf16>(ra, y.a);
+      unpack8<kBf16>(rb, y.b);
+      if constexpr (norm.value) norm_rotate<D, kBf16>(y, w, a.eps, cs, csHop);
+      f(r, ra, rb, y);
     }
-    // The lane's values of the chunk's r-th live row (r past the last: no row, anything).
-    auto value = [&](int r, uint4& rawa, uint4& rawb, Chunks& y) {
-      const int rc = min(r, rows - 1);
-      rawa = buf[place<D>(rc, ca)];
-      rawb = buf[place<D>(rc, cb)];
-      unpack8<kBf16>(rawa, y.a);
-      unpack8<kBf16>(rawb, y.b);
-      if (!isv) norm_rotate<D, kBf16>(y, w, a.eps, rotated, table + (first - tlo + rc) * 4 * hl + l, hl);
+  };
+  using Norm = std::integral_constant<bool, true>;
+  using Copy = std::integral_constant<bool, false>;
+  // Largest value of row position `lane` of a K or V item's group (0 for none), over all of a block's rows in it.
+  auto row_maxima = [&](const Item& it, int slot, bool isv) {
+    const int off = (it.first - t0) & (kTile - 1);
+    float rm = 0.f;
+    auto take = [&](int r, const uint4&, const uint4&, const Chunks& y) {
+      float m = fmaxf(finite_max(y.a), finite_max(y.b));
+#pragma unroll
+      for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      const int mine = lane - off - (r - sub);  // lane's row among these
+      m = __shfl_sync(kFull, m, (mine & (RPI - 1)) * CPR);
+      if (mine >= 0 && mine < RPI && lane - off < it.rows) rm = m;
     };
-
-    if (kKv8 && !isq && !cur.second) {  // the largest value of each row, then of each block
-      float rm = 0.f;
-      for (int i = 0; i * RPI < rows; ++i) {
-        uint4 ra, rb;
-        Chunks y;
-        value(i * RPI + sub, ra, rb, y);
-        float m = fmaxf(finite_max(y.a), finite_max(y.b));
+    if (isv)
+      each_row(it, slot, Copy{}, take);
+    else
+      each_row(it, slot, Norm{}, take);
+    for (int o = 1; o < min(1 << a.blockShift, kTile); o <<= 1) rm = fmaxf(rm, __shfl_xor_sync(kFull, rm, o));
+    return rm;
+  };
+  // The scale of a block whose first position is row tb, for a head's largest new value bm: `kept` is its stored scale,
+  // read only if it holds older tokens.  Those keep their scale, or grow it by the smallest power of two that fits.
+  auto new_scale = [&](int tb, float bm, const float* kept, float& shrink) {
+    shrink = 1.f;
+    if (tb >= 0) return fminf(fmaxf(__fdiv_rn(bm, kE4m3Max), kScaleLo), kScaleHi);
+    const float was = read_scale(*kept);
+    const float over = __fdiv_rn(bm, kE4m3Max * was);
+    if (!(over > 1.f)) return was;
+    const int bits = __float_as_int(over);
+    const float now = fminf(ldexpf(was, (bits >> 23) - 127 + ((bits & 0x7fffff) ? 1 : 0)), kScaleHi);
+    shrink = was / now;
+    return now;
+  };
+  auto scale_at = [&](int pageId, int tb, int hk) {
+    return a.scale +
+           ((static_cast<size_t>(pageId) << (7 - a.blockShift)) + (((c + tb) & 127) >> a.blockShift)) * a.Hkv + hk;
+  };
+  // Older rows of the block that starts in front of row 0, divided by 2^k (a warp's work).
+  auto shrink_older = [&](int pageId, int hk, float f) {
+    for (int p = (c & ~((1 << a.blockShift) - 1)) + lane / LPR; p < c; p += RPW) {
+      uint2* row = reinterpret_cast<uint2*>(
+                       a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + (p & 127)) * a.Hkv + hk) * a.poolHeadDim) +
+                   lane % LPR;
+      *row = rescale8(*row, f);
+    }
+  };
+  auto weights = [&](int which) {
+    if (have == which) return;
+    have = which;
 #pragma unroll
-        for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        const int r = lane - off - i * RPI;  // lane's row among these
-        m = __shfl_sync(kFull, m, (r & (RPI - 1)) * CPR);
-        if (r >= 0 && r < RPI && lane - off < rows) rm = m;
-      }
-      const int sb = 1 << a.blockShift;
-      for (int o = 1; o < min(sb, kTile); o <<= 1) rm = fmaxf(rm, __shfl_xor_sync(kFull, rm, o));
-      bm = base == c0 ? rm : fmaxf(bm, rm);
-      if (base + kTile >= thi) {  // every row is in: the scale of this lane's block
-        const int rr = lane & (kTile - 1);
-        const int tb = t0 + (twice ? 0 : rr & ~(sb - 1));  // row at the block's first position
-        const bool fill = max(tb, tlo) < min(tb + sb, thi) && pageId >= 0;
-        float* sp = a.scale +
-                    ((static_cast<size_t>(fill ? pageId : 0) << (7 - a.blockShift)) +
-                     (fill ? ((c + tb) & 127) >> a.blockShift : 0)) * a.Hkv + hk;
-        float now = 1.f, shrink = 1.f;
-        if (fill) {
-          if (tb < 0) {  // older tokens: keep their scale, or grow it by the smallest power of two that fits
-            const float kept = read_scale(*sp);
-            const float over = __fdiv_rn(bm, kE4m3Max * kept);
-            now = kept;
-            if (over > 1.f) {
-              const int bits = __float_as_int(over);
-              const int k = (bits >> 23) - 127 + ((bits & 0x7fffff) ? 1 : 0);
-              now = fminf(ldexpf(kept, k), kScaleHi);
-              shrink = kept / now;
-            }
-          } else {
-            now = fminf(fmaxf(__fdiv_rn(bm, kE4m3Max), kScaleLo), kScaleHi);
-          }
-        }
-        __syncwarp();  // every lane of a block has read its scale
-        if (fill && (twice ? lane == 0 : lane < kTile && (rr & (sb - 1)) == 0)) *sp = now;
-        rowInv = 1.0f / now;
-        // older rows of the grown block (at most one block of the tile holds older tokens)
-        const float f = __shfl_sync(kFull, shrink, twice || t0 >= 0 ? 0 : (-t0) & ~(sb - 1));
-        if (t0 < 0 && f != 1.f && pageId >= 0)
-          for (int p = (c & ~(sb - 1)) + lane / LPR; p < c; p += RPW) {
-            uint2* row = reinterpret_cast<uint2*>(
-                             a.pool + ((static_cast<size_t>(pageId) * kTokensPerPage + (p & 127)) * a.Hkv + hk) *
-                                          a.poolHeadDim) + lane % LPR;
-            *row = rescale8(*row, f);
-          }
-      }
+    for (int k = 0; k < 4; ++k) {
+      w.a[k] = *reinterpret_cast<const uint64_t*>(&w1[which][8 * ca + 2 * k]);
+      w.b[k] = *reinterpret_cast<const uint64_t*>(&w1[which][8 * cb + 2 * k]);
     }
+  };
 
-    if (!kKv8 || isq || !twice || cur.second) {
-      uint4* dense = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
-      const int heads = isq ? a.Hq : a.Hkv;
-      if (dense) dense += ((static_cast<size_t>(b) * a.S + first + sub) * heads + hk) * LPR;
-      constexpr int kElem = kKv8 ? 1 : 2;
-      const size_t rowBytes = static_cast<size_t>(a.Hkv) * a.poolHeadDim * kElem;
-      uint8_t* prow = pageId < 0 ? nullptr
-                                 : a.pool + (static_cast<size_t>(pageId) * kTokensPerPage + ((c + first) & 127) + sub) * rowBytes +
-                                       static_cast<size_t>(hk) * a.poolHeadDim * kElem;
-#pragma unroll 2
-      for (int i = 0; i * RPI < rows; ++i) {
-        const int r = i * RPI + sub;
-        uint4 ra, rb;
-        Chunks y;
-        value(r, ra, rb, y);
-        const float qs = kKv8 && !isq ? __shfl_sync(kFull, rowInv, (off + r) & (kTile - 1)) : 0.f;
-        if (r < rows) {
-          if (!isv && (dense || !kKv8)) {
-            ra = pack8<kBf16>(y.a);
-            rb = pack8<kBf16>(y.b);
-          }
-          if (dense) {
-            dense[ca] = ra;
-            dense[cb] = rb;
-          }
-          if (prow) {
-            if constexpr (kKv8) {
-              reinterpret_cast<uint2*>(prow)[ca] = quantise8(y.a, qs);
-              reinterpret_cast<uint2*>(prow)[cb] = quantise8(y.b, qs);
-            } else {
-              reinterpret_cast<uint4*>(prow)[ca] = ra;
-              reinterpret_cast<uint4*>(prow)[cb] = rb;
-            }
-          }
-        }
-        if (dense) dense += static_cast<size_t>(RPI) * heads * LPR;
-        if (prow) prow += RPI * rowBytes;
-      }
+  // Runs over this warp's items from `from` on, each with the next one's rows on their way (after the last, item
+  // `then`'s, if there is one).
+  auto run = [&](int from, int then, auto&& f) {
+    for (int i = from + warp; i < items; i += kWarps, slot ^= 1) {
+      const Item it = next;
+      const int after = i + kWarps < items ? i + kWarps : then;
+      if (after >= 0 && after < items) copy(next = item_at(after), slot ^ 1);
+      cp_async_commit();
+      cp_async_wait<1>();
+      __syncwarp();
+      f(it);
+      __syncwarp();  // every lane is done with the slot
     }
-    __syncwarp();  // every lane is done with the slot
-    cur = nxt;
+  };
+
+  if (wide) {
+    run(begin, warp, [&](const Item& it) {
+      const bool isv = it.h >= a.Hq + a.Hkv;
+      if (!isv) weights(1);
+      const float rm = row_maxima(it, slot, isv);
+      if (lane == 0) atomicMax(&blockMax[it.h - hs], __float_as_int(rm));  // of numbers >= 0: whole-number order is theirs
+    });
+    if (begin + warp >= items && warp < items) {  // a warp without such items has not copied its first yet
+      copy(next = item_at(warp), slot);
+      cp_async_commit();
+    }
+    __syncthreads();
+    for (int i = warp; i < h1 - hs; i += kWarps) {
+      const int h = hs + i;
+      const bool isv = h >= a.Hq + a.Hkv;
+      const int hk = isv ? h - a.Hq - a.Hkv : h - a.Hq, pageId = isv ? pg[1] : pg[0];
+      if (pageId < 0) continue;
+      float* sp = scale_at(pageId, t0, hk);
+      float f;
+      const float now = new_scale(t0, __int_as_float(blockMax[i]), sp, f);
+      __syncwarp();  // every lane has read the stored scale
+      if (lane == 0) {
+        *sp = now;
+        blockInv[i] = 1.0f / now;
+      }
+      if (f != 1.f) shrink_older(pageId, hk, f);
+    }
+    __syncthreads();
   }
+
+  run(0, -1, [&](const Item& it) {
+    const bool isq = it.h < a.Hq, isv = it.h >= a.Hq + a.Hkv;
+    const int hk = isq ? it.h : (isv ? it.h - a.Hq - a.Hkv : it.h - a.Hq);  // among the q, k or v heads
+    const int heads = isq ? a.Hq : a.Hkv, pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
+    constexpr int kElem = kKv8 ? 1 : 2;
+    const size_t rowBytes = static_cast<size_t>(a.Hkv) * a.poolHeadDim * kElem, denseRow = static_cast<size_t>(heads) * LPR;
+    uint4* dense = static_cast<uint4*>(isq ? a.qout : (isv ? a.vout : a.kout));
+    if (dense) dense += (static_cast<size_t>(b) * a.S + it.first) * denseRow + hk * LPR;
+    uint8_t* prow = pageId < 0 ? nullptr
+                               : a.pool + (static_cast<size_t>(pageId) * kTokensPerPage + ((c + it.first) & 127)) * rowBytes +
+                                     static_cast<size_t>(hk) * a.poolHeadDim * kElem;
+    if (!isv) weights(isq ? 0 : 1);
+    if (!kKv8 || isq) {
+      auto put = [&](int r, const uint4& ra, const uint4& rb) {
+        if (r >= it.rows) return;
+        if (dense) {
+          uint4* d = dense + r * denseRow;
+          d[ca] = ra;
+          d[cb] = rb;
+        }
+        if (!kKv8 && prow) {
+          uint4* d = reinterpret_cast<uint4*>(prow + r * rowBytes);
+          d[ca] = ra;
+          d[cb] = rb;
+        }
+      };
+      if (!kKv8 && isv)
+        each_row(it, slot, Copy{}, [&](int r, const uint4& ra, const uint4& rb, const Chunks&) { put(r, ra, rb); });
+      else
+        each_row(it, slot, Norm{}, [&](int r, const uint4&, const uint4&, const Chunks& y) {
+          put(r, pack8<kBf16>(y.a), pack8<kBf16>(y.b));
+        });
+      return;
+    }
+    if constexpr (kKv8) {
+      const int off = (it.first - t0) & (kTile - 1);
+      float rowInv = 0.f;  // 1 / scale at row position `lane` of the group
+      if (wide) {
+        rowInv = blockInv[it.h - hs];
+      } else {
+        const float bm = row_maxima(it, slot, isv);
+        const int sb = 1 << a.blockShift, rr = lane & (kTile - 1);
+        const int tb = t0 + (rr & ~(sb - 1));  // row at the first position of this lane's block
+        const bool fill = lane < kTile && max(tb, tlo) < min(tb + sb, thi) && pageId >= 0;
+        float* sp = scale_at(fill ? pageId : 0, fill ? tb : 0, hk);
+        float now = 1.f, f = 1.f;
+        if (fill) now = new_scale(tb, bm, sp, f);
+        __syncwarp();  // every lane of a block has read its scale
+        if (fill && (rr & (sb - 1)) == 0) *sp = now;
+        rowInv = 1.0f / now;
+        f = __shfl_sync(kFull, f, t0 < 0 ? (-t0) & ~(sb - 1) : 0);  // of the block that holds row 0
+        if (t0 < 0 && f != 1.f && pageId >= 0) shrink_older(pageId, hk, f);
+      }
+      auto put = [&](int r, const uint4& ra, const uint4& rb, const Chunks& y) {
+        const float qs = __shfl_sync(kFull, rowInv, (off + r) & (kTile - 1));
+        if (r >= it.rows) return;
+        if (dense) {
+          uint4* d = dense + r * denseRow;
+          d[ca] = isv ? ra : pack8<kBf16>(y.a);
+          d[cb] = isv ? rb : pack8<kBf16>(y.b);
+        }
+        if (prow) {
+          uint2* d = reinterpret_cast<uint2*>(prow + r * rowBytes);
+          d[ca] = quantise8(y.a, qs);
+          d[cb] = quantise8(y.b, qs);
+        }
+      };
+      if (isv)
+        each_row(it, slot, Copy{}, put);
+      else
+        each_row(it, slot, Norm{}, put);
+    }
+  });
   cp_async_wait<0>();  // the last groups are empty; nothing is in flight at exit
 }
 
 template <int D, bool kBf16, bool kKv8>
-cudaError_t append_go(const AppendArgs& a, int B, cudaStream_t st) {
+cudaError_t append_go(AppendArgs a, int B, cudaStream_t st) {
   auto kernel = append_kv_kernel<D, kBf16, kKv8>;
-  // the warps' rings, and the table of 8 bytes per row and rotated pair: at most 64 KB each
+  constexpr int RPI = 512 / D;  // rows a warp computes at once
+  const int NH = a.Hq + 2 * a.Hkv, sms = sm_count();
+  const long long tiles = static_cast<long long>(B) * a.tiles;
+  const int rows = std::min(a.tile, a.S);  // most live rows of a tile
+  // Groups of kTile rows when that gives every resident warp one; else the fewest rows that fill a warp, so that a small
+  // call's rows run side by side.
+  const long long warps = static_cast<long long>(kCtasPerSm) * kWarps * sms;
+  a.group = tiles * NH * ((rows + kTile - 1) / kTile) >= warps ? kTile : RPI;
+  // One CTA per tile when the tiles fill the GPU; otherwise a tile's heads are dealt out to as many CTAs as are resident
+  // at once, down to one item per warp.  (A second wave repeats the tile's table and waits: 4 x 1000 rows took 20.1 us
+  // with four CTAs' worth of parts per SM, 14.5 us with one wave.)
+  const int perHead = (rows + a.group - 1) / a.group;
+  const int most = std::max(1, (NH * perHead + kWarps - 1) / kWarps);
+  int parts = static_cast<int>(std::min<long long>({most, NH, std::max<long long>(1, kCtasPerSm * sms / tiles)}));
+  if (kKv8 && a.tile > kTile) parts = std::max(parts, (NH + kMaxWideHeads - 1) / kMaxWideHeads);
+  a.headsPerCta = (NH + parts - 1) / parts;
+  parts = (NH + a.headsPerCta - 1) / a.headsPerCta;
+  // the warps' rings, and the table of 8 bytes per row and rotated pair (one access of RPI rows past its end)
+  a.slotRows = (std::min(kTile, a.S) + RPI - 1) / RPI * RPI;
   const size_t smem = kWarps * 2 * static_cast<size_t>(a.slotRows) * (D * 2) +
-                      static_cast<size_t>(std::min(a.tile, a.S)) * (a.rot / 2) * 8;
-  if (smem > 40 * 1024) {  // past what a kernel may have without asking (48 KB, w1 among it)
+                      static_cast<size_t>(rows + RPI) * (a.rot / 2) * 8;
+  if (smem > 40 * 1024) {  // past what a kernel may have without asking (48 KB, the static arrays among it)
     const cudaError_t attr =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (attr != cudaSuccess) return attr;
   }
-  // One CTA per tile when the tiles fill the GPU a few times over; otherwise the heads of a tile are dealt
-  // out to several CTAs, down to one head per warp.
-  const long long tiles = static_cast<long long>(B) * a.tiles;
-  const int most = (a.Hq + 2 * a.Hkv + kWarps - 1) / kWarps;
-  const long long want = 4LL * sm_count();
-  const int parts = static_cast<int>(std::min<long long>(most, std::max<long long>(1, (want + tiles - 1) / tiles)));
   kernel<<<dim3(static_cast<unsigned>(tiles), parts), kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -477,7 +556,6 @@ cudaError_t launch_append_kv(const QsaAppendKvParams& p, const RopeFreqs& rf, bo
   a.tile = std::max(kTile, p.scaleBlock);
   // the most aligned tiles that seqLen consecutive positions touch
   a.tiles = static_cast<int>((static_cast<long long>(p.seqLen) + a.tile - 2) / a.tile + 1);
-  a.slotRows = std::min(kTile, p.seqLen);
   a.eps = p.rmsNormEps;
   for (int i = 0; i < 64; ++i) a.turn[i] = rf.turn[i];
   cudaStream_t st = static_cast<cudaStream_t>(p.stream);
