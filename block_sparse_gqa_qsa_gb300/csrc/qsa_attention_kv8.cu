@@ -20,11 +20,13 @@
 // cp.async into its own K tile and V tile.  A step's K tile is free after its
 // first product, its V tile after the second, and the next step's rows start
 // then: one tile of each keeps half a step of copies in flight per warp.
-// S^T = C^K Q^T and O^T += (C^V)^T P^T are m16n8k16 MMAs with the head group as
-// N.  The summed dims of the first and the output dims of the second may be
-// permuted freely, so a lane reads its codes as whole 16-byte chunks and
-// converts them to fp16 pairs in registers (exact), for V after interleaving
-// the bytes of two keys.
+//
+// S^T = C^K Q^T and O^T += (C^V)^T P^T are m16n8k16 MMAs in fp16 with the head
+// group as N; codes are converted to fp16 pairs in registers (exact).  The
+// summed dims of the first are permuted so that a lane reads its K codes as
+// whole 16-byte chunks; for the second, ldmatrix transposes 16 x 16 bytes, so
+// a register holds four keys of one dim.  The rows of S^T are the keys in the
+// order that makes its columns the second product's fragments of P^T.
 #include <algorithm>
 #include <cfloat>
 #include <utility>
@@ -95,10 +97,12 @@ __device__ __forceinline__ uint2 pack4(float4 v) {
                : make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
 }
 
-// Byte offset of 16-byte chunk c of key row r in a step's K tile (a lane group reads chunks 0..3 or 4..7 of
-// two neighbouring rows) and V tile (chunks 0, 1 of rows 0, 2, 4, 6): each access covers all banks once.
+// Byte offset of 16-byte chunk c of key row r in a step's K tile (a lane group reads chunks 0..3 or 4..7 of two rows of
+// different parity) and V tile (ldmatrix reads one chunk of 8 successive rows): each access covers all banks once.
 __device__ __forceinline__ uint32_t k_off(int r, int c) { return r * kD + ((c ^ ((r & 1) << 2)) << 4); }
-__device__ __forceinline__ uint32_t v_off(int r, int c) { return r * kD + ((c ^ (r & 6)) << 4); }
+__device__ __forceinline__ uint32_t v_off(int r, int c) { return r * kD + ((c ^ (r & 7)) << 4); }
+// Key of row g of an S^T fragment (row g + 8: two keys on), within its 16 keys.
+__device__ __forceinline__ int key_of(int g) { return 4 * (g >> 1) + (g & 1); }
 
 // 16-byte copy to dst + kOff.
 template <int kOff>
@@ -142,8 +146,16 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// Two transposed 16 x 16 byte matrices (rows at the addresses of lanes 0..15 and 16..31): of each, the lane gets rows
+// 4 q .. 4 q + 3 of column g, then of column g + 8.
+__device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
 // A warp's running state: O^T fragments, max and sum of its heads 8 nt + 2 q, 8 nt + 2 q + 1 (q = lane & 3).
-// Tile mt holds dims 16 g + 2 mt (rows g) and 16 g + 2 mt + 1 (rows g + 8), g = lane >> 2.
+// Tile mt holds dims 16 mt + g and 16 mt + g + 8, g = lane >> 2.
 template <int NT>
 struct Acc {
   float o[8][NT][4];
@@ -151,18 +163,18 @@ struct Acc {
   float l[NT][2];
 };
 
-// S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + g and + 8, heads 8 nt + 2 q and + 1.
+// S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + key_of(g) and 2 on, heads 8 nt + 2 q and + 1.
 template <int NT>
 __device__ __forceinline__ void scores32(float (&s)[2][NT][4], uint32_t tile, const uint32_t (&qf)[NT][8][2]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int lane = threadIdx.x & 31, key = key_of(lane >> 2), q = lane & 3;
 #pragma unroll
   for (int gk = 0; gk < 2; ++gk) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s[gk][nt][0] = s[gk][nt][1] = s[gk][nt][2] = s[gk][nt][3] = 0.f;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint4 r0 = lds16(tile + k_off(16 * gk + g, q + 4 * half));
-      const uint4 r1 = lds16(tile + k_off(16 * gk + g + 8, q + 4 * half));
+      const uint4 r0 = lds16(tile + k_off(16 * gk + key, q + 4 * half));
+      const uint4 r1 = lds16(tile + k_off(16 * gk + key + 2, q + 4 * half));
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a[4];
@@ -185,11 +197,11 @@ template <int NT, bool kBf16>
 __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], const float (&qs)[NT][2],
                                           const float4* entries, uint32_t (&pb)[2][NT][2]) {
   constexpr float kHeadroom = 8.f;
-  const int lane = threadIdx.x & 31, g = lane >> 2;
-  float ks[4], lv[4], iv[4];  // of keys g, g + 8, g + 16, g + 24
+  const int key = key_of((threadIdx.x & 31) >> 2);
+  float ks[4], lv[4], iv[4];  // of the lane's keys
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 e = entries[g + 8 * i];
+    const float4 e = entries[key + 16 * (i >> 1) + 2 * (i & 1)];
     ks[i] = e.x;
     lv[i] = e.y;
     iv[i] = e.z;
@@ -257,22 +269,19 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 // O^T += (C^V)^T P^T.
 template <int NT>
 __device__ __forceinline__ void values32(Acc<NT>& A, uint32_t tile, const uint32_t (&pb)[2][NT][2]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const uint32_t row = tile + v_off(threadIdx.x & 31, 0);
 #pragma unroll
-  for (int gk = 0; gk < 2; ++gk) {
-    const uint4 va = lds16(tile + v_off(16 * gk + 2 * q, g)), vb = lds16(tile + v_off(16 * gk + 2 * q + 1, g));
-    const uint4 vc = lds16(tile + v_off(16 * gk + 2 * q + 8, g)), vd = lds16(tile + v_off(16 * gk + 2 * q + 9, g));
+  for (int mt = 0; mt < 8; ++mt) {
+    uint32_t r[4];
+    ldsm_bytes_t(row ^ (mt << 4), r);
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int gk = 0; gk < 2; ++gk) {
+      uint32_t a[4];
+      e4m3_to_f16(r[2 * gk], a[0], a[2]);
+      e4m3_to_f16(r[2 * gk + 1], a[1], a[3]);
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {  // dims 16 g + 4 w + 2 d and the next one
-        const uint32_t sel = d ? 0x7362 : 0x5140;
-        uint32_t a[4];
-        e4m3_to_f16(__byte_perm(word(va, w), word(vb, w), sel), a[0], a[1]);
-        e4m3_to_f16(__byte_perm(word(vc, w), word(vd, w), sel), a[2], a[3]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(A.o[2 * w + d][nt], a, pb[gk][nt][0], pb[gk][nt][1]);
-      }
+      for (int nt = 0; nt < NT; ++nt) mma16816(A.o[mt][nt], a, pb[gk][nt][0], pb[gk][nt][1]);
+    }
   }
 }
 
@@ -320,13 +329,15 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
   }
 }
 
+constexpr int kPad = kD + 4;  // floats of a head in the merge buffers
+
 // Resident CTAs per SM: the register budget (128 or 168 a thread) decides.
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 4 : 3;
 // The tiles, and later the merge buffers: the warps' O, m and l, then the CTA's.
 template <int NT>
-constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kD + 2) * 4 ? kWarps * kWarpBytes
-                                                                               : (kWarps + 1) * 8 * NT * (kD + 2) * 4;
+constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kPad + 2) * 4 ? kWarps * kWarpBytes
+                                                                               : (kWarps + 1) * 8 * NT * (kPad + 2) * 4;
 
 template <int NT, bool kBf16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_kernel(const PagedArgs a) {
@@ -461,15 +472,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
   if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
   __syncthreads();  // the rings become the merge buffers
 
-  // Per warp [8 NT heads][128 dims] fp32 and (m, l); 16-byte units of a head XOR-swizzled by its pair index, so
-  // that both the writes below and the row-wise reads are free of bank conflicts.
+  // Per warp [8 NT heads][128 dims, padded] fp32 and (m, l).  kPad puts a fragment's writes in different banks.
   constexpr int H = 8 * NT;
-  float4* ow = reinterpret_cast<float4*>(smem);                  // [kWarps][H][32]
-  float* mw = reinterpret_cast<float*>(ow + kWarps * H * 32);    // [kWarps][H]
+  float* ow = reinterpret_cast<float*>(smem);   // [kWarps][H][kPad]
+  float* oc = ow + kWarps * H * kPad;           // the CTA's merged [H][kPad]
+  float* mw = oc + H * kPad;                    // [kWarps][H]
   float* lw = mw + kWarps * H;
-  float4* oc = reinterpret_cast<float4*>(lw + kWarps * H);       // the CTA's merged [H][32], in plain order
-  float* mc = reinterpret_cast<float*>(oc + H * 32);
-  float* lc = mc + H;
+  float* mc = lw + kWarps * H;                  // [H], then the sums
   const int g = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -485,9 +494,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
         lw[warp * H + h] = l;
       }
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        ow[(warp * H + h) * 32 + 4 * g + (w ^ q)] = make_float4(A.o[2 * w][nt][j], A.o[2 * w][nt][2 + j],
-                                                               A.o[2 * w + 1][nt][j], A.o[2 * w + 1][nt][2 + j]);
+      for (int mt = 0; mt < 8; ++mt) {
+        ow[(warp * H + h) * kPad + 16 * mt + g] = A.o[mt][nt][j];
+        ow[(warp * H + h) * kPad + 16 * mt + g + 8] = A.o[mt][nt][2 + j];
+      }
     }
   __syncthreads();
   for (int h = warp; h < a.G; h += kWarps) {
@@ -498,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = exp2f(mw[w * H + h] - M);
-      const float4 x = ow[(w * H + h) * 32 + (lane ^ ((h >> 1) & 3))];
+      const float4 x = *reinterpret_cast<const float4*>(ow + (w * H + h) * kPad + 4 * lane);
       l += f * lw[w * H + h];
       o.x += f * x.x;
       o.y += f * x.y;
@@ -506,10 +516,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
       o.w += f * x.w;
     }
     if (a.split > 1) {
-      oc[h * 32 + lane] = o;
+      *reinterpret_cast<float4*>(oc + h * kPad + 4 * lane) = o;
       if (lane == 0) {
         mc[h] = M;
-        lc[h] = l;
+        mc[H + h] = l;
       }
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
     for (int r = 0; r < kMaxCluster; ++r)
       if (r < a.split) {
         const float f = exp2f(ms[r] - M);
-        const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * 32 + lane) * 16, r));
+        const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * kPad + 4 * lane) * 4, r));
         l += f * cluster_ld(cluster_addr(mcAddr + (H + h) * 4, r));
         o.x += f * x.x;
         o.y += f * x.y;
