@@ -428,10 +428,12 @@ def sparse_decode_noalloc(q, pool, page_table, indices, ctx, out, *, D, scale, s
 
 # -------------------------------------------------------------- paged cache
 # A decode step calls these once per layer, and its kernels take a few microseconds, so the host side is kept
-# short: one check per tensor, the params packed in one go (same layout as the ctypes structs above).
+# short: the checks of all tensors in one expression (`_arg` names the culprit when it fails), the params packed
+# in one go (same layout as the ctypes structs above).
 _APPEND_PACK = struct.Struct("@12P10i2fP")
 _PAGED_PACK = struct.Struct("@8P10ifPP")
 _packed_calls = {}
+_F32, _I32, _F16, _BF16, _E4M3 = torch.float32, torch.int32, torch.float16, torch.bfloat16, torch.float8_e4m3fn
 
 
 def _packed(name: str):
@@ -459,55 +461,62 @@ def _raw_stream(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
-def _current_device(*tensors) -> int:
-    """The current CUDA device; refuses CPU tensors before anything touches CUDA."""
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-    return torch.cuda.current_device()
+def _current_device(t: torch.Tensor) -> int:
+    """The current CUDA device; refuses a CPU tensor before anything touches CUDA."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return torch._C._cuda_getDevice()
 
 
-def _append(name, qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
+def _append(name, fn, qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
             v_out, status, stream):
     et = qkv.dtype
-    bf16 = et is torch.bfloat16
-    if not bf16 and et is not torch.float16:
+    bf16 = et is _BF16
+    if not bf16 and et is not _F16:
         raise ValueError(f"{name}: qkv must be float16 or bfloat16")
-    if qkv.dim() != 4 or pool.dim() != 4 or page_table.dim() != 3:
-        raise ValueError(f"{name}: qkv and pool have 4 dimensions, page_table 3")
-    B, S, NH, D = qkv.shape
-    nflat, tpp, ph, phd = pool.shape
-    ptb, two, pages = page_table.shape
+    try:
+        B, S, NH, D = qkv.shape
+        nflat, tpp, ph, phd = pool.shape
+        ptb, two, pages = page_table.shape
+    except ValueError:
+        raise ValueError(f"{name}: qkv and pool have 4 dimensions, page_table 3") from None
     if NH != Hq + 2 * Hkv or q_out.shape != (B, S, Hq, D) or wq.shape != (D,) or wk.shape != (D,) or \
             ctx.shape != (B,) or tpp != 128 or ph != Hkv or ptb != B or two != 2:
         raise ValueError(f"{name}: shape mismatch")
-    for t in (k_out, v_out):
-        if t is not None and t.shape != (B, S, Hkv, D):
-            raise ValueError(f"{name}: k_out/v_out shape mismatch")
+    if (k_out is not None and k_out.shape != (B, S, Hkv, D)) or (v_out is not None and v_out.shape != (B, S, Hkv, D)):
+        raise ValueError(f"{name}: k_out/v_out shape mismatch")
     if new_lengths is not None and new_lengths.shape != (B,):
         raise ValueError(f"{name}: new_lengths must have shape ({B},)")
-    block = 0
+    block, pt = 0, et
     if scale is not None:
         if scale.dim() != 3 or scale.shape[0] != nflat or scale.shape[2] != Hkv or scale.shape[1] < 1 or \
                 128 % scale.shape[1]:
             raise ValueError(f"{name}: scale must be [{nflat}, 128 / block, {Hkv}]")
-        block = 128 // scale.shape[1]
+        block, pt = 128 // scale.shape[1], _E4M3
     dev = _current_device(qkv)
-    f32, i32 = torch.float32, torch.int32
+    if wq.dtype is not _F32 or wk.dtype is not _F32 or ctx.dtype is not _I32 or q_out.dtype is not et or \
+            pool.dtype is not pt or page_table.dtype is not _I32 or \
+            not (qkv.get_device() == wq.get_device() == wk.get_device() == ctx.get_device() == q_out.get_device() ==
+                 pool.get_device() == page_table.get_device() == dev) or \
+            not (qkv.is_contiguous() and wq.is_contiguous() and wk.is_contiguous() and ctx.is_contiguous() and
+                 q_out.is_contiguous() and pool.is_contiguous() and page_table.is_contiguous()):
+        for t, d, n in ((qkv, et, "qkv"), (wq, _F32, "qNormW"), (wk, _F32, "kNormW"), (ctx, _I32, "contextLengths"),
+                        (q_out, et, "q_out"), (pool, pt, "pool"), (page_table, _I32, "pageTable")):
+            _arg(t, d, n, dev)
     packed = _APPEND_PACK.pack(
-        _arg(qkv, et, "qkv", dev), _arg(wq, f32, "qNormW", dev), _arg(wk, f32, "kNormW", dev),
-        _arg(ctx, i32, "contextLengths", dev), _arg(new_lengths, i32, "new_lengths", dev),
-        _arg(q_out, et, "q_out", dev), _arg(k_out, et, "k_out", dev), _arg(v_out, et, "v_out", dev),
-        _arg(pool, et if scale is None else torch.float8_e4m3fn, "pool", dev), _arg(scale, f32, "scale", dev),
-        _arg(page_table, i32, "pageTable", dev), _arg(status, i32, "status", dev), B, S, Hq, Hkv, D, rot, phd, nflat,
-        pages, block, theta, eps, _raw_stream(stream, dev))
-    r = _packed(_APPEND_NAMES[name, bf16])(packed)
+        qkv.data_ptr(), wq.data_ptr(), wk.data_ptr(), ctx.data_ptr(),
+        0 if new_lengths is None else _arg(new_lengths, _I32, "new_lengths", dev), q_out.data_ptr(),
+        0 if k_out is None else _arg(k_out, et, "k_out", dev), 0 if v_out is None else _arg(v_out, et, "v_out", dev),
+        pool.data_ptr(), 0 if scale is None else _arg(scale, _F32, "scale", dev), page_table.data_ptr(),
+        0 if status is None else _arg(status, _I32, "status", dev), B, S, Hq, Hkv, D, rot, phd, nflat, pages, block, theta,
+        eps, _raw_stream(stream, dev))
+    r = _packed(fn[bf16])(packed)
     if r:
         _check(r)
 
 
-_APPEND_NAMES = {(n, b): "qsa_" + n + ("_bf16" if b else "") for n in ("append_kv", "append_kv8")
-                 for b in (False, True)}
+_APPEND_KV = ("qsa_append_kv", "qsa_append_kv_bf16")
+_APPEND_KV8 = ("qsa_append_kv8", "qsa_append_kv8_bf16")
 
 
 def append_kv(qkv, wq, wk, ctx, q_out, pool, page_table, *, Hq, Hkv, rot, theta, eps, new_lengths=None, k_out=None,
@@ -516,7 +525,7 @@ def append_kv(qkv, wq, wk, ctx, q_out, pool, page_table, *, Hq, Hkv, rot, theta,
     at their positions: q_out [B,S,Hq,D], the K/V rows of pool [numFlat,128,Hkv,poolHeadDim] (qkv's type) through
     page_table [B,2,pages], and optional dense mirrors k_out / v_out [B,S,Hkv,D].  ctx int32 [B] holds total lengths,
     new_lengths int32 [B] how many of them are new (None: min(S, ctx))."""
-    _append("append_kv", qkv, wq, wk, ctx, q_out, pool, None, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
+    _append("append_kv", _APPEND_KV, qkv, wq, wk, ctx, q_out, pool, None, page_table, Hq, Hkv, rot, theta, eps, new_lengths, k_out,
             v_out, status, stream)
 
 
@@ -526,7 +535,7 @@ def append_kv8(qkv, wq, wk, ctx, q_out, pool, scale, page_table, *, Hq, Hkv, rot
     [numFlat,128,Hkv,poolHeadDim] with scale float32 [numFlat,128/block,Hkv], one per block of tokens and head."""
     if scale is None:
         raise ValueError("append_kv8: scale is missing")
-    _append("append_kv8", qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths,
+    _append("append_kv8", _APPEND_KV8, qkv, wq, wk, ctx, q_out, pool, scale, page_table, Hq, Hkv, rot, theta, eps, new_lengths,
             k_out, v_out, status, stream)
 
 
@@ -536,28 +545,36 @@ def sparse_paged_kv8(q, pool, kv_scale, page_table, indices, ctx, out, *, scale,
     [numFlat,128,Hkv,poolHeadDim], kv_scale float32 [numFlat,128/block,Hkv], indices int32 [B,S,topK], ctx int32 [B]
     total lengths, new_lengths int32 [B] query rows (None: min(S, ctx)); scale multiplies q . k."""
     et = q.dtype
-    bf16 = et is torch.bfloat16
-    if not bf16 and et is not torch.float16:
+    bf16 = et is _BF16
+    if not bf16 and et is not _F16:
         raise ValueError("sparse_paged_kv8: q must be float16 or bfloat16")
-    if q.dim() != 4 or pool.dim() != 4 or kv_scale.dim() != 3 or page_table.dim() != 3 or indices.dim() != 3:
-        raise ValueError("sparse_paged_kv8: q and pool have 4 dimensions, kv_scale, page_table and indices 3")
-    B, S, Hq, D = q.shape
-    nflat, tpp, Hkv, phd = pool.shape
-    sf, nblk, sh = kv_scale.shape
-    ptb, two, pages = page_table.shape
-    ib, is_, topK = indices.shape
+    try:
+        B, S, Hq, D = q.shape
+        nflat, tpp, Hkv, phd = pool.shape
+        sf, nblk, sh = kv_scale.shape
+        ptb, two, pages = page_table.shape
+        ib, is_, topK = indices.shape
+    except ValueError:
+        raise ValueError("sparse_paged_kv8: q and pool have 4 dimensions, kv_scale, page_table and indices 3") from None
     if out.shape != (B, S, Hq, D) or tpp != 128 or ptb != B or two != 2 or ib != B or is_ != S or ctx.shape != (B,) or \
             sf != nflat or sh != Hkv or nblk < 1 or 128 % nblk or \
             (new_lengths is not None and new_lengths.shape != (B,)):
         raise ValueError("sparse_paged_kv8: shape mismatch")
     dev = _current_device(q)
-    f32, i32 = torch.float32, torch.int32
+    if pool.dtype is not _E4M3 or kv_scale.dtype is not _F32 or page_table.dtype is not _I32 or \
+            indices.dtype is not _I32 or ctx.dtype is not _I32 or out.dtype is not et or \
+            not (q.get_device() == pool.get_device() == kv_scale.get_device() == page_table.get_device() ==
+                 indices.get_device() == ctx.get_device() == out.get_device() == dev) or \
+            not (q.is_contiguous() and pool.is_contiguous() and kv_scale.is_contiguous() and page_table.is_contiguous() and
+                 indices.is_contiguous() and ctx.is_contiguous() and out.is_contiguous()):
+        for t, d, n in ((q, et, "q"), (pool, _E4M3, "pool"), (kv_scale, _F32, "kv_scale"), (page_table, _I32, "pageTable"),
+                        (indices, _I32, "indices"), (ctx, _I32, "contextLengths"), (out, et, "out")):
+            _arg(t, d, n, dev)
     packed = _PAGED_PACK.pack(
-        _arg(q, et, "q", dev), _arg(pool, torch.float8_e4m3fn, "pool", dev), _arg(kv_scale, f32, "kv_scale", dev),
-        _arg(page_table, i32, "pageTable", dev), _arg(indices, i32, "indices", dev),
-        _arg(ctx, i32, "contextLengths", dev), _arg(new_lengths, i32, "new_lengths", dev), _arg(out, et, "out", dev), B,
-        S, Hq, Hkv, D, phd, nflat, pages, topK, 128 // nblk, scale, _raw_stream(stream, dev),
-        _arg(status, i32, "status", dev))
+        q.data_ptr(), pool.data_ptr(), kv_scale.data_ptr(), page_table.data_ptr(), indices.data_ptr(), ctx.data_ptr(),
+        0 if new_lengths is None else _arg(new_lengths, _I32, "new_lengths", dev), out.data_ptr(), B, S, Hq, Hkv, D, phd,
+        nflat, pages, topK, 128 // nblk, scale, _raw_stream(stream, dev),
+        0 if status is None else _arg(status, _I32, "status", dev))
     r = _packed("qsa_sparse_paged_kv8_bf16" if bf16 else "qsa_sparse_paged_kv8")(packed)
     if r:
         _check(r)

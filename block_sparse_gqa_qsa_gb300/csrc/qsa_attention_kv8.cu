@@ -331,9 +331,10 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
 
 constexpr int kPad = kD + 4;  // floats of a head in the merge buffers
 
-// Resident CTAs per SM: the register budget (128 or 168 a thread) decides.
+// Resident CTAs per SM: the register budget decides (5 at 96 registers spill and took 1333 us for an 8192-row prompt
+// against 1275; 16-head groups at 168 registers 2008 against 1928).
 template <int NT>
-constexpr int kCtasPerSm = NT == 1 ? 4 : 3;
+constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
 // The tiles, and later the merge buffers: the warps' O, m and l, then the CTA's.
 template <int NT>
 constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kPad + 2) * 4 ? kWarps * kWarpBytes
@@ -348,9 +349,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
   // a sequence's rows from the last position down: the longest lists start first
   const int kvh = pair % a.Hkv, rowid = pair / a.Hkv;
   const int b = rowid / a.S, t = a.S - 1 - rowid % a.S;
-  const int L = static_cast<int>(max(0, min(a.ctx[b], a.maxPagesPerSeq * kTokensPerPage)));
-  const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
+  // the warp's first three steps of the list, on their way while the lengths are read
   const size_t bt = static_cast<size_t>(b) * a.S + t;
+  const int32_t* lst = a.indices + bt * a.topK;
+  const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
+  const int first = kStep * (rank * kWarps + warp) + lane;
+  auto list_at = [&](int slot) { return slot < a.topK ? __ldg(lst + slot) : -1; };
+  const int j0 = list_at(first), j1 = list_at(first + hop);
+  int slot = first + 2 * hop, j2 = list_at(slot);
+  const int L = max(0, min(a.ctx[b], a.maxPagesPerSeq * kTokensPerPage));
+  const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
   const size_t head0 = bt * a.Hq + static_cast<size_t>(kvh) * a.G;
   uint2* out = static_cast<uint2*>(a.o) + head0 * (kD / 4);  // 4 values each
   if (t >= n) {  // the whole cluster leaves
@@ -358,11 +366,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
       for (int e = tid; e < a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int32_t* lst = a.indices + bt * a.topK;
   const int32_t* ptK = a.pageTable + static_cast<size_t>(b) * 2 * a.maxPagesPerSeq;
   const int32_t* ptV = ptK + a.maxPagesPerSeq;
-  const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
-  const int first = kStep * (rank * kWarps + warp) + lane;
   uint8_t* mine = smem + warp * kWarpBytes;
   const uint32_t ktile = smem_addr(mine), vtile = ktile + kTileBytes;
   int* rows = reinterpret_cast<int*>(mine + kRowsAt);  // [step & 1][K, V][row & 3][row >> 2]
@@ -372,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
 
   // Resolving an entry is free of branches: what an entry cannot name is looked up at 0 and dropped.
   int bad = 0;
-  auto list_at = [&](int slot) { return slot < a.topK ? __ldg(lst + slot) : -1; };
   struct Pages {
     int j, k, v;  // entry (-1: none), its page ids
   };
@@ -428,12 +432,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
     A.l[nt][0] = A.l[nt][1] = 0.f;
   }
   const int steps = max(0, (a.topK - (first - lane) + hop - 1) / hop);
-  Rows cur = resolve(pages_of(list_at(first)), 0);
+  Rows cur = resolve(pages_of(j0), 0);
   __syncwarp();
   gather(0, 0, cur.mask, kdst);
   gather(0, 1, cur.mask, vdst);
-  Pages p1 = pages_of(list_at(first + hop));
-  int slot = first + 2 * hop, j2 = list_at(slot);
+  Pages p1 = pages_of(j1);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
   load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + head0 * (kD / 8), a.G, qf, qs);
@@ -558,8 +561,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
 template <int NT, bool kBf16>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   auto kernel = sparse_paged_kv8_kernel<NT, kBf16>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<NT>);
-  if (e != cudaSuccess) return e;
+  static_assert(kSmem<NT> <= 48 * 1024, "no attribute is set");
   // As many CTAs per pair as stay resident at once, at most one per 128 entries of the list.
   const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();
   const int most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
@@ -577,7 +579,7 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.split > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
