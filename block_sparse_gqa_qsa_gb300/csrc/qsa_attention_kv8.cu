@@ -340,90 +340,104 @@ template <int NT>
 constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kPad + 2) * 4 ? kWarps * kWarpBytes
                                                                                : (kWarps + 1) * 8 * NT * (kPad + 2) * 4;
 
-template <int NT, bool kBf16>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_kernel(const PagedArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(blockIdx.x % a.split);
-  const int pair = static_cast<int>(blockIdx.x / a.split);
-  // a sequence's rows from the last position down: the longest lists start first
-  const int kvh = pair % a.Hkv, rowid = pair / a.Hkv;
-  const int b = rowid / a.S, t = a.S - 1 - rowid % a.S;
-  // the warp's first three steps of the list, on their way while the lengths are read
-  const size_t bt = static_cast<size_t>(b) * a.S + t;
-  const int32_t* lst = a.indices + bt * a.topK;
-  const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
-  const int first = kStep * (rank * kWarps + warp) + lane;
-  auto list_at = [&](int slot) { return slot < a.topK ? __ldg(lst + slot) : -1; };
-  const int j0 = list_at(first), j1 = list_at(first + hop);
-  int slot = first + 2 * hop, j2 = list_at(slot);
-  const int L = max(0, min(a.ctx[b], a.maxPagesPerSeq * kTokensPerPage));
-  const int n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
-  const size_t head0 = bt * a.Hq + static_cast<size_t>(kvh) * a.G;
-  uint2* out = static_cast<uint2*>(a.o) + head0 * (kD / 4);  // 4 values each
-  if (t >= n) {  // the whole cluster leaves
-    if (rank == 0)
-      for (int e = tid; e < a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const int32_t* ptK = a.pageTable + static_cast<size_t>(b) * 2 * a.maxPagesPerSeq;
-  const int32_t* ptV = ptK + a.maxPagesPerSeq;
-  uint8_t* mine = smem + warp * kWarpBytes;
-  const uint32_t ktile = smem_addr(mine), vtile = ktile + kTileBytes;
-  int* rows = reinterpret_cast<int*>(mine + kRowsAt);  // [step & 1][K, V][row & 3][row >> 2]
-  float4* entries = reinterpret_cast<float4*>(mine + kEntriesAt);
-  const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
-  const uint8_t* base = a.pool + static_cast<size_t>(kvh) * a.poolHeadDim + (lane & 7) * 16;
+// What a CTA (or cluster) works on: a row of the call and successive KV heads.
+struct Row {
+  int kvh, b, t, L, n;  // first KV head, sequence, row, its length, its live rows
+  size_t bt, head0;     // list row; first query head
+};
+// The place of work item `id` with `heads` KV heads each; its lengths are read by row_lengths.
+__device__ __forceinline__ Row row_of(const PagedArgs& a, int id, int heads) {
+  Row r;
+  const int per = a.Hkv / heads, rowid = id / per;
+  r.kvh = (id - rowid * per) * heads;
+  r.b = rowid / a.S;
+  r.t = a.S - 1 - (rowid - r.b * a.S);  // a sequence's rows from the last position down: the longest lists start first
+  r.bt = static_cast<size_t>(r.b) * a.S + r.t;
+  r.head0 = r.bt * a.Hq + static_cast<size_t>(r.kvh) * a.G;
+  return r;
+}
+__device__ __forceinline__ void row_lengths(const PagedArgs& a, Row& r) {
+  r.L = max(0, min(a.ctx[r.b], a.maxPagesPerSeq * kTokensPerPage));
+  r.n = max(0, min(a.newLen ? a.newLen[r.b] : a.S, min(a.S, r.L)));
+}
 
-  // Resolving an entry is free of branches: what an entry cannot name is looked up at 0 and dropped.
-  int bad = 0;
-  struct Pages {
-    int j, k, v;  // entry (-1: none), its page ids
-  };
-  auto pages_of = [&](int j) {
+// From list entries to pool rows, free of branches: what an entry cannot name is looked up at 0 and dropped.
+struct Pages {
+  int j, k, v;  // entry (-1: none), its page ids
+};
+struct PoolRows {
+  bool ok;   // the entry names a row
+  int k, v;  // its rows of the pool (0 for none)
+};
+struct List {
+  const PagedArgs& a;
+  const int32_t *entries, *ptK, *ptV;
+  int L, bad;
+  __device__ __forceinline__ List(const PagedArgs& args, const Row& r)
+      : a(args),
+        entries(args.indices + r.bt * args.topK),
+        ptK(args.pageTable + static_cast<size_t>(r.b) * 2 * args.maxPagesPerSeq),
+        ptV(ptK + args.maxPagesPerSeq),
+        L(0),
+        bad(0) {}
+  __device__ __forceinline__ int at(int slot) const { return slot < a.topK ? __ldg(entries + slot) : -1; }
+  __device__ __forceinline__ Pages pages_of(int j) {
     const bool in = static_cast<unsigned>(j) < static_cast<unsigned>(L);
     bad |= !in && j != -1 ? kErrBadIndex : 0;
-    const int at = in ? j >> 7 : 0;
-    return Pages{in ? j : -1, __ldg(ptK + at), __ldg(ptV + at)};
-  };
-  struct Rows {
-    bool ok;        // the lane's entry names a row
-    float ks, vs;   // its scales as stored
-    unsigned mask;  // lanes whose entry does
-  };
-  auto resolve = [&](const Pages& p, int parity) {
-    Rows r;
+    const int page = in ? j >> 7 : 0;
+    return Pages{in ? j : -1, __ldg(ptK + page), __ldg(ptV + page)};
+  }
+  __device__ __forceinline__ PoolRows rows_of(const Pages& p) {
     const bool pages = static_cast<unsigned>(p.k) < static_cast<unsigned>(a.numFlatPages) &&
                        static_cast<unsigned>(p.v) < static_cast<unsigned>(a.numFlatPages);
-    r.ok = p.j >= 0 && pages;
+    const bool ok = p.j >= 0 && pages;
     bad |= p.j >= 0 && !pages ? kErrBadPage : 0;
-    const int krow = r.ok ? p.k * kTokensPerPage + (p.j & 127) : 0;
-    const int vrow = r.ok ? p.v * kTokensPerPage + (p.j & 127) : 0;
-    r.ks = __ldg(a.scale + static_cast<size_t>(krow >> a.blockShift) * a.Hkv + kvh);
-    r.vs = __ldg(a.scale + static_cast<size_t>(vrow >> a.blockShift) * a.Hkv + kvh);
-    r.mask = __ballot_sync(kFull, r.ok);
-    int* at = rows + parity * 2 * kStep + (lane & 3) * (kStep / 4) + (lane >> 2);
-    at[0] = r.ok ? krow : -1;
-    at[kStep] = r.ok ? vrow : -1;
-    return r;
-  };
-  // Gathers a step's K (plane 0) or V (1) rows into the tile, 8 lanes to a row of 128 bytes: one copy group.
-  const uint32_t kdst[2] = {ktile + k_off(lane >> 3, lane & 7), ktile + k_off(lane >> 3, lane & 7)};
-  const uint32_t v0 = vtile + v_off(lane >> 3, lane & 7), vdst[2] = {v0, v0 ^ 64};  // rows 4 i: bit 2 flips with i
-  auto gather = [&](int parity, int plane, unsigned mask, const uint32_t (&dst)[2]) {
-    const int4* at = reinterpret_cast<const int4*>(rows + (parity * 2 + plane) * kStep + (lane >> 3) * (kStep / 4));
-    if (mask) {
-      const int4 x = at[0], y = at[1];
-      const int row[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      if (mask == kFull)
-        copy_rows<true>(row, dst, base, rowBytes, std::make_index_sequence<8>{});
-      else
-        copy_rows<false>(row, dst, base, rowBytes, std::make_index_sequence<8>{});
-    }
-    cp_async_commit();
-  };
+    return PoolRows{ok, ok ? p.k * kTokensPerPage + (p.j & 127) : 0, ok ? p.v * kTokensPerPage + (p.j & 127) : 0};
+  }
+  __device__ __forceinline__ void report() {
+    bad = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
+    if (bad && (threadIdx.x & 31) == 0 && a.status) atomicOr(a.status, bad);
+  }
+};
+// The scales of a pool row, from KV head kvh on.
+__device__ __forceinline__ const float* scales_of(const PagedArgs& a, int row, int kvh) {
+  return a.scale + static_cast<size_t>(row >> a.blockShift) * a.Hkv + kvh;
+}
+// What the softmax needs of an entry: see softmax32.
+__device__ __forceinline__ float4 entry_of(const PagedArgs& a, bool ok, float ks, float vs) {
+  vs = read_scale(vs);
+  return ok ? make_float4(read_scale(ks) * a.sl2, lg2_ftz(vs), rcp_ftz(vs), 0.f) : make_float4(0.f, -INFINITY, 0.f, 0.f);
+}
+// Place of a step's entry i among its 32 row ids: a lane gathers rows 4 i + (lane >> 3), which lie together.
+__device__ __forceinline__ int row_place(int i) { return (i & 3) * (kStep / 4) + (i >> 2); }
 
-  Acc<NT> A;
+// Where a lane's copies of a step's K and V rows go in a warp's tiles.
+struct TileDst {
+  uint32_t k[2], v[2];
+  __device__ __forceinline__ TileDst(uint32_t ktile, uint32_t vtile) {
+    const int r = (threadIdx.x & 31) >> 3, c = threadIdx.x & 7;
+    k[0] = k[1] = ktile + k_off(r, c);
+    v[0] = vtile + v_off(r, c);
+    v[1] = v[0] ^ 64;  // rows 4 i + r: bit 2 of the row flips with i
+  }
+};
+// Gathers the rows whose ids lie at `ids` (by row_place, -1 for none): one copy group, empty if mask names none.
+__device__ __forceinline__ void gather_rows(const int* ids, unsigned mask, const uint32_t (&dst)[2], const uint8_t* base,
+                                            uint32_t rowBytes) {
+  if (mask) {
+    const int4* at = reinterpret_cast<const int4*>(ids + ((threadIdx.x & 31) >> 3) * (kStep / 4));
+    const int4 x = at[0], y = at[1];
+    const int row[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    if (mask == kFull)
+      copy_rows<true>(row, dst, base, rowBytes, std::make_index_sequence<8>{});
+    else
+      copy_rows<false>(row, dst, base, rowBytes, std::make_index_sequence<8>{});
+  }
+  cp_async_commit();
+}
+
+template <int NT>
+__device__ __forceinline__ void acc_init(Acc<NT>& A) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -431,102 +445,166 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
     A.m[nt][0] = A.m[nt][1] = -FLT_MAX;
     A.l[nt][0] = A.l[nt][1] = 0.f;
   }
+}
+
+// A warp's result to shared memory: o [8 NT heads][kPad] fp32 (kPad puts a fragment's writes in different banks), m, l [8 NT].
+template <int NT>
+__device__ __forceinline__ void stash(const Acc<NT>& A, float* o, float* m, float* l) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h = 8 * nt + 2 * q + j;
+      float sum = A.l[nt][j];
+      sum += __shfl_xor_sync(kFull, sum, 4);
+      sum += __shfl_xor_sync(kFull, sum, 8);
+      sum += __shfl_xor_sync(kFull, sum, 16);
+      if (g == 0) {
+        m[h] = A.m[nt][j];
+        l[h] = sum;
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        o[h * kPad + 16 * mt + g] = A.o[mt][nt][j];
+        o[h * kPad + 16 * mt + g + 8] = A.o[mt][nt][2 + j];
+      }
+    }
+}
+// Joins `count` stashed results of head h, `stride` heads apart: the lane's four dims relative to the largest maximum,
+// which is returned with the sum.
+__device__ __forceinline__ float4 join(const float* o, const float* m, const float* l, int h, int count, int stride, float& M,
+                                       float& sum) {
+  M = -FLT_MAX;
+  sum = 0.f;
+  for (int w = 0; w < count; ++w) M = fmaxf(M, m[w * stride + h]);
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = 0; w < count; ++w) {
+    const int k = w * stride + h;
+    const float f = exp2f(m[k] - M);
+    const float4 x = *reinterpret_cast<const float4*>(o + k * kPad + 4 * (threadIdx.x & 31));
+    sum += f * l[k];
+    r.x += f * x.x;
+    r.y += f * x.y;
+    r.z += f * x.z;
+    r.w += f * x.w;
+  }
+  return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint2 normalised(const float4& o, float sum) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  return pack4<kBf16>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+}
+
+// Few (row, KV head) pairs: the warps of a CTA, and the CTAs of a cluster, share one pair's list.
+template <int NT, bool kBf16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_split_kernel(const PagedArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(blockIdx.x % a.split);
+  Row r = row_of(a, static_cast<int>(blockIdx.x / a.split), 1);
+  List list(a, r);
+  // the warp's first three steps of the list, on their way while the lengths are read
+  const int hop = kStep * kWarps * a.split;  // entries between a warp's steps
+  const int first = kStep * (rank * kWarps + warp) + lane;
+  const int j0 = list.at(first), j1 = list.at(first + hop);
+  int slot = first + 2 * hop, j2 = list.at(slot);
+  row_lengths(a, r);
+  list.L = r.L;
+  uint2* out = static_cast<uint2*>(a.o) + r.head0 * (kD / 4);  // 4 values each
+  if (r.t >= r.n) {  // the whole cluster leaves
+    if (rank == 0)
+      for (int e = tid; e < a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  uint8_t* mine = smem + warp * kWarpBytes;
+  const uint32_t ktile = smem_addr(mine), vtile = ktile + kTileBytes;
+  int* ids = reinterpret_cast<int*>(mine + kRowsAt);  // [step & 1][K, V][row_place]
+  float4* entries = reinterpret_cast<float4*>(mine + kEntriesAt);
+  const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
+  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh) * a.poolHeadDim + (lane & 7) * 16;
+  const TileDst dst(ktile, vtile);
+
+  struct Named {
+    bool ok;        // the lane's entry names a row
+    float ks, vs;   // its scales as stored
+    unsigned mask;  // lanes whose entry does
+  };
+  auto resolve = [&](const Pages& p, int parity) {
+    const PoolRows rows = list.rows_of(p);
+    const Named n{rows.ok, __ldg(scales_of(a, rows.k, r.kvh)), __ldg(scales_of(a, rows.v, r.kvh)), __ballot_sync(kFull, rows.ok)};
+    int* at = ids + parity * 2 * kStep + row_place(lane);
+    at[0] = rows.ok ? rows.k : -1;
+    at[kStep] = rows.ok ? rows.v : -1;
+    return n;
+  };
+  auto gather = [&](int parity, int plane, unsigned mask) {
+    gather_rows(ids + (parity * 2 + plane) * kStep, mask, plane ? dst.v : dst.k, base, rowBytes);
+  };
+
+  Acc<NT> A;
+  acc_init(A);
   const int steps = max(0, (a.topK - (first - lane) + hop - 1) / hop);
-  Rows cur = resolve(pages_of(j0), 0);
+  Named cur = resolve(list.pages_of(j0), 0);
   __syncwarp();
-  gather(0, 0, cur.mask, kdst);
-  gather(0, 1, cur.mask, vdst);
-  Pages p1 = pages_of(j1);
+  gather(0, 0, cur.mask);
+  gather(0, 1, cur.mask);
+  Pages p1 = list.pages_of(j1);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
-  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + head0 * (kD / 8), a.G, qf, qs);
+  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, qf, qs);
   for (int i = 0; i < steps; ++i) {
     const int par = (i + 1) & 1;
-    const Rows next = resolve(p1, par);
-    p1 = pages_of(j2);
+    const Named next = resolve(p1, par);
+    p1 = list.pages_of(j2);
     slot += hop;
-    j2 = list_at(slot);
+    j2 = list.at(slot);
     if (cur.mask) {
-      const float vs = read_scale(cur.vs);
-      entries[lane] = cur.ok ? make_float4(read_scale(cur.ks) * a.sl2, lg2_ftz(vs), rcp_ftz(vs), 0.f)
-                             : make_float4(0.f, -INFINITY, 0.f, 0.f);
+      entries[lane] = entry_of(a, cur.ok, cur.ks, cur.vs);
       float s[2][NT][4];
       uint32_t pb[2][NT][2];
       cp_async_wait<1>();  // this lane's share of the K tile; the V tile may be in flight
       __syncwarp();
       scores32<NT>(s, ktile, qf);
       __syncwarp();  // every lane is done with the K tile
-      gather(par, 0, next.mask, kdst);
+      gather(par, 0, next.mask);
       softmax32<NT, kBf16>(A, s, qs, entries, pb);
       cp_async_wait<1>();  // the V tile; the next K tile may be in flight
       __syncwarp();
       values32<NT>(A, vtile, pb);
       __syncwarp();  // every lane is done with the V tile
-      gather(par, 1, next.mask, vdst);
+      gather(par, 1, next.mask);
     } else {  // nothing was copied for this step
       __syncwarp();
-      gather(par, 0, next.mask, kdst);
-      gather(par, 1, next.mask, vdst);
+      gather(par, 0, next.mask);
+      gather(par, 1, next.mask);
     }
     cur = next;
   }
   cp_async_wait<0>();
-  bad = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
-  if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
-  __syncthreads();  // the rings become the merge buffers
+  list.report();
+  __syncthreads();  // the tiles become the merge buffers
 
-  // Per warp [8 NT heads][128 dims, padded] fp32 and (m, l).  kPad puts a fragment's writes in different banks.
   constexpr int H = 8 * NT;
   float* ow = reinterpret_cast<float*>(smem);   // [kWarps][H][kPad]
   float* oc = ow + kWarps * H * kPad;           // the CTA's merged [H][kPad]
   float* mw = oc + H * kPad;                    // [kWarps][H]
   float* lw = mw + kWarps * H;
   float* mc = lw + kWarps * H;                  // [H], then the sums
-  const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int h = 8 * nt + 2 * q + j;
-      float l = A.l[nt][j];
-      l += __shfl_xor_sync(kFull, l, 4);
-      l += __shfl_xor_sync(kFull, l, 8);
-      l += __shfl_xor_sync(kFull, l, 16);
-      if (g == 0) {
-        mw[warp * H + h] = A.m[nt][j];
-        lw[warp * H + h] = l;
-      }
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        ow[(warp * H + h) * kPad + 16 * mt + g] = A.o[mt][nt][j];
-        ow[(warp * H + h) * kPad + 16 * mt + g + 8] = A.o[mt][nt][2 + j];
-      }
-    }
+  stash<NT>(A, ow + warp * H * kPad, mw + warp * H, lw + warp * H);
   __syncthreads();
   for (int h = warp; h < a.G; h += kWarps) {
-    float M = -FLT_MAX, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mw[w * H + h]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(mw[w * H + h] - M);
-      const float4 x = *reinterpret_cast<const float4*>(ow + (w * H + h) * kPad + 4 * lane);
-      l += f * lw[w * H + h];
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
-    }
+    float M, sum;
+    const float4 o = join(ow, mw, lw, h, kWarps, H, M, sum);
     if (a.split > 1) {
       *reinterpret_cast<float4*>(oc + h * kPad + 4 * lane) = o;
       if (lane == 0) {
         mc[h] = M;
-        mc[H + h] = l;
+        mc[H + h] = sum;
       }
     } else {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      out[h * 32 + lane] = pack4<kBf16>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      out[h * 32 + lane] = normalised<kBf16>(o, sum);
     }
   }
   if (a.split == 1) return;
@@ -535,38 +613,187 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_ker
   const uint32_t ocAddr = smem_addr(oc), mcAddr = smem_addr(mc);
   for (int h = rank * kWarps + warp; h < a.G; h += a.split * kWarps) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ms[kMaxCluster], M = -FLT_MAX, l = 0.f;
+    float ms[kMaxCluster], M = -FLT_MAX, sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      ms[r] = r < a.split ? cluster_ld(cluster_addr(mcAddr + h * 4, r)) : -FLT_MAX;
-      M = fmaxf(M, ms[r]);
+    for (int c = 0; c < kMaxCluster; ++c) {
+      ms[c] = c < a.split ? cluster_ld(cluster_addr(mcAddr + h * 4, c)) : -FLT_MAX;
+      M = fmaxf(M, ms[c]);
     }
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < a.split) {
-        const float f = exp2f(ms[r] - M);
-        const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * kPad + 4 * lane) * 4, r));
-        l += f * cluster_ld(cluster_addr(mcAddr + (H + h) * 4, r));
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < a.split) {
+        const float f = exp2f(ms[c] - M);
+        const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * kPad + 4 * lane) * 4, c));
+        sum += f * cluster_ld(cluster_addr(mcAddr + (H + h) * 4, c));
         o.x += f * x.x;
         o.y += f * x.y;
         o.z += f * x.z;
         o.w += f * x.w;
       }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    out[h * 32 + lane] = pack4<kBf16>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    out[h * 32 + lane] = normalised<kBf16>(o, sum);
   }
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
+// Many rows: a CTA takes HC KV heads of a row, kWarps / HC warps each.  The heads share the list, so its entries are
+// resolved once for all of them, 128 at a time and 32 per warp: row ids, and per head what the softmax needs, go to
+// shared memory for every warp.  Chunk c + 1's row ids are written before the barrier that opens chunk c (its first
+// rows are gathered in chunk c's last step), its scales, which are loaded meanwhile, behind chunk c's steps.
+constexpr int kChunk = kStep * kWarps;  // entries
+template <int HC>
+struct RowsSmem {
+  static constexpr int ids = kWarps * 2 * kTileBytes;                // [chunk % 3][step][K, V][kStep]
+  static constexpr int masks = ids + 3 * kChunk * 2 * 4;             // [chunk % 3][step]
+  static constexpr int entries = masks + 64;                         // [chunk & 1][HC][kChunk]
+  static constexpr int bytes = entries + 2 * HC * kChunk * 16;
+};
+template <int NT, int HC, bool kBf16>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_rows_kernel(const PagedArgs a) {
+  constexpr int WPH = kWarps / HC;  // warps of a head
+  using Smem = RowsSmem<HC>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hc = warp % HC, sub = warp / HC;
+  Row r = row_of(a, static_cast<int>(blockIdx.x), HC);
+  List list(a, r);
+  const int j0 = list.at(tid), j1 = list.at(tid + kChunk);
+  int slot = tid + 2 * kChunk, j2 = list.at(slot);
+  row_lengths(a, r);
+  list.L = r.L;
+  uint2* out = static_cast<uint2*>(a.o) + r.head0 * (kD / 4);  // HC G heads of 4 values each
+  if (r.t >= r.n) {
+    for (int e = tid; e < HC * a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const uint32_t ktile = smem_addr(smem) + warp * 2 * kTileBytes, vtile = ktile + kTileBytes;
+  int* ids = reinterpret_cast<int*>(smem + Smem::ids);
+  unsigned* masks = reinterpret_cast<unsigned*>(smem + Smem::masks);
+  float4* entries = reinterpret_cast<float4*>(smem + Smem::entries);
+  const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
+  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + hc) * a.poolHeadDim + (lane & 7) * 16;
+  const TileDst dst(ktile, vtile);
+
+  struct Scales {
+    bool ok;
+    float k[HC], v[HC];
+  };
+  auto put_rows = [&](const Pages& p, int buf) {  // row ids of the thread's entry of a chunk, and its scales' loads
+    const PoolRows rows = list.rows_of(p);
+    int* at = ids + (buf * kWarps + warp) * 2 * kStep + row_place(lane);
+    at[0] = rows.ok ? rows.k : -1;
+    at[kStep] = rows.ok ? rows.v : -1;
+    const unsigned mask = __ballot_sync(kFull, rows.ok);
+    if (lane == 0) masks[buf * kWarps + warp] = mask;
+    Scales s;
+    s.ok = rows.ok;
+    const float *ks = scales_of(a, rows.k, r.kvh), *vs = scales_of(a, rows.v, r.kvh);
+#pragma unroll
+    for (int c = 0; c < HC; ++c) {
+      s.k[c] = __ldg(ks + c);
+      s.v[c] = __ldg(vs + c);
+    }
+    return s;
+  };
+  auto put_entries = [&](const Scales& s, int buf) {
+#pragma unroll
+    for (int c = 0; c < HC; ++c) entries[(buf * HC + c) * kChunk + tid] = entry_of(a, s.ok, s.k[c], s.v[c]);
+  };
+  auto gather = [&](int buf, int step, int plane, unsigned mask) {
+    gather_rows(ids + ((buf * kWarps + step) * 2 + plane) * kStep, mask, plane ? dst.v : dst.k, base, rowBytes);
+  };
+
+  Acc<NT> A;
+  acc_init(A);
+  Scales sc = put_rows(list.pages_of(j0), 0);
+  Pages p1 = list.pages_of(j1);
+  uint32_t qf[NT][8][2];
+  float qs[NT][2];
+  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + hc * a.G) * (kD / 8), a.G, qf, qs);
+  put_entries(sc, 0);
+  __syncthreads();
+  unsigned mask = masks[sub];  // of the warp's current step, whose rows are gathered
+  gather(0, sub, 0, mask);
+  gather(0, sub, 1, mask);
+  const int chunks = (a.topK + kChunk - 1) / kChunk;
+  int buf = 0;
+  for (int c = 0; c < chunks; ++c) {
+    const int nbuf = buf == 2 ? 0 : buf + 1;
+    sc = put_rows(p1, nbuf);
+    p1 = list.pages_of(j2);
+    slot += kChunk;
+    j2 = list.at(slot);
+    __syncthreads();
+#pragma unroll 1
+    for (int e = sub; e < kWarps; e += WPH) {
+      const bool here = e + WPH < kWarps;  // the warp's next step is in this chunk
+      const int gbuf = here ? buf : nbuf, ge = here ? e + WPH : sub;
+      const unsigned next = masks[gbuf * kWarps + ge];
+      if (mask) {
+        float s[2][NT][4];
+        uint32_t pb[2][NT][2];
+        cp_async_wait<1>();  // this lane's share of the K tile; the V tile may be in flight
+        __syncwarp();
+        scores32<NT>(s, ktile, qf);
+        __syncwarp();  // every lane is done with the K tile
+        gather(gbuf, ge, 0, next);
+        softmax32<NT, kBf16>(A, s, qs, entries + ((c & 1) * HC + hc) * kChunk + e * kStep, pb);
+        cp_async_wait<1>();  // the V tile; the next K tile may be in flight
+        __syncwarp();
+        values32<NT>(A, vtile, pb);
+        __syncwarp();  // every lane is done with the V tile
+        gather(gbuf, ge, 1, next);
+      } else {
+        gather(gbuf, ge, 0, next);
+        gather(gbuf, ge, 1, next);
+      }
+      mask = next;
+    }
+    put_entries(sc, (c + 1) & 1);
+    buf = nbuf;
+  }
+  cp_async_wait<0>();
+  list.report();
+  __syncthreads();  // the tiles become the merge buffers
+  constexpr int H = 8 * NT;
+  float* ow = reinterpret_cast<float*>(smem);  // [kWarps][H][kPad]
+  float* mw = ow + kWarps * H * kPad;          // [kWarps][H]
+  float* lw = mw + kWarps * H;
+  stash<NT>(A, ow + warp * H * kPad, mw + warp * H, lw + warp * H);
+  if constexpr (WPH == 1)
+    __syncwarp();
+  else
+    __syncthreads();
+  for (int h = sub; h < a.G; h += WPH) {
+    float M, sum;
+    const float4 o = join(ow + hc * H * kPad, mw + hc * H, lw + hc * H, h, WPH, HC * H, M, sum);
+    out[(hc * a.G + h) * 32 + lane] = normalised<kBf16>(o, sum);
+  }
+}
+
+template <int NT, int HC, bool kBf16>
+cudaError_t rows_go(const PagedArgs& a, long long ctas, cudaStream_t st) {
+  auto kernel = sparse_paged_kv8_rows_kernel<NT, HC, kBf16>;
+  constexpr int merge = kWarps * 8 * NT * (kPad + 2) * 4;
+  constexpr int smem = RowsSmem<HC>::bytes > merge ? RowsSmem<HC>::bytes : merge;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<static_cast<unsigned>(ctas), kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <int NT, bool kBf16>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
-  auto kernel = sparse_paged_kv8_kernel<NT, kBf16>;
-  static_assert(kSmem<NT> <= 48 * 1024, "no attribute is set");
-  // As many CTAs per pair as stay resident at once, at most one per 128 entries of the list.
-  const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();
+  const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();  // CTAs resident at once
+  // KV heads share a CTA where that leaves a few waves of CTAs.
+  if (a.Hkv % 4 == 0 && pairs / 4 >= 4 * slots) return rows_go<NT, 4, kBf16>(a, pairs / 4, st);
+  if (a.Hkv % 2 == 0 && pairs / 2 >= 4 * slots) return rows_go<NT, 2, kBf16>(a, pairs / 2, st);
+  // Otherwise as many CTAs per pair as stay resident at once, at most one per 128 entries of the list.
   const int most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
   a.split = static_cast<int>(std::max<long long>(1, std::min<long long>(most, slots / pairs)));
-  if (pairs * a.split > 0x7fffffffLL) a.split = 1;
+  auto kernel = sparse_paged_kv8_split_kernel<NT, kBf16>;
+  static_assert(kSmem<NT> <= 48 * 1024, "no attribute is set");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.split));
   cfg.blockDim = dim3(kThreads);

@@ -89,6 +89,26 @@ def test_whole_prompt():
     check(c, run(c))
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv,S,topK", [
+    (torch.float16, 32, 4, 2600, 131), (torch.bfloat16, 8, 8, 1300, 300), (torch.float16, 14, 2, 2600, 70),
+    (torch.bfloat16, 24, 2, 1400, 129), (torch.float16, 64, 4, 1300, 128), (torch.float16, 12, 6, 1700, 40),
+    (torch.bfloat16, 3, 3, 900, 257)])
+def test_many_rows(dtype, Hq, Hkv, S, topK):
+    """Enough rows that a CTA takes four or two KV heads of one (or, for 3 heads, one), with padded and empty rows."""
+    c = make(dtype, Hq, Hkv, S, (S + 50, 200), (S - 3, 150), topK, 16, tail=16, seed=Hq + S)
+    c["lists"][0, 7] = -1
+    c["lists"][0, 11, :-1] = -1
+    c["lists"][0, 12:40, 3::5] = -1
+    c["lists"][1, 0, topK // 2] = -1
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = run(c, status=status)
+    check(c, out)
+    assert int(status) == 0 and torch.equal(out, run(c))
+    want = out
+    c["lists"][0, 7, topK - 1], c["lists"][1, 0, topK // 2] = S + 50, -5  # from naming nothing to naming no token
+    assert torch.equal(run(c, status=status), want) and int(status) == 4
+
+
 @pytest.mark.parametrize("B", (1, 2, 9, 20, 40, 60, 114, 160))
 def test_cluster_sizes(B):
     """4 KV heads x B pairs: 8 down to 1 CTAs per pair; two runs give the same bits."""
