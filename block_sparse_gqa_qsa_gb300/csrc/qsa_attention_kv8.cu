@@ -5,21 +5,23 @@
 //
 // over the row's list, with e4m3 codes c and one fp32 scale per block of
 // tokens and head.  In log2 units, with x_j = ks_j scale log2(e) (q . c^K_j) and
-// e_j = x_j + log2(vs_j), one pass keeps M = max e_j, l = sum 2^(e_j - M) / vs_j
+// e_j = x_j + log2(vs_j), one pass keeps a maximum M of e_j, l = sum 2^(e_j - M) / vs_j
 // and O = sum 2^(e_j - M) c^V_j: the V scale rides in the exponent, so the
-// probabilities that the second product rounds to fp16 are at most 1 whatever
-// the scales are, and o = O / l.  (log2(vs_j) is the hardware's approximation;
-// its error enters O and l alike.)
+// weights that the second product rounds to fp16 are relative to the largest
+// weight times scale, whatever the scales are, and o = O / l.  (log2(vs_j) is
+// the hardware's approximation; its error enters O and l alike.)
 //
-// One CTA of 4 warps takes a (row, KV head) pair; when there are few pairs a
-// cluster of up to 8 CTAs shares one.  The list is dealt out to the warps of
-// the pair in steps of 32 entries, and each warp runs by itself, with no CTA
-// barrier inside the loop: lane i resolves entry i of a step (list entry three
-// steps ahead, page ids two, scales one, so that each dependent load has a
-// step to arrive), and the warp gathers the 32 K and V rows of 128 bytes with
-// cp.async into its own K tile and V tile.  A step's K tile is free after its
-// first product, its V tile after the second, and the next step's rows start
-// then: one tile of each keeps half a step of copies in flight per warp.
+// Two kernels share the arithmetic.  With few (row, KV head) pairs, a CTA of 4
+// warps takes one, or a cluster of up to 8 CTAs shares it, the list dealt out
+// to the warps in steps of 32 entries; with many, a CTA takes four KV heads of a
+// row, a warp each, and resolves the list once for all four.
+//
+// A warp runs its steps by itself.  Every dependent load of a step (list entry,
+// page ids, scales) has a step or more to arrive; the 32 K and V rows of 128
+// bytes are gathered with cp.async into the warp's own K tile and V tile.  A
+// step's K tile is free after its first product, its V tile after the second,
+// and the next step's rows start then: one tile of each keeps half a step of
+// copies in flight per warp.
 //
 // S^T = C^K Q^T and O^T += (C^V)^T P^T are m16n8k16 MMAs in fp16 with the head
 // group as N; codes are converted to fp16 pairs in registers (exact).  The
@@ -471,16 +473,18 @@ __device__ __forceinline__ void stash(const Acc<NT>& A, float* o, float* m, floa
       }
     }
 }
-// Joins `count` stashed results of head h, `stride` heads apart: the lane's four dims relative to the largest maximum,
-// which is returned with the sum.
-__device__ __forceinline__ float4 join(const float* o, const float* m, const float* l, int h, int count, int stride, float& M,
-                                       float& sum) {
+// Joins the warps' stashed results of head h: the lane's four dims relative to the largest maximum, which is returned
+// with the sum.
+template <int H>
+__device__ __forceinline__ float4 join(const float* o, const float* m, const float* l, int h, float& M, float& sum) {
   M = -FLT_MAX;
   sum = 0.f;
-  for (int w = 0; w < count; ++w) M = fmaxf(M, m[w * stride + h]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m[w * H + h]);
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int w = 0; w < count; ++w) {
-    const int k = w * stride + h;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int k = w * H + h;
     const float f = exp2f(m[k] - M);
     const float4 x = *reinterpret_cast<const float4*>(o + k * kPad + 4 * (threadIdx.x & 31));
     sum += f * l[k];
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_spl
   __syncthreads();
   for (int h = warp; h < a.G; h += kWarps) {
     float M, sum;
-    const float4 o = join(ow, mw, lw, h, kWarps, H, M, sum);
+    const float4 o = join<H>(ow, mw, lw, h, M, sum);
     if (a.split > 1) {
       *reinterpret_cast<float4*>(oc + h * kPad + 4 * lane) = o;
       if (lane == 0) {
@@ -635,47 +639,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_spl
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
-// Many rows: a CTA takes HC KV heads of a row, kWarps / HC warps each.  The heads share the list, so its entries are
-// resolved once for all of them, 128 at a time and 32 per warp: row ids, and per head what the softmax needs, go to
-// shared memory for every warp.  Chunk c + 1's row ids are written before the barrier that opens chunk c (its first
+// Many rows: a CTA takes four KV heads of a row, a warp one head and the whole list.  The heads share the list, so its
+// entries are resolved once for all of them, 128 at a time and 32 per warp: row ids, and per head what the softmax needs,
+// go to shared memory for every warp.  Chunk c + 1's row ids are written before the barrier that opens chunk c (its first
 // rows are gathered in chunk c's last step), its scales, which are loaded meanwhile, behind chunk c's steps.
-constexpr int kChunk = kStep * kWarps;  // entries
-template <int HC>
-struct RowsSmem {
-  static constexpr int ids = kWarps * 2 * kTileBytes;                // [chunk % 3][step][K, V][kStep]
-  static constexpr int masks = ids + 3 * kChunk * 2 * 4;             // [chunk % 3][step]
-  static constexpr int entries = masks + 64;                         // [chunk & 1][HC][kChunk]
-  static constexpr int bytes = entries + 2 * HC * kChunk * 16;
-};
-template <int NT, int HC, bool kBf16>
+constexpr int kChunk = kStep * kWarps;                             // entries
+constexpr int kIdsAt = kWarps * 2 * kTileBytes;                    // [chunk % 3][step][K, V][kStep] row ids
+constexpr int kMasksAt = kIdsAt + 3 * kChunk * 2 * 4;              // [chunk % 3][step] entries that name a row
+constexpr int kChunkEntriesAt = kMasksAt + 64;                     // [chunk & 1][head][kChunk]
+constexpr int kRowsSmem = kChunkEntriesAt + 2 * kWarps * kChunk * 16;
+
+template <int NT, bool kBf16>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_rows_kernel(const PagedArgs a) {
-  constexpr int WPH = kWarps / HC;  // warps of a head
-  using Smem = RowsSmem<HC>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hc = warp % HC, sub = warp / HC;
-  Row r = row_of(a, static_cast<int>(blockIdx.x), HC);
+  Row r = row_of(a, static_cast<int>(blockIdx.x), kWarps);
   List list(a, r);
   const int j0 = list.at(tid), j1 = list.at(tid + kChunk);
   int slot = tid + 2 * kChunk, j2 = list.at(slot);
   row_lengths(a, r);
   list.L = r.L;
-  uint2* out = static_cast<uint2*>(a.o) + r.head0 * (kD / 4);  // HC G heads of 4 values each
+  uint2* out = static_cast<uint2*>(a.o) + r.head0 * (kD / 4);  // kWarps G heads of 4 values each
   if (r.t >= r.n) {
-    for (int e = tid; e < HC * a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+    for (int e = tid; e < kWarps * a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
     return;
   }
   const uint32_t ktile = smem_addr(smem) + warp * 2 * kTileBytes, vtile = ktile + kTileBytes;
-  int* ids = reinterpret_cast<int*>(smem + Smem::ids);
-  unsigned* masks = reinterpret_cast<unsigned*>(smem + Smem::masks);
-  float4* entries = reinterpret_cast<float4*>(smem + Smem::entries);
+  int* ids = reinterpret_cast<int*>(smem + kIdsAt);
+  unsigned* masks = reinterpret_cast<unsigned*>(smem + kMasksAt);
+  float4* entries = reinterpret_cast<float4*>(smem + kChunkEntriesAt);
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
-  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + hc) * a.poolHeadDim + (lane & 7) * 16;
+  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + warp) * a.poolHeadDim + (lane & 7) * 16;
   const TileDst dst(ktile, vtile);
 
   struct Scales {
     bool ok;
-    float k[HC], v[HC];
+    float k[kWarps], v[kWarps];
   };
   auto put_rows = [&](const Pages& p, int buf) {  // row ids of the thread's entry of a chunk, and its scales' loads
     const PoolRows rows = list.rows_of(p);
@@ -688,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
     s.ok = rows.ok;
     const float *ks = scales_of(a, rows.k, r.kvh), *vs = scales_of(a, rows.v, r.kvh);
 #pragma unroll
-    for (int c = 0; c < HC; ++c) {
+    for (int c = 0; c < kWarps; ++c) {
       s.k[c] = __ldg(ks + c);
       s.v[c] = __ldg(vs + c);
     }
@@ -696,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
   };
   auto put_entries = [&](const Scales& s, int buf) {
 #pragma unroll
-    for (int c = 0; c < HC; ++c) entries[(buf * HC + c) * kChunk + tid] = entry_of(a, s.ok, s.k[c], s.v[c]);
+    for (int c = 0; c < kWarps; ++c) entries[(buf * kWarps + c) * kChunk + tid] = entry_of(a, s.ok, s.k[c], s.v[c]);
   };
   auto gather = [&](int buf, int step, int plane, unsigned mask) {
     gather_rows(ids + ((buf * kWarps + step) * 2 + plane) * kStep, mask, plane ? dst.v : dst.k, base, rowBytes);
@@ -708,12 +707,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
   Pages p1 = list.pages_of(j1);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
-  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + hc * a.G) * (kD / 8), a.G, qf, qs);
+  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + warp * a.G) * (kD / 8), a.G, qf, qs);
   put_entries(sc, 0);
   __syncthreads();
-  unsigned mask = masks[sub];  // of the warp's current step, whose rows are gathered
-  gather(0, sub, 0, mask);
-  gather(0, sub, 1, mask);
+  unsigned mask = masks[0];  // of the current step, whose rows are gathered
+  gather(0, 0, 0, mask);
+  gather(0, 0, 1, mask);
   const int chunks = (a.topK + kChunk - 1) / kChunk;
   int buf = 0;
   for (int c = 0; c < chunks; ++c) {
@@ -724,9 +723,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
     j2 = list.at(slot);
     __syncthreads();
 #pragma unroll 1
-    for (int e = sub; e < kWarps; e += WPH) {
-      const bool here = e + WPH < kWarps;  // the warp's next step is in this chunk
-      const int gbuf = here ? buf : nbuf, ge = here ? e + WPH : sub;
+    for (int e = 0; e < kWarps; ++e) {
+      const bool last = e == kWarps - 1;
+      const int gbuf = last ? nbuf : buf, ge = last ? 0 : e + 1;  // the next step
       const unsigned next = masks[gbuf * kWarps + ge];
       if (mask) {
         float s[2][NT][4];
@@ -736,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
         scores32<NT>(s, ktile, qf);
         __syncwarp();  // every lane is done with the K tile
         gather(gbuf, ge, 0, next);
-        softmax32<NT, kBf16>(A, s, qs, entries + ((c & 1) * HC + hc) * kChunk + e * kStep, pb);
+        softmax32<NT, kBf16>(A, s, qs, entries + ((c & 1) * kWarps + warp) * kChunk + e * kStep, pb);
         cp_async_wait<1>();  // the V tile; the next K tile may be in flight
         __syncwarp();
         values32<NT>(A, vtile, pb);
@@ -753,42 +752,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
   }
   cp_async_wait<0>();
   list.report();
-  __syncthreads();  // the tiles become the merge buffers
+  __syncthreads();  // the tiles become output buffers
   constexpr int H = 8 * NT;
-  float* ow = reinterpret_cast<float*>(smem);  // [kWarps][H][kPad]
-  float* mw = ow + kWarps * H * kPad;          // [kWarps][H]
-  float* lw = mw + kWarps * H;
-  stash<NT>(A, ow + warp * H * kPad, mw + warp * H, lw + warp * H);
-  if constexpr (WPH == 1)
-    __syncwarp();
-  else
-    __syncthreads();
-  for (int h = sub; h < a.G; h += WPH) {
-    float M, sum;
-    const float4 o = join(ow + hc * H * kPad, mw + hc * H, lw + hc * H, h, WPH, HC * H, M, sum);
-    out[(hc * a.G + h) * 32 + lane] = normalised<kBf16>(o, sum);
-  }
+  float* ow = reinterpret_cast<float*>(smem) + warp * H * kPad;          // [kWarps][H][kPad]
+  float* mw = reinterpret_cast<float*>(smem) + kWarps * H * kPad + warp * 2 * H;  // [kWarps][m, l][H]
+  stash<NT>(A, ow, mw, mw + H);
+  __syncwarp();
+  for (int h = 0; h < a.G; ++h)
+    out[(warp * a.G + h) * 32 + lane] =
+        normalised<kBf16>(*reinterpret_cast<const float4*>(ow + h * kPad + 4 * lane), mw[H + h]);
 }
 
-template <int NT, int HC, bool kBf16>
+template <int NT, bool kBf16>
 cudaError_t rows_go(const PagedArgs& a, long long ctas, cudaStream_t st) {
-  auto kernel = sparse_paged_kv8_rows_kernel<NT, HC, kBf16>;
-  constexpr int merge = kWarps * 8 * NT * (kPad + 2) * 4;
-  constexpr int smem = RowsSmem<HC>::bytes > merge ? RowsSmem<HC>::bytes : merge;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<static_cast<unsigned>(ctas), kThreads, smem, st>>>(a);
+  auto kernel = sparse_paged_kv8_rows_kernel<NT, kBf16>;
+  static_assert(kRowsSmem >= kWarps * 8 * NT * (kPad + 2) * 4, "the output buffers fit");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(ctas), kThreads, kRowsSmem, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int NT, bool kBf16>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();  // CTAs resident at once
-  // KV heads share a CTA where that leaves a few waves of CTAs.
-  if (a.Hkv % 4 == 0 && pairs / 4 >= 4 * slots) return rows_go<NT, 4, kBf16>(a, pairs / 4, st);
-  if (a.Hkv % 2 == 0 && pairs / 2 >= 4 * slots) return rows_go<NT, 2, kBf16>(a, pairs / 2, st);
+  // Four KV heads share a CTA from two waves of such CTAs on: 2 x 700 rows of 4 heads (2.3 waves) took 203 us instead of
+  // 224, 2 x 350 (1.2 waves) 146 instead of 127.  (Two heads a CTA, two warps each, took as long as one: 223 us.)
+  if (a.Hkv % kWarps == 0 && pairs / kWarps >= 2 * slots) return rows_go<NT, kBf16>(a, pairs / kWarps, st);
   // Otherwise as many CTAs per pair as stay resident at once, at most one per 128 entries of the list.
   const int most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
   a.split = static_cast<int>(std::max<long long>(1, std::min<long long>(most, slots / pairs)));

@@ -176,6 +176,42 @@ def test_append_heads(block, D, rot, Hq, Hkv):
     check(c, rot, out, dense=False)
 
 
+@pytest.mark.parametrize("S", (2, 5, 15, 16, 17))
+@pytest.mark.parametrize("D,block", [(128, 0), (64, 16), (128, 8), (64, 64)])
+def test_append_short_chunks(S, D, block):
+    """Chunks shorter than a warp's group of rows, at every offset of a block."""
+    ctx = tuple(200 + 3 * i for i in range(12))
+    c = make(torch.bfloat16, D, 5, 1, S, ctx, (S,) * 12, block, tail=16, seed=S + D)
+    check(c, 32, run(c, 32))
+
+
+def test_append_many_sequences():
+    """More sequences than CTAs at once, one token each."""
+    c = make(torch.float16, 128, 2, 1, 1, tuple(1 + (7 * i) % 100 for i in range(1500)), None, 16, seed=6)
+    check(c, 64, run(c, 64))
+
+
+@pytest.mark.parametrize("block", (0, 16, 32))
+def test_append_many_heads(block):
+    """More K and V heads than a CTA shares a wide block's maxima of."""
+    c = make(torch.float16, 64, 3, 270, 3, (3, 37), (3, 2), block, seed=7)
+    check(c, 32, run(c, 32, dense=False), dense=False)
+
+
+@pytest.mark.parametrize("block", (0, 16, 64))
+def test_append_again(block):
+    """The same tokens a second time, as after a rejected draft, leave the same cache and scales."""
+    c = make(torch.float16, 128, 8, 2, 20, (20, 75), (20, 20), block, seed=13)
+    c["qkv"][:, :, 10:] *= 50  # V outgrows the older tokens' scale
+    first = run(c, 64)
+    c["pool"] = first[3]
+    if block:
+        c["scale"] = first[4]
+    again = run(c, 64)
+    for a, b in zip(first, again):
+        assert (a is None and b is None) or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_append_many_tiles():
     """More tiles than the GPU holds at once, and a whole prompt far from position 0."""
     c = make(torch.bfloat16, 128, 8, 1, 2100, (2100, 65536, 1999, 2100), (2100, 2100, 1999, 700), 16, seed=5)
