@@ -30,6 +30,7 @@
 // a register holds four keys of one dim.  The rows of S^T are the keys in the
 // order that makes its columns the second product's fragments of P^T.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <utility>
 
@@ -773,29 +774,57 @@ cudaError_t rows_go(const PagedArgs& a, long long ctas, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <int NT>
+cudaLaunchConfig_t split_config(long long pairs, int split, cudaStream_t st, cudaLaunchAttribute* at) {
+  static_assert(kSmem<NT> <= 48 * 1024, "no attribute is set");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem<NT>;
+  cfg.stream = st;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = split;
+  at->val.clusterDim.y = 1;
+  at->val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cfg;
+}
+
+// Clusters of `split` CTAs that the current device holds at once (a cluster's CTAs lie in one GPC, so this is less than
+// the CTAs allow), asked for once per device.
+template <int NT, bool kBf16>
+long long resident_clusters(int split) {
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];  // 0: not asked yet; -1: none
+  int dev = 0;
+  const bool cached = cudaGetDevice(&dev) == cudaSuccess && dev < kDevices;
+  int n = cached ? known[dev][split].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = split_config<NT>(1, split, nullptr, &at);
+    if (cudaOccupancyMaxActiveClusters(&n, sparse_paged_kv8_split_kernel<NT, kBf16>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();  // a failed query is not the launch's error: this size is just not used
+      n = 0;
+    }
+    n = n < 1 ? -1 : n;
+    if (cached) known[dev][split].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 template <int NT, bool kBf16>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();  // CTAs resident at once
   // Four KV heads share a CTA from two waves of such CTAs on: 2 x 700 rows of 4 heads (2.3 waves) took 203 us instead of
   // 224, 2 x 350 (1.2 waves) 146 instead of 127.  (Two heads a CTA, two warps each, took as long as one: 223 us.)
   if (a.Hkv % kWarps == 0 && pairs / kWarps >= 2 * slots) return rows_go<NT, kBf16>(a, pairs / kWarps, st);
-  // Otherwise as many CTAs per pair as stay resident at once, at most one per 128 entries of the list.
-  const int most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
-  a.split = static_cast<int>(std::max<long long>(1, std::min<long long>(most, slots / pairs)));
+  // Otherwise as many CTAs per pair as leave all clusters resident at once, at most one per 128 entries of the list.
+  a.split = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
+  while (a.split > 1 && pairs > resident_clusters<NT, kBf16>(a.split)) --a.split;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = split_config<NT>(pairs, a.split, st, &at);
   auto kernel = sparse_paged_kv8_split_kernel<NT, kBf16>;
-  static_assert(kSmem<NT> <= 48 * 1024, "no attribute is set");
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem<NT>;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = a.split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = a.split > 1 ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
