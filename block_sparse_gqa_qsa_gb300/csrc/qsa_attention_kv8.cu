@@ -20,8 +20,9 @@
 // page ids, scales) has a step or more to arrive; the 32 K and V rows of 128
 // bytes are gathered with cp.async into the warp's own K tile and V tile.  A
 // step's K tile is free after its first product, its V tile after the second,
-// and the next step's rows start then: one tile of each keeps half a step of
-// copies in flight per warp.
+// and the rows of the next step (many rows: one tile of each, half a step of
+// copies in flight per warp, which 16 warps cover) or of the one after it (few
+// pairs: two of each, more in flight where latency decides) start then.
 //
 // S^T = C^K Q^T and O^T += (C^V)^T P^T are m16n8k16 MMAs in fp16 with the head
 // group as N; codes are converted to fp16 pairs in registers (exact).  The
@@ -45,8 +46,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kD = 128;
 constexpr int kStep = 32;                      // list entries of a warp's step
 constexpr int kTileBytes = kStep * kD;         // K (or V) rows of a step
-// A warp's shared memory: a K tile, a V tile, the pool rows of two steps' entries (K then V), a step's Entry values.
-constexpr int kRowsAt = 2 * kTileBytes;
+// A warp's shared memory in the split form: two K tiles, two V tiles, the pool rows of two steps' entries (K then V), the
+// values of a step's entries.
+constexpr int kRowsAt = 4 * kTileBytes;
 constexpr int kEntriesAt = kRowsAt + 2 * 2 * kStep * 4;
 constexpr int kWarpBytes = kEntriesAt + kStep * 16;
 constexpr int kMaxCluster = 8;
@@ -334,8 +336,12 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
 
 constexpr int kPad = kD + 4;  // floats of a head in the merge buffers
 
-// Resident CTAs per SM: the register budget decides (5 at 96 registers spill and took 1333 us for an 8192-row prompt
-// against 1275; 16-head groups at 168 registers 2008 against 1928).
+// Resident CTAs per SM.  Many rows: the register budget decides (5 at 96 registers spill and took 1333 us for an 8192-row
+// prompt against 1275 with 4; 16-head groups at 168 registers 2008 against 1928 with 2).  Split: two tiles of each kind per
+// warp (69 KB a CTA) rather than a fourth CTA with one: decode of 8, 16, 38, 64, 200 sequences with 4 KV heads took 7.0,
+// 9.7, 18.3, 26.4, 70.6 us instead of 7.5, 10.5, 19.8, 29.1, 78.1, of 32 sequences 17.1 either way.
+template <int NT>
+constexpr int kSplitCtasPerSm = NT == 1 ? 3 : 2;
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
 // The tiles, and later the merge buffers: the warps' O, m and l, then the CTA's.
@@ -504,7 +510,7 @@ __device__ __forceinline__ uint2 normalised(const float4& o, float sum) {
 
 // Few (row, KV head) pairs: the warps of a CTA, and the CTAs of a cluster, share one pair's list.
 template <int NT, bool kBf16>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_split_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv8_split_kernel(const PagedArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x % a.split);
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_spl
     return;
   }
   uint8_t* mine = smem + warp * kWarpBytes;
-  const uint32_t ktile = smem_addr(mine), vtile = ktile + kTileBytes;
+  const uint32_t ktile = smem_addr(mine), vtile = ktile + 2 * kTileBytes;
   int* ids = reinterpret_cast<int*>(mine + kRowsAt);  // [step & 1][K, V][row_place]
   float4* entries = reinterpret_cast<float4*>(mine + kEntriesAt);
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
@@ -545,47 +551,57 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_spl
     return n;
   };
   auto gather = [&](int parity, int plane, unsigned mask) {
-    gather_rows(ids + (parity * 2 + plane) * kStep, mask, plane ? dst.v : dst.k, base, rowBytes);
+    const uint32_t o = parity * kTileBytes;
+    const uint32_t d[2] = {(plane ? dst.v[0] : dst.k[0]) + o, (plane ? dst.v[1] : dst.k[1]) + o};
+    gather_rows(ids + (parity * 2 + plane) * kStep, mask, d, base, rowBytes);
   };
 
   Acc<NT> A;
   acc_init(A);
   const int steps = max(0, (a.topK - (first - lane) + hop - 1) / hop);
   Named cur = resolve(list.pages_of(j0), 0);
+  Pages p1 = list.pages_of(j1);
   __syncwarp();
   gather(0, 0, cur.mask);
   gather(0, 1, cur.mask);
-  Pages p1 = list.pages_of(j1);
+  slot += hop;
+  int j3 = list.at(slot);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
   load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, qf, qs);
+  Named next = resolve(p1, 1);
+  p1 = list.pages_of(j2);
+  __syncwarp();
+  gather(1, 0, next.mask);
+  gather(1, 1, next.mask);
   for (int i = 0; i < steps; ++i) {
-    const int par = (i + 1) & 1;
-    const Named next = resolve(p1, par);
-    p1 = list.pages_of(j2);
+    const int par = i & 1;
+    const Named then = resolve(p1, par);  // step i + 2: its rows go where step i's are
+    p1 = list.pages_of(j3);
     slot += hop;
-    j2 = list.at(slot);
+    j3 = list.at(slot);
     if (cur.mask) {
       entries[lane] = entry_of(a, cur.ok, cur.ks, cur.vs);
       float s[2][NT][4];
       uint32_t pb[2][NT][2];
-      cp_async_wait<1>();  // this lane's share of the K tile; the V tile may be in flight
+      cp_async_wait<3>();  // this lane's share of the K tile; its V tile and the next step's two may be in flight
       __syncwarp();
-      scores32<NT>(s, ktile, qf);
+      scores32<NT>(s, ktile + par * kTileBytes, qf);
       __syncwarp();  // every lane is done with the K tile
-      gather(par, 0, next.mask);
+      gather(par, 0, then.mask);
       softmax32<NT, kBf16>(A, s, qs, entries, pb);
-      cp_async_wait<1>();  // the V tile; the next K tile may be in flight
+      cp_async_wait<3>();  // the V tile
       __syncwarp();
-      values32<NT>(A, vtile, pb);
+      values32<NT>(A, vtile + par * kTileBytes, pb);
       __syncwarp();  // every lane is done with the V tile
-      gather(par, 1, next.mask);
+      gather(par, 1, then.mask);
     } else {  // nothing was copied for this step
       __syncwarp();
-      gather(par, 0, next.mask);
-      gather(par, 1, next.mask);
+      gather(par, 0, then.mask);
+      gather(par, 1, then.mask);
     }
     cur = next;
+    next = then;
   }
   cp_async_wait<0>();
   list.report();
@@ -776,7 +792,6 @@ cudaError_t rows_go(const PagedArgs& a, long long ctas, cudaStream_t st) {
 
 template <int NT>
 cudaLaunchConfig_t split_config(long long pairs, int split, cudaStream_t st, cudaLaunchAttribute* at) {
-  static_assert(kSmem<NT> <= 48 * 1024, "no attribute is set");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs * split));
   cfg.blockDim = dim3(kThreads);
@@ -792,7 +807,7 @@ cudaLaunchConfig_t split_config(long long pairs, int split, cudaStream_t st, cud
 }
 
 // Clusters of `split` CTAs that the current device holds at once (a cluster's CTAs lie in one GPC, so this is less than
-// the CTAs allow), asked for once per device.
+// the CTAs allow), asked for once per device, when the kernel's shared memory is allowed too.
 template <int NT, bool kBf16>
 long long resident_clusters(int split) {
   constexpr int kDevices = 16;
@@ -803,7 +818,9 @@ long long resident_clusters(int split) {
   if (n == 0) {
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = split_config<NT>(1, split, nullptr, &at);
-    if (cudaOccupancyMaxActiveClusters(&n, sparse_paged_kv8_split_kernel<NT, kBf16>, &cfg) != cudaSuccess) {
+    auto kernel = sparse_paged_kv8_split_kernel<NT, kBf16>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<NT>) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();  // a failed query is not the launch's error: this size is just not used
       n = 0;
     }
@@ -821,11 +838,16 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   if (a.Hkv % kWarps == 0 && pairs / kWarps >= 2 * slots) return rows_go<NT, kBf16>(a, pairs / kWarps, st);
   // Otherwise as many CTAs per pair as leave all clusters resident at once, at most one per 128 entries of the list.
   a.split = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
-  while (a.split > 1 && pairs > resident_clusters<NT, kBf16>(a.split)) --a.split;
+  while (pairs > resident_clusters<NT, kBf16>(a.split) && a.split > 1) --a.split;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = split_config<NT>(pairs, a.split, st, &at);
   auto kernel = sparse_paged_kv8_split_kernel<NT, kBf16>;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
+  if (e == cudaErrorInvalidValue) {  // the attribute is the context's: a new one has not got it
+    (void)cudaGetLastError();
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<NT>);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const PagedArgs>(a));
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
