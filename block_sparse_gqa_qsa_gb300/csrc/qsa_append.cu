@@ -514,8 +514,9 @@ cudaError_t append_go(AppendArgs a, int B, cudaStream_t st) {
   const size_t smem = kWarps * 2 * static_cast<size_t>(a.slotRows) * (D * 2) +
                       static_cast<size_t>(rows + RPI) * (a.rot / 2) * 8;
   if (smem > 40 * 1024) {  // past what a kernel may have without asking (48 KB, the static arrays among it)
-    const cudaError_t attr =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // always the most that any call needs: another thread may launch the same kernel between this and the launch
+    constexpr int kMost = kWarps * 2 * kTile * D * 2 + (kTokensPerPage + RPI) * (D / 2) * 8;
+    const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (attr != cudaSuccess) return attr;
   }
   kernel<<<dim3(static_cast<unsigned>(tiles), parts), kThreads, smem, st>>>(a);

@@ -276,6 +276,43 @@ def test_large_bf16_values():
     assert bool((err <= step_of(small[0].double(), torch.bfloat16)).all())
 
 
+def test_calls_from_many_threads():
+    """Calls whose kernels need different amounts of shared memory, from several threads at once."""
+    import ctypes
+    import threading
+    cases = [(make(torch.float16, 128, 4, 2, 140, (140,), None, 128, seed=20), 128),
+             (make(torch.float16, 128, 4, 2, 40, (140,), None, 16, seed=21), 16)]
+    want = [run(c, rot, dense=False)[0] for c, rot in cases]
+    fn = qb.lib().qsa_append_kv8
+    bad = []
+
+    def loop(i):
+        c, rot = cases[i % 2]
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            t = {n: c[n].to(DEV) for n in ("qkv", "wq", "wk", "ctx", "pool", "scale", "pt")}
+            q = torch.empty((1, c["S"], 4, 128), dtype=torch.float16, device=DEV)
+        st.synchronize()
+        p = qb.QsaAppendKvParams(
+            qkv=t["qkv"].data_ptr(), qNormW=t["wq"].data_ptr(), kNormW=t["wk"].data_ptr(),
+            contextLengths=t["ctx"].data_ptr(), qOut=q.data_ptr(), kvPool=t["pool"].data_ptr(),
+            kvScale=t["scale"].data_ptr(), pageTable=t["pt"].data_ptr(), batchSize=1, seqLen=c["S"], numQHeads=4,
+            numKVHeads=2, headDim=128, rotDim=rot, poolHeadDim=128, numFlatPages=c["pool"].shape[0],
+            maxPagesPerSeq=c["pt"].shape[2], scaleBlock=c["block"], ropeTheta=ref.THETA, rmsNormEps=ref.EPS,
+            stream=st.cuda_stream)
+        errors = sum(fn(ctypes.byref(p)) != 0 for _ in range(10000))
+        st.synchronize()
+        if errors or not torch.equal(q.cpu().view(torch.int16), want[i % 2].view(torch.int16)):
+            bad.append((i, errors))
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
 @pytest.mark.parametrize("block", (0, 16, 64))
 def test_bad_pages(block):
     """Page ids outside the pool and positions behind the table: skipped, reported, the rest written."""
