@@ -105,20 +105,20 @@ __device__ __forceinline__ float mean_square(const Chunks& x) {
 // (sin, sin) of elements 2k, 2k + 1 (lanes past rotDim get (1, 1), (0, 0)).
 template <int D, bool kBf16>
 __device__ __forceinline__ void norm_rotate(Chunks& x, const Chunks& w, float eps, const ulonglong2* cs, int hop) {
-  float m = mean_square<D>(x) + eps, back = 1.0f;
-  if (kBf16 && __any_sync(kFull, m == INFINITY)) {  // squares past fp32: the same on values scaled by 2^-64
-    Chunks z;
+  float m = mean_square<D>(x) + eps;
+  if constexpr (kBf16) {  // squares past fp32's range, or below it beside a small eps: the same on scaled values
+    if (__any_sync(kFull, m == INFINITY || m < 0x1p-90f)) {
+      const float f = m == INFINITY ? 0x1p-64f : m < 0x1p-90f ? 0x1p100f : 1.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      z.a[k] = fmul2(x.a[k], pack_f2(0x1p-64f, 0x1p-64f));
-      z.b[k] = fmul2(x.b[k], pack_f2(0x1p-64f, 0x1p-64f));
+      for (int k = 0; k < 4; ++k) {
+        x.a[k] = fmul2(x.a[k], pack_f2(f, f));
+        x.b[k] = fmul2(x.b[k], pack_f2(f, f));
+      }
+      m = mean_square<D>(x) + eps * f * f;
     }
-    const float ms = mean_square<D>(z);  // eps is nothing beside squares of 2^128
-    back = m == INFINITY ? 0x1p-64f : 1.0f;
-    m = m == INFINITY ? ms : m;
   }
   const float r = rsqrtf(m);
-  const float inv = back * r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
+  const float inv = r * fmaf(-0.5f * m * r, r, 1.5f);  // one Newton step: a few units of 2^-24
   const uint64_t inv2 = pack_f2(inv, inv);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {

@@ -424,7 +424,8 @@ QSA_API size_t qsa_gather_scratch_elems(int32_t batchSize, int32_t numKVHeads, i
  * i.e. a prefill from position 0, or one token when seqLen is 1).  Row t < n
  * is the token at position p = L - n + t:
  *   q/k heads: y = x / sqrt(mean(x^2) + eps) * (1 + w), then the half-split
- *              rotation of dims [0, rotDim) at p, in fp32;
+ *              rotation of dims [0, rotDim) at p, in fp32 (all NaN if an x is
+ *              infinite or NaN);
  *   v heads:   as they are.
  * qOut gets the q heads, rounded once; kOut / vOut (dense mirrors, NULL for
  * none) the k heads, rounded once, and the v heads.  Rows t >= n are padding:

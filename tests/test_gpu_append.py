@@ -46,7 +46,7 @@ def make(dtype, D, Hq, Hkv, S, ctx, new, block, extra=0, tail=0, seed=0):
     return c
 
 
-def run(c, rot, dense=True, status=None, stream=None):
+def run(c, rot, dense=True, status=None, stream=None, eps=ref.EPS):
     """The call on the GPU; returns q, k, v, pool, scale on the CPU."""
     B, S, D, Hq, Hkv = len(c["n"]), c["S"], c["D"], c["Hq"], c["Hkv"]
     et = c["qkv"].dtype
@@ -54,7 +54,7 @@ def run(c, rot, dense=True, status=None, stream=None):
     k, v = (torch.full((B, S, Hkv, D), float("nan"), dtype=et, device=DEV) if dense else None for _ in range(2))
     pool = c["pool"].to(DEV)
     new = None if c["new"] is None else c["new"].to(DEV)
-    kw = dict(Hq=Hq, Hkv=Hkv, rot=rot, theta=ref.THETA, eps=ref.EPS, new_lengths=new, k_out=k, v_out=v, status=status,
+    kw = dict(Hq=Hq, Hkv=Hkv, rot=rot, theta=ref.THETA, eps=eps, new_lengths=new, k_out=k, v_out=v, status=status,
               stream=stream)
     a = (c["qkv"].to(DEV), c["wq"].to(DEV), c["wk"].to(DEV), c["ctx"].to(DEV), q, pool)
     if c["block"]:
@@ -274,6 +274,42 @@ def test_large_bf16_values():
     # eps is 1e-6 of a mean square near 1: 5e-7 relative, under a quarter of which rounds differently
     err = (big[0].double() - small[0].double()).abs()
     assert bool((err <= step_of(small[0].double(), torch.bfloat16)).all())
+
+
+@pytest.mark.parametrize("e,eps", [(-110, 0.0), (-60, 1e-37)])
+@pytest.mark.parametrize("block", (0, 16))
+def test_small_bf16_values(block, e, eps):
+    """Squares below fp32's range without an eps, and near its end with one of their size."""
+    c = make(torch.bfloat16, 128, 4, 1, 9, (9,), None, block)
+    rows = c["qkv"][0].double()
+    c["qkv"] = (c["qkv"].float() * 2.0 ** e).bfloat16()  # exact
+    q, k = run(c, 64, eps=eps)[:2]
+    # the same numbers from rows scaled so that EPS is to them what eps is to these (for 0: 2^-100 of their mean square)
+    f = 2.0 ** e * (ref.EPS / eps) ** 0.5 if eps else 2.0 ** 40
+    for got, want in ((q, ref.normed_rotated(rows[:, :4] * f, c["wq"], torch.arange(9), 64)),
+                      (k, ref.normed_rotated(rows[:, 4:5] * f, c["wk"], torch.arange(9), 64))):
+        check_dense(got[0], want, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("block", (0, 16))
+def test_rows_that_are_no_numbers(block, dtype):
+    """A q or k row with an infinity or a NaN comes out as NaN; its neighbours are unharmed, in an 8-bit block too."""
+    c = make(dtype, 128, 4, 2, 20, (20,), None, block)
+    clean = run(c, 64)
+    c["qkv"][0, 3, 1, 100], c["qkv"][0, 9, 4, 7] = float("inf"), float("nan")
+    q, k, v, pool, scale = run(c, 64)
+    assert bool(q[0, 3, 1].isnan().all()) and bool(k[0, 9, 0].isnan().all())
+    for got, was, at in ((q, clean[0], (0, 3, 1)), (k, clean[1], (0, 9, 0))):
+        got[at], was = 0, was.clone()
+        was[at] = 0
+        assert torch.equal(got.view(torch.int16), was.view(torch.int16))
+    page = int(c["pt"][0, 0, 0])
+    row = pool.view(torch.uint8)[page, 9, 0, :128] & 0x7f if block else pool[page, 9, 0, :128]
+    assert bool((row == 0x7f).all()) if block else bool(row.isnan().all())
+    if block:
+        amax = k[0, :16, 0].double().abs().amax()  # the NaN row was set to zeros above
+        assert abs(float(scale[page, 0, 0]) - float(amax) / 448) <= step_of(amax, dtype) / 448
 
 
 def test_calls_from_many_threads():
