@@ -14,7 +14,7 @@
 // Two kernels share the arithmetic.  With few (row, KV head) pairs, a CTA of 4
 // warps takes one, or a cluster of up to 8 CTAs shares it, the list dealt out
 // to the warps in steps of 32 entries; with many, a CTA takes four KV heads of a
-// row, a warp each, and resolves the list once for all four.
+// row (or two of two rows), a warp each, and resolves a list once for its heads.
 //
 // A warp runs its steps by itself.  Every dependent load of a step (list entry,
 // page ids, scales) has a step or more to arrive; the 32 K and V rows of 128
@@ -656,55 +656,73 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
-// Many rows: a CTA takes four KV heads of a row, a warp one head and the whole list.  The heads share the list, so its
-// entries are resolved once for all of them, 128 at a time and 32 per warp: row ids, and per head what the softmax needs,
-// go to shared memory for every warp.  Chunk c + 1's row ids are written before the barrier that opens chunk c (its first
-// rows are gathered in chunk c's last step), its scales, which are loaded meanwhile, behind chunk c's steps.
-constexpr int kChunk = kStep * kWarps;                             // entries
-constexpr int kIdsAt = kWarps * 2 * kTileBytes;                    // [chunk % 3][step][K, V][kStep] row ids
-constexpr int kMasksAt = kIdsAt + 3 * kChunk * 2 * 4;              // [chunk % 3][step] entries that name a row
-constexpr int kChunkEntriesAt = kMasksAt + 64;                     // [chunk & 1][head][kChunk]
-constexpr int kRowsSmem = kChunkEntriesAt + 2 * kWarps * kChunk * 16;
+// Many rows: a warp takes one KV head of a row and the whole list, a group of kH warps (4 or 2) kH heads of the row, a CTA
+// 4 / kH groups.  The heads share the list, so a group's warps resolve its entries once for all of them, a chunk of 32 kH
+// at a time, 32 per warp: row ids, and per head what the softmax needs, go to shared memory for every warp of the group.  Chunk c + 1's row ids are written before the barrier that opens chunk c (its first rows are
+// gathered in chunk c's last step), its scales, which are loaded meanwhile, behind chunk c's steps.  Groups share
+// nothing: each has a barrier of its own and leaves when it is done.
+template <int NT>
+constexpr int kWarpTiles = 2 * kTileBytes > 8 * NT * (kPad + 2) * 4 ? 2 * kTileBytes : 8 * NT * (kPad + 2) * 4;  // later: O, m, l
+template <int NT>
+constexpr int kIdsAt = kWarps * kWarpTiles<NT>;                    // [chunk % 3][warp's step][K, V][kStep] row ids
+template <int NT>
+constexpr int kMasksAt = kIdsAt<NT> + 3 * kWarps * kStep * 2 * 4;  // [chunk % 3][warp's step] entries that name a row
+template <int NT>
+constexpr int kChunkEntriesAt = kMasksAt<NT> + 64;                 // [chunk & 1][warp][kH kStep]
+template <int NT, int kH>
+constexpr int kRowsSmem = kChunkEntriesAt<NT> + 2 * kWarps * kH * kStep * 16;
 
-template <int NT, bool kBf16>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_rows_kernel(const PagedArgs a) {
+template <int NT, bool kBf16, int kH>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_rows_kernel(const PagedArgs a, int items) {
+  constexpr int kChunk = kH * kStep;  // entries
   extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Row r = row_of(a, static_cast<int>(blockIdx.x), kWarps);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / kH, w0 = group * kH;          // this group and its first warp
+  const int tid = static_cast<int>(threadIdx.x) - w0 * 32;  // within the group
+  const int item = static_cast<int>(blockIdx.x) * (kWarps / kH) + group;
+  if (item >= items) return;
+  auto group_sync = [&] {
+    if (group == 0)
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kH) : "memory");
+    else
+      asm volatile("bar.sync 2, %0;\n" ::"n"(32 * kH) : "memory");
+  };
+  Row r = row_of(a, item, kH);
   List list(a, r);
   const int j0 = list.at(tid), j1 = list.at(tid + kChunk);
   int slot = tid + 2 * kChunk, j2 = list.at(slot);
   row_lengths(a, r);
   list.L = r.L;
-  uint2* out = static_cast<uint2*>(a.o) + r.head0 * (kD / 4);  // kWarps G heads of 4 values each
+  uint2* out = static_cast<uint2*>(a.o) + r.head0 * (kD / 4);  // kH G heads of 4 values each
   if (r.t >= r.n) {
-    for (int e = tid; e < kWarps * a.G * kD / 8; e += kThreads) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
+    for (int e = tid; e < kH * a.G * kD / 8; e += 32 * kH) reinterpret_cast<uint4*>(out)[e] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const uint32_t ktile = smem_addr(smem) + warp * 2 * kTileBytes, vtile = ktile + kTileBytes;
-  int* ids = reinterpret_cast<int*>(smem + kIdsAt);
-  unsigned* masks = reinterpret_cast<unsigned*>(smem + kMasksAt);
-  float4* entries = reinterpret_cast<float4*>(smem + kChunkEntriesAt);
+  uint8_t* mine = smem + warp * kWarpTiles<NT>;
+  const uint32_t ktile = smem_addr(mine), vtile = ktile + kTileBytes;
+  int* ids = reinterpret_cast<int*>(smem + kIdsAt<NT>) + w0 * 2 * kStep;
+  unsigned* masks = reinterpret_cast<unsigned*>(smem + kMasksAt<NT>) + w0;
+  float4* entries = reinterpret_cast<float4*>(smem + kChunkEntriesAt<NT>) + w0 * kChunk;
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
-  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + warp) * a.poolHeadDim + (lane & 7) * 16;
+  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + warp - w0) * a.poolHeadDim + (lane & 7) * 16;
   const TileDst dst(ktile, vtile);
 
   struct Scales {
     bool ok;
-    float k[kWarps], v[kWarps];
+    float k[kH], v[kH];
   };
   auto put_rows = [&](const Pages& p, int buf) {  // row ids of the thread's entry of a chunk, and its scales' loads
     const PoolRows rows = list.rows_of(p);
-    int* at = ids + (buf * kWarps + warp) * 2 * kStep + row_place(lane);
+    int* at = ids + (buf * kWarps + warp - w0) * 2 * kStep + row_place(lane);
     at[0] = rows.ok ? rows.k : -1;
     at[kStep] = rows.ok ? rows.v : -1;
     const unsigned mask = __ballot_sync(kFull, rows.ok);
-    if (lane == 0) masks[buf * kWarps + warp] = mask;
+    if (lane == 0) masks[buf * kWarps + warp - w0] = mask;
     Scales s;
     s.ok = rows.ok;
     const float *ks = scales_of(a, rows.k, r.kvh), *vs = scales_of(a, rows.v, r.kvh);
 #pragma unroll
-    for (int c = 0; c < kWarps; ++c) {
+    for (int c = 0; c < kH; ++c) {
       s.k[c] = __ldg(ks + c);
       s.v[c] = __ldg(vs + c);
     }
@@ -712,21 +730,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
   };
   auto put_entries = [&](const Scales& s, int buf) {
 #pragma unroll
-    for (int c = 0; c < kWarps; ++c) entries[(buf * kWarps + c) * kChunk + tid] = entry_of(a, s.ok, s.k[c], s.v[c]);
+    for (int c = 0; c < kH; ++c) entries[(buf * kWarps + c) * kChunk + tid] = entry_of(a, s.ok, s.k[c], s.v[c]);
   };
   auto gather = [&](int buf, int step, int plane, unsigned mask) {
     gather_rows(ids + ((buf * kWarps + step) * 2 + plane) * kStep, mask, plane ? dst.v : dst.k, base, rowBytes);
   };
-
   Acc<NT> A;
   acc_init(A);
   Scales sc = put_rows(list.pages_of(j0), 0);
   Pages p1 = list.pages_of(j1);
   uint32_t qf[NT][8][2];
   float qs[NT][2];
-  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + warp * a.G) * (kD / 8), a.G, qf, qs);
+  load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + (warp - w0) * a.G) * (kD / 8), a.G, qf, qs);
   put_entries(sc, 0);
-  __syncthreads();
+  group_sync();
   unsigned mask = masks[0];  // of the current step, whose rows are gathered
   gather(0, 0, 0, mask);
   gather(0, 0, 1, mask);
@@ -738,10 +755,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
     p1 = list.pages_of(j2);
     slot += kChunk;
     j2 = list.at(slot);
-    __syncthreads();
+    group_sync();
 #pragma unroll 1
-    for (int e = 0; e < kWarps; ++e) {
-      const bool last = e == kWarps - 1;
+    for (int e = 0; e < kH; ++e) {
+      const bool last = e == kH - 1;
       const int gbuf = last ? nbuf : buf, ge = last ? 0 : e + 1;  // the next step
       const unsigned next = masks[gbuf * kWarps + ge];
       if (mask) {
@@ -752,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
         scores32<NT>(s, ktile, qf);
         __syncwarp();  // every lane is done with the K tile
         gather(gbuf, ge, 0, next);
-        softmax32<NT, kBf16>(A, s, qs, entries + ((c & 1) * kWarps + warp) * kChunk + e * kStep, pb);
+        softmax32<NT, kBf16>(A, s, qs, entries + ((c & 1) * kWarps + warp - w0) * kChunk + e * kStep, pb);
         cp_async_wait<1>();  // the V tile; the next K tile may be in flight
         __syncwarp();
         values32<NT>(A, vtile, pb);
@@ -769,24 +786,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv8_row
   }
   cp_async_wait<0>();
   list.report();
-  __syncthreads();  // the tiles become output buffers
+  __syncwarp();  // the warp's tiles become its output buffer
   constexpr int H = 8 * NT;
-  float* ow = reinterpret_cast<float*>(smem) + warp * H * kPad;          // [kWarps][H][kPad]
-  float* mw = reinterpret_cast<float*>(smem) + kWarps * H * kPad + warp * 2 * H;  // [kWarps][m, l][H]
+  float* ow = reinterpret_cast<float*>(mine);  // [H][kPad]
+  float* mw = ow + H * kPad;                   // [m, l][H]
   stash<NT>(A, ow, mw, mw + H);
   __syncwarp();
   for (int h = 0; h < a.G; ++h)
-    out[(warp * a.G + h) * 32 + lane] =
+    out[((warp - w0) * a.G + h) * 32 + lane] =
         normalised<kBf16>(*reinterpret_cast<const float4*>(ow + h * kPad + 4 * lane), mw[H + h]);
 }
 
-template <int NT, bool kBf16>
-cudaError_t rows_go(const PagedArgs& a, long long ctas, cudaStream_t st) {
-  auto kernel = sparse_paged_kv8_rows_kernel<NT, kBf16>;
-  static_assert(kRowsSmem >= kWarps * 8 * NT * (kPad + 2) * 4, "the output buffers fit");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
+template <int NT, bool kBf16, int kH>
+cudaError_t rows_go(const PagedArgs& a, long long pairs, cudaStream_t st) {
+  auto kernel = sparse_paged_kv8_rows_kernel<NT, kBf16, kH>;
+  constexpr int kSmemBytes = kRowsSmem<NT, kH>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(ctas), kThreads, kRowsSmem, st>>>(a);
+  kernel<<<static_cast<unsigned>((pairs + kWarps - 1) / kWarps), kThreads, kSmemBytes, st>>>(
+      a, static_cast<int>(pairs / kH));
   return cudaGetLastError();
 }
 
@@ -833,9 +851,13 @@ long long resident_clusters(int split) {
 template <int NT, bool kBf16>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();  // CTAs resident at once
-  // Four KV heads share a CTA from two waves of such CTAs on: 2 x 700 rows of 4 heads (2.3 waves) took 203 us instead of
-  // 224, 2 x 350 (1.2 waves) 146 instead of 127.  (Two heads a CTA, two warps each, took as long as one: 223 us.)
-  if (a.Hkv % kWarps == 0 && pairs / kWarps >= 2 * slots) return rows_go<NT, kBf16>(a, pairs / kWarps, st);
+  // A warp per pair from two waves of such CTAs on: 2 x 700 rows of 4 heads (2.3 waves) took 202 us instead of 224, 2 x 350
+  // (1.2 waves) 146 instead of 127.  With 2 heads 4096 rows (3.4 waves) 294 instead of 301, 8192 618 instead of 657, 12
+  // query heads each 887 instead of 987, but 1100 + 1100 rows (1.8 waves) 213 instead of 198.  (Two warps per pair, four
+  // heads: 223 us where one took 223.  Lists of their own per warp, for odd numbers of heads: 406 us where the split form
+  // took 332, 8192 rows of one head.)
+  if (a.Hkv % 2 == 0 && pairs / kWarps >= 2 * slots)
+    return a.Hkv % 4 == 0 ? rows_go<NT, kBf16, 4>(a, pairs, st) : rows_go<NT, kBf16, 2>(a, pairs, st);
   // Otherwise as many CTAs per pair as leave all clusters resident at once, at most one per 128 entries of the list.
   a.split = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
   while (pairs > resident_clusters<NT, kBf16>(a.split) && a.split > 1) --a.split;

@@ -109,6 +109,16 @@ def test_many_rows(dtype, Hq, Hkv, S, topK):
     assert torch.equal(run(c, status=status), want) and int(status) == 4
 
 
+@pytest.mark.parametrize("dtype,Hq,Hkv", [(torch.float16, 16, 2), (torch.bfloat16, 30, 2), (torch.float16, 6, 6)])
+def test_odd_number_of_rows(dtype, Hq, Hkv):
+    """Two KV heads of two rows per CTA, an odd number of rows (the last CTA has one), some CTAs with one live row."""
+    c = make(dtype, Hq, Hkv, 1301, (1400, 700, 1300), (1300, 501, 1301), 97, 8, seed=Hq)
+    c["lists"][2, 5], c["lists"][2, 8, :96] = -1, -1
+    out = run(c)
+    check(c, out)
+    assert torch.equal(out, run(c))
+
+
 @pytest.mark.parametrize("B", (1, 2, 9, 20, 40, 60, 114, 160))
 def test_cluster_sizes(B):
     """4 KV heads x B pairs: 8 down to 1 CTAs per pair; two runs give the same bits."""
