@@ -53,7 +53,7 @@ struct AppendArgs {
   int tiles;             // tiles per sequence
   int slotRows;          // rows of a ring slot
   int group;             // rows of a q head's item (any head's, for a 16-bit pool)
-  int headsPerCta;
+  int kvCost, unitsPerCta;  // a K or V head's share of a tile's work, a q head's being 1; a CTA's share
   float eps;
   unsigned long long turn[64];  // inv_freq of pair i as a 64-bit fixed-point fraction of a turn
 };
@@ -197,7 +197,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   const int tlo = max(t0, 0);                     // first row of this CTA
   const int thi = min(min(a.S, n), t0 + a.tile);  // past its last live row; the tile's later rows are padding
   const int NH = a.Hq + 2 * a.Hkv;
-  const int h0 = blockIdx.y * a.headsPerCta, h1 = min(NH, h0 + a.headsPerCta);
+  auto head_at = [&](int unit) { return unit <= a.Hq ? unit : a.Hq + (unit - a.Hq) / a.kvCost; };
+  // the dearer K and V heads of small blocks first, where there is more than a wave (4000 rows of 48 heads: 26.2 us, 28.1
+  // with them last)
+  const int part = kKv8 && a.tile == kTile ? gridDim.y - 1 - blockIdx.y : blockIdx.y;
+  const int h0 = head_at(part * a.unitsPerCta), h1 = min(NH, head_at((part + 1) * a.unitsPerCta));
   const bool wide = kKv8 && a.tile > kTile;       // the tile is one block of more than kTile tokens
 
   // padding rows: zeros in the dense outputs, where the tile's lie together
@@ -500,15 +504,18 @@ cudaError_t append_go(AppendArgs a, int B, cudaStream_t st) {
   // call's rows run side by side.
   const long long warps = static_cast<long long>(kCtasPerSm) * kWarps * sms;
   a.group = tiles * NH * ((rows + kTile - 1) / kTile) >= warps ? kTile : RPI;
-  // One CTA per tile when the tiles fill the GPU; otherwise a tile's heads are dealt out to as many CTAs as are resident
-  // at once, down to one item per warp.  (A second wave repeats the tile's table and waits: 4 x 1000 rows took 20.1 us
-  // with four CTAs' worth of parts per SM, 14.5 us with one wave.)
+  // One CTA per tile when the tiles fill the GPU; otherwise a tile's heads are dealt out to about as many CTAs as are
+  // resident at once (to the nearest number, padding rows leave early: 4 x 333..1000 rows of 20 heads took 11.0 us with 512
+  // CTAs, 13.6 with 256), down to one item per warp.  The K and V heads of a block that is passed over twice count twice:
+  // blocks of 32 12.4 us instead of 14.1, of 128 18.5 instead of 22.4, and three times is no better.
   const int perHead = (rows + a.group - 1) / a.group;
   const int most = std::max(1, (NH * perHead + kWarps - 1) / kWarps);
-  int parts = static_cast<int>(std::min<long long>({most, NH, std::max<long long>(1, kCtasPerSm * sms / tiles)}));
-  if (kKv8 && a.tile > kTile) parts = std::max(parts, (NH + kMaxWideHeads - 1) / kMaxWideHeads);
-  a.headsPerCta = (NH + parts - 1) / parts;
-  parts = (NH + a.headsPerCta - 1) / a.headsPerCta;
+  int parts = static_cast<int>(std::min<long long>({most, NH, std::max<long long>(1, (kCtasPerSm * sms + tiles / 2) / tiles)}));
+  a.kvCost = kKv8 && a.tile > kTile ? 2 : 1;
+  const int units = a.Hq + 2 * a.Hkv * a.kvCost;
+  if (kKv8 && a.tile > kTile) parts = std::max(parts, (NH + kMaxWideHeads - 2) / (kMaxWideHeads - 1));
+  a.unitsPerCta = (units + parts - 1) / parts;
+  parts = (units + a.unitsPerCta - 1) / a.unitsPerCta;
   // the warps' rings, and the table of 8 bytes per row and rotated pair (one access of RPI rows past its end)
   a.slotRows = (std::min(kTile, a.S) + RPI - 1) / RPI * RPI;
   const size_t smem = kWarps * 2 * static_cast<size_t>(a.slotRows) * (D * 2) +
