@@ -9,7 +9,7 @@
 // takes the rows of one tile of kTile (or scaleBlock, where that is more)
 // consecutive cache positions, aligned in the page: the tile lies in one page,
 // its cos/sin table is formed once and shared by all heads, and every block of
-// scales lies in one tile, so one warp owns a block and no atomics are needed.
+// scales lies in one tile, so one CTA (of small blocks one warp) owns a block.
 // A warp takes one head of up to 16 of the tile's rows at a time, copied by
 // cp.async into its own two-slot ring in shared memory: the next head's rows
 // travel while this one is computed.  rotDim is a multiple of 16, so a row's
@@ -17,8 +17,9 @@
 // of a first half and its partner chunk (or two chunks past rotDim), so the
 // rotation needs no exchange, and the D/16 lanes of a row reduce its sum of
 // squares with shuffles.  For an 8-bit pool a K or V head is passed over twice
-// in shared memory: its blocks' largest values first, then the codes.  Blocks
-// of more than 16 tokens are copied twice (the second time from L2).
+// in shared memory: its blocks' largest values first, then the codes.  A block
+// of more than 16 tokens is spread over 2 to 8 successive warps, 16 rows each,
+// which join their maxima in shared memory between the two.
 #include <algorithm>
 #include <type_traits>
 
@@ -174,7 +175,8 @@ __device__ __forceinline__ int place(int r, int c) {
   return r * (D / 8) + (D == 128 ? c ^ ((c >> 3) << 2) : c ^ ((r & 1) << 2));
 }
 
-template <int D, bool kBf16, bool kKv8>
+// kWide: the tile is one block of more than kTile tokens of an 8-bit pool.
+template <int D, bool kBf16, bool kKv8, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8;    // chunks per row, lanes that copy one
   constexpr int RPW = 32 / LPR; // rows of a warp-wide copy
@@ -183,8 +185,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   extern __shared__ __align__(16) uint4 smem[];  // [kWarps][2][slotRows][LPR] rows, then the cos/sin table
   __shared__ __align__(16) float w1[2][D];       // 1 + w of q and k heads
   __shared__ ulonglong2 identity;                // the table entry of lanes past rotDim
-  __shared__ int blockMax[kMaxWideHeads];        // blocks above kTile: largest value of each K/V head, as float bits
-  __shared__ float blockInv[kMaxWideHeads];      // and 1 / their scale
+  __shared__ int blockMax[kWide ? kMaxWideHeads : 1];  // largest value of each K/V head's block, as float bits
   const int slotChunks = a.slotRows * LPR;
   ulonglong2* table = reinterpret_cast<ulonglong2*>(smem + kWarps * 2 * slotChunks);  // [live row][4][rot / 16]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,11 +199,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
   const int thi = min(min(a.S, n), t0 + a.tile);  // past its last live row; the tile's later rows are padding
   const int NH = a.Hq + 2 * a.Hkv;
   auto head_at = [&](int unit) { return unit <= a.Hq ? unit : a.Hq + (unit - a.Hq) / a.kvCost; };
-  // the dearer K and V heads of small blocks first, where there is more than a wave (4000 rows of 48 heads: 26.2 us, 28.1
-  // with them last)
-  const int part = kKv8 && a.tile == kTile ? gridDim.y - 1 - blockIdx.y : blockIdx.y;
+  // The dearer K and V heads of small blocks first, where there is more than a wave (4000 rows of 48 heads: 26.0 us, 28.1
+  // with them last).
+  const int part = kKv8 && !kWide ? gridDim.y - 1 - blockIdx.y : blockIdx.y;
   const int h0 = head_at(part * a.unitsPerCta), h1 = min(NH, head_at((part + 1) * a.unitsPerCta));
-  const bool wide = kKv8 && a.tile > kTile;       // the tile is one block of more than kTile tokens
 
   // padding rows: zeros in the dense outputs, where the tile's lie together
   const int tpad = min(a.S, t0 + a.tile), tfirst = max(thi, tlo);
@@ -228,18 +228,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     pg[1] = __ldg(pt + a.maxPagesPerSeq);
   }
 
-  // The work of a CTA, dealt to its warps one item at a time: a head and a group of its rows, `group` rows for a q head
-  // (any head of a 16-bit pool), kTile for a K or V head of an 8-bit pool.  Groups start at the tile's first position.
+  // The work of a CTA, dealt to its warps one item at a time: a head and a group of its rows, kTile for a K or V head of an
+  // 8-bit pool, `group` rows for a q head (any head of a 16-bit pool).  Groups start at the tile's first position.  Wide:
+  // the K and V heads come first, each with a power of two of groups (the last ones may have no live row), so that a head's
+  // groups go to successive warps in the same round.  Otherwise the K and V heads, which take longer, come first where a
+  // CTA has all heads (4 x 16384 rows: 165 us instead of 171), last where it has a few (they wait for the table).
   struct Item {
-    int h, first, rows;  // head, first live row, live rows
+    int h, first, rows;  // head, first live row, live rows (none: <= 0)
   };
   const int hs = kKv8 ? max(h0, min(a.Hq, h1)) : h1;  // heads [h0, hs) take groups of `group` rows, [hs, h1) of kTile
   const int gq0 = (tlo - t0) / a.group, gq = (thi - t0 + a.group - 1) / a.group - gq0;
-  const int gk0 = (tlo - t0) / kTile, gk = (thi - t0 + kTile - 1) / kTile - gk0;
-  const int nq = (hs - h0) * gq, items = nq + (h1 - hs) * gk;
+  const int gk0 = kWide ? (tlo - t0) / kTile : 0, ng = kWide ? (thi - t0 + kTile - 1) / kTile - gk0 : 1;
+  const int gk = ng > 4 ? 8 : ng > 2 ? 4 : ng, nkv = (h1 - hs) * gk, nq = (hs - h0) * gq, items = nq + nkv;
+  const bool kvFirst = kWide || (kKv8 && gridDim.y == 1);
+  const int early = kvFirst ? nkv : nq;  // items of the kind that comes first
   auto item_at = [&](int i) {
-    const bool q = i < nq;
-    const int per = q ? gq : gk, size = q ? a.group : kTile, k = q ? i : i - nq, h = k / per;
+    const bool late = i >= early, q = late == kvFirst;
+    const int per = q ? gq : gk, size = q ? a.group : kTile, k = late ? i - early : i, h = k / per;
     const int base = t0 + (k - h * per + (q ? gq0 : gk0)) * size, first = max(base, tlo);
     return Item{(q ? h0 : hs) + h, first, min(thi, base + size) - first};
   };
@@ -260,16 +265,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
         cp_async16(smem_addr(d + place<D>(r, lane % LPR)), g, true);
     }
   };
-  const int begin = wide ? nq : 0;  // wide blocks: the K and V heads twice, first for their largest values
   Item next{0, 0, 0};  // the item whose rows are in, or on their way to, ring slot `slot`
   int slot = 0;
-  if (begin + warp < items) copy(next = item_at(begin + warp), 0);
+  if (warp < items) copy(next = item_at(warp), 0);
   cp_async_commit();
 
   const int hl = a.rot >> 4;  // chunks of half a rotation
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) w1[i / D][i % D] = 1.0f + __ldg((i < D ? a.qw : a.kw) + i % D);
   if (threadIdx.x == 0) identity = make_ulonglong2(pack_f2(1.f, 1.f), 0);
-  if (wide)
+  if constexpr (kWide)
     for (int i = threadIdx.x; i < h1 - hs; i += kThreads) blockMax[i] = 0;
   if (h0 < a.Hq + a.Hkv)  // V heads need no table
     for (int r = warp; r < thi - tlo; r += kWarps)
@@ -337,11 +341,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     return rm;
   };
   // The scale of a block whose first position is row tb, for a head's largest new value bm: `kept` is its stored scale,
-  // read only if it holds older tokens.  Those keep their scale, or grow it by the smallest power of two that fits.
-  auto new_scale = [&](int tb, float bm, const float* kept, float& shrink) {
+  // used only if it holds older tokens.  Those keep their scale, or grow it by the smallest power of two that fits.
+  auto new_scale = [&](int tb, float bm, float kept, float& shrink) {
     shrink = 1.f;
     if (tb >= 0) return fminf(fmaxf(__fdiv_rn(bm, kE4m3Max), kScaleLo), kScaleHi);
-    const float was = read_scale(*kept);
+    const float was = read_scale(kept);
     const float over = __fdiv_rn(bm, kE4m3Max * was);
     if (!(over > 1.f)) return was;
     const int bits = __float_as_int(over);
@@ -362,6 +366,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
       *row = rescale8(*row, f);
     }
   };
+  // Meeting of the gk warps that share a block of more than kTile tokens.
+  auto block_sync = [&] {
+    if (gk == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + warp / gk), "r"(32 * gk) : "memory");
+  };
   auto weights = [&](int which) {
     if (have == which) return;
     have = which;
@@ -372,52 +383,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     }
   };
 
-  // Runs over this warp's items from `from` on, each with the next one's rows on their way (after the last, item
-  // `then`'s, if there is one).
-  auto run = [&](int from, int then, auto&& f) {
-    for (int i = from + warp; i < items; i += kWarps, slot ^= 1) {
-      const Item it = next;
-      const int after = i + kWarps < items ? i + kWarps : then;
-      if (after >= 0 && after < items) copy(next = item_at(after), slot ^ 1);
-      cp_async_commit();
-      cp_async_wait<1>();
-      __syncwarp();
-      f(it);
-      __syncwarp();  // every lane is done with the slot
-    }
-  };
-
-  if (wide) {
-    run(begin, warp, [&](const Item& it) {
-      const bool isv = it.h >= a.Hq + a.Hkv;
-      if (!isv) weights(1);
-      const float rm = row_maxima(it, slot, isv);
-      if (lane == 0) atomicMax(&blockMax[it.h - hs], __float_as_int(rm));  // of numbers >= 0: whole-number order is theirs
-    });
-    if (begin + warp >= items && warp < items) {  // a warp without such items has not copied its first yet
-      copy(next = item_at(warp), slot);
-      cp_async_commit();
-    }
-    __syncthreads();
-    for (int i = warp; i < h1 - hs; i += kWarps) {
-      const int h = hs + i;
-      const bool isv = h >= a.Hq + a.Hkv;
-      const int hk = isv ? h - a.Hq - a.Hkv : h - a.Hq, pageId = isv ? pg[1] : pg[0];
-      if (pageId < 0) continue;
-      float* sp = scale_at(pageId, t0, hk);
-      float f;
-      const float now = new_scale(t0, __int_as_float(blockMax[i]), sp, f);
-      __syncwarp();  // every lane has read the stored scale
-      if (lane == 0) {
-        *sp = now;
-        blockInv[i] = 1.0f / now;
-      }
-      if (f != 1.f) shrink_older(pageId, hk, f);
-    }
-    __syncthreads();
-  }
-
-  run(0, -1, [&](const Item& it) {
+  // this warp's items, each with the next one's rows on their way
+  for (int i = warp; i < items; i += kWarps, slot ^= 1) {
+    const Item it = next;
+    if (i + kWarps < items) copy(next = item_at(i + kWarps), slot ^ 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncwarp();
     const bool isq = it.h < a.Hq, isv = it.h >= a.Hq + a.Hkv;
     const int hk = isq ? it.h : (isv ? it.h - a.Hq - a.Hkv : it.h - a.Hq);  // among the q, k or v heads
     const int heads = isq ? a.Hq : a.Hkv, pageId = isq ? -1 : (isv ? pg[1] : pg[0]);
@@ -449,21 +421,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
         each_row(it, slot, Norm{}, [&](int r, const uint4&, const uint4&, const Chunks& y) {
           put(r, pack8<kBf16>(y.a), pack8<kBf16>(y.b));
         });
-      return;
-    }
-    if constexpr (kKv8) {
+    } else if constexpr (kKv8) {
       const int off = (it.first - t0) & (kTile - 1);
-      float rowInv = 0.f;  // 1 / scale at row position `lane` of the group
-      if (wide) {
-        rowInv = blockInv[it.h - hs];
+      const float bm = row_maxima(it, slot, isv);
+      float rowInv, f = 1.f;  // 1 / scale at row position `lane` of the group; what older codes are multiplied by
+      if constexpr (kWide) {
+        float* sp = scale_at(max(pageId, 0), t0, hk);
+        const float kept = t0 < 0 ? *sp : 1.f;
+        if (lane == 0) atomicMax(&blockMax[it.h - hs], __float_as_int(bm));  // numbers >= 0: whole-number order is theirs
+        block_sync();  // the block's warps: all maxima are in, all have read the stored scale
+        const float now = new_scale(t0, __int_as_float(*static_cast<volatile int*>(&blockMax[it.h - hs])), kept, f);
+        rowInv = 1.0f / now;
+        if (pageId >= 0 && warp % gk == 0) {
+          if (lane == 0) *sp = now;
+          if (f != 1.f) shrink_older(pageId, hk, f);
+        }
       } else {
-        const float bm = row_maxima(it, slot, isv);
         const int sb = 1 << a.blockShift, rr = lane & (kTile - 1);
         const int tb = t0 + (rr & ~(sb - 1));  // row at the first position of this lane's block
         const bool fill = lane < kTile && max(tb, tlo) < min(tb + sb, thi) && pageId >= 0;
         float* sp = scale_at(fill ? pageId : 0, fill ? tb : 0, hk);
-        float now = 1.f, f = 1.f;
-        if (fill) now = new_scale(tb, bm, sp, f);
+        float now = 1.f;
+        if (fill) now = new_scale(tb, bm, tb < 0 ? *sp : 1.f, f);
         __syncwarp();  // every lane of a block has read its scale
         if (fill && (rr & (sb - 1)) == 0) *sp = now;
         rowInv = 1.0f / now;
@@ -489,13 +468,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
       else
         each_row(it, slot, Norm{}, put);
     }
-  });
+    __syncwarp();  // every lane is done with the slot
+  }
   cp_async_wait<0>();  // the last groups are empty; nothing is in flight at exit
 }
 
-template <int D, bool kBf16, bool kKv8>
+template <int D, bool kBf16, bool kKv8, bool kWide = false>
 cudaError_t append_go(AppendArgs a, int B, cudaStream_t st) {
-  auto kernel = append_kv_kernel<D, kBf16, kKv8>;
+  auto kernel = append_kv_kernel<D, kBf16, kKv8, kWide>;
   constexpr int RPI = 512 / D;  // rows a warp computes at once
   const int NH = a.Hq + 2 * a.Hkv, sms = sm_count();
   const long long tiles = static_cast<long long>(B) * a.tiles;
@@ -506,14 +486,14 @@ cudaError_t append_go(AppendArgs a, int B, cudaStream_t st) {
   a.group = tiles * NH * ((rows + kTile - 1) / kTile) >= warps ? kTile : RPI;
   // One CTA per tile when the tiles fill the GPU; otherwise a tile's heads are dealt out to about as many CTAs as are
   // resident at once (to the nearest number, padding rows leave early: 4 x 333..1000 rows of 20 heads took 11.0 us with 512
-  // CTAs, 13.6 with 256), down to one item per warp.  The K and V heads of a block that is passed over twice count twice:
-  // blocks of 32 12.4 us instead of 14.1, of 128 18.5 instead of 22.4, and three times is no better.
+  // CTAs, 13.6 with 256), down to one item per warp.  K and V heads of wide blocks count twice (with blocks of 32 12.5 us
+  // instead of 14.0, one 8192-row prompt with blocks of 64 44.7 instead of 51.7).
   const int perHead = (rows + a.group - 1) / a.group;
   const int most = std::max(1, (NH * perHead + kWarps - 1) / kWarps);
   int parts = static_cast<int>(std::min<long long>({most, NH, std::max<long long>(1, (kCtasPerSm * sms + tiles / 2) / tiles)}));
-  a.kvCost = kKv8 && a.tile > kTile ? 2 : 1;
+  a.kvCost = kWide ? 2 : 1;
   const int units = a.Hq + 2 * a.Hkv * a.kvCost;
-  if (kKv8 && a.tile > kTile) parts = std::max(parts, (NH + kMaxWideHeads - 2) / (kMaxWideHeads - 1));
+  if (kWide) parts = std::max(parts, (NH + kMaxWideHeads - 2) / (kMaxWideHeads - 1));
   a.unitsPerCta = (units + parts - 1) / parts;
   parts = (units + a.unitsPerCta - 1) / a.unitsPerCta;
   // the warps' rings, and the table of 8 bytes per row and rotated pair (one access of RPI rows past its end)
@@ -532,6 +512,7 @@ cudaError_t append_go(AppendArgs a, int B, cudaStream_t st) {
 
 template <int D>
 cudaError_t append_d(const AppendArgs& a, int B, bool bf16, bool kv8, cudaStream_t st) {
+  if (kv8 && a.tile > kTile) return bf16 ? append_go<D, true, true, true>(a, B, st) : append_go<D, false, true, true>(a, B, st);
   if (kv8) return bf16 ? append_go<D, true, true>(a, B, st) : append_go<D, false, true>(a, B, st);
   return bf16 ? append_go<D, true, false>(a, B, st) : append_go<D, false, false>(a, B, st);
 }
