@@ -142,16 +142,19 @@ __device__ __forceinline__ float finite_max(const uint64_t (&y)[4]) {
   return m;
 }
 
-// 8 codes of y * inv; infinities become NaN.
-__device__ __forceinline__ uint2 quantise8(const uint64_t (&y)[4], float inv) {
-  float v[8];
+// 8 codes of y / s; inv is 1 / s in fp32.  y * inv alone is off by up to two roundings, which sends a quotient halfway
+// between two codes to either; with its remainder put back, a quotient that fp32 holds is exact.  The remainder of an
+// infinity is NaN.
+__device__ __forceinline__ uint2 quantise8(const uint64_t (&y)[4], float s, float inv) {
+  const uint64_t ms2 = pack_f2(-s, -s), inv2 = pack_f2(inv, inv);
+  uint64_t v[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float a = lo_f2(y[k]), b = hi_f2(y[k]);
-    v[2 * k] = fabsf(a) < INFINITY ? a * inv : NAN;
-    v[2 * k + 1] = fabsf(b) < INFINITY ? b * inv : NAN;
+    const uint64_t q = fmul2(y[k], inv2);
+    v[k] = ffma2(ffma2(q, ms2, y[k]), inv2, q);
   }
-  return make_uint2(f32_to_e4m3(v[0], v[1], v[2], v[3]), f32_to_e4m3(v[4], v[5], v[6], v[7]));
+  return make_uint2(f32_to_e4m3(lo_f2(v[0]), hi_f2(v[0]), lo_f2(v[1]), hi_f2(v[1])),
+                    f32_to_e4m3(lo_f2(v[2]), hi_f2(v[2]), lo_f2(v[3]), hi_f2(v[3])));
 }
 
 // 8 stored codes multiplied by f and rounded to codes again (exact for a power of two, above 2^-6).
@@ -424,14 +427,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
     } else if constexpr (kKv8) {
       const int off = (it.first - t0) & (kTile - 1);
       const float bm = row_maxima(it, slot, isv);
-      float rowInv, f = 1.f;  // 1 / scale at row position `lane` of the group; what older codes are multiplied by
+      float rowScale, f = 1.f;  // scale at row position `lane` of the group; what older codes are multiplied by
       if constexpr (kWide) {
         float* sp = scale_at(max(pageId, 0), t0, hk);
         const float kept = t0 < 0 ? *sp : 1.f;
         if (lane == 0) atomicMax(&blockMax[it.h - hs], __float_as_int(bm));  // numbers >= 0: whole-number order is theirs
         block_sync();  // the block's warps: all maxima are in, all have read the stored scale
         const float now = new_scale(t0, __int_as_float(*static_cast<volatile int*>(&blockMax[it.h - hs])), kept, f);
-        rowInv = 1.0f / now;
+        rowScale = now;
         if (pageId >= 0 && warp % gk == 0) {
           if (lane == 0) *sp = now;
           if (f != 1.f) shrink_older(pageId, hk, f);
@@ -445,12 +448,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
         if (fill) now = new_scale(tb, bm, tb < 0 ? *sp : 1.f, f);
         __syncwarp();  // every lane of a block has read its scale
         if (fill && (rr & (sb - 1)) == 0) *sp = now;
-        rowInv = 1.0f / now;
+        rowScale = now;
         f = __shfl_sync(kFull, f, t0 < 0 ? (-t0) & ~(sb - 1) : 0);  // of the block that holds row 0
         if (t0 < 0 && f != 1.f && pageId >= 0) shrink_older(pageId, hk, f);
       }
+      const float rowInv = 1.0f / rowScale;
       auto put = [&](int r, const uint4& ra, const uint4& rb, const Chunks& y) {
-        const float qs = __shfl_sync(kFull, rowInv, (off + r) & (kTile - 1));
+        const int from = (off + r) & (kTile - 1);
+        const float qs = __shfl_sync(kFull, rowScale, from), inv = __shfl_sync(kFull, rowInv, from);
         if (r >= it.rows) return;
         if (dense) {
           uint4* d = dense + r * denseRow;
@@ -459,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kv_kernel(const A
         }
         if (prow) {
           uint2* d = reinterpret_cast<uint2*>(prow + r * rowBytes);
-          d[ca] = quantise8(y.a, qs);
-          d[cb] = quantise8(y.b, qs);
+          d[ca] = quantise8(y.a, qs, inv);
+          d[cb] = quantise8(y.b, qs, inv);
         }
       };
       if (isv)

@@ -441,7 +441,8 @@ QSA_API size_t qsa_gather_scratch_elems(int32_t batchSize, int32_t numKVHeads, i
  * NaN 0x7f), with one fp32 scale per block: the scaleBlock consecutive tokens
  * (a power of two, 1..128, so blocks never cross a page) of one page and one
  * KV head, at kvScale[page][token in page / scaleBlock][head].  A stored value
- * stands for code * scale.  Values are quantised from fp32, to nearest even:
+ * stands for code * scale.  A value's code is its quotient by the scale, in
+ * fp32, rounded to nearest even:
  *   - a block whose first token is among the new ones: scale = amax / 448,
  *     amax the largest finite |value| of its new tokens;
  *   - a block that holds older tokens of the sequence keeps its scale s if

@@ -403,3 +403,34 @@ def test_append_equals_rope():
     for a, r in ((q, rq), (k, rk), (v, rv), (pool, rpool)):
         bar = step_of(a.double(), torch.float16) + EVAL
         assert bool(((a.double() - r.cpu().double()).abs() <= bar).all())
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("block", (1, 4, 16, 32, 128))
+def test_values_halfway_between_codes(dtype, block):
+    """Values that lie exactly halfway between two codes of their block take the even one, for scales that have no exact
+    reciprocal.  Head h has the scale s = k 2^-6, k = 3, 5, 7 .., in every block: its largest value is 7 k = 448 s.  The
+    others are k t 2^(e - 6), in units of s the odd t = 17 .. 31 (5 bits where a code has 4) times 2^e.  All are exact in
+    the input's type, and so is the quotient."""
+    bits = 11 if dtype == torch.float16 else 8
+    ks = (3, 5, 7, 9, 11, 13, 15) if dtype == torch.float16 else (3, 5, 7)
+    c = make(dtype, 128, 2, len(ks), 20, (40,), (20,), block, seed=30)  # tokens 20 .. 39, some behind older ones of a block
+    c["scale"][:] = torch.tensor(ks) * 2.0 ** -6
+    for h, k in enumerate(ks):
+        odd = [t for t in range(17, 32, 2) if k * t < 2 ** bits]
+        units = torch.tensor([t * 2.0 ** e for t in odd for e in range(-9, 5) if t * 2.0 ** e < 448], dtype=torch.float64)
+        pick = torch.randint(len(units), (20, 128), generator=torch.Generator().manual_seed(h))
+        v = units[pick] * torch.where(pick % 2 == 0, 1.0, -1.0) * k * 2.0 ** -6
+        v[:, 5] = 7.0 * k
+        assert torch.equal(v.to(dtype).double(), v)
+        c["qkv"][0, :, 2 + len(ks) + h] = v.to(dtype)
+    out = run(c, 64)
+    check(c, 64, out)
+    pos = torch.arange(20, 40)
+    s = out[4][c["pt"][0, 1, 0].long(), pos // block].double()  # [token, head]
+    assert torch.equal(s, torch.tensor(ks).double().expand(20, -1) * 2.0 ** -6)
+    got = ref.E4M3[out[3].view(torch.uint8)[int(c["pt"][0, 1, 0]), pos].long()]
+    x = c["qkv"][0, :, 2 + len(ks):].double() / s[..., None]  # exact
+    _, e = torch.frexp(x)
+    step = torch.ldexp(torch.ones_like(x), e - 4)  # every value lies in the normal range
+    assert torch.equal(got, torch.round(x / step) * step)
