@@ -195,7 +195,9 @@ __device__ __forceinline__ void scores32(float (&s)[2][NT][4], uint32_t tile, co
 // Online softmax of a step: s becomes the weights relative to the running maximum, returned in fp16 as the B
 // fragments of the second product.  The maximum moves only when a weight would pass 2^kHeadroom (the weights
 // are relative numbers: nothing is lost by their being up to 256 instead of 1), so that O is hardly ever
-// rescaled after a warp's first step.  It starts at the lowest finite number, so that an entry that names nothing
+// rescaled after a warp's first step.  The sums use the weights as the second product does, rounded to 11 bits: where
+// few keys decide, a rounding that only one of the two had would show in an fp16 output (up to 2^-11 of it, as much as
+// its half step).  The maximum starts at the lowest finite number, so that an entry that names nothing
 // (-inf) weighs 0 even before the first that does.  entries[i], of key i: x = K scale * attentionScale * log2(e),
 // y = log2(V scale), z = 1 / V scale; (0, -inf, 0) for an entry that names nothing.
 template <int NT, bool kBf16>
@@ -254,15 +256,17 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float& x = s[i >> 1][nt][2 * (i & 1) + h];
-        x = ex2_ftz(x - A.m[nt][h]);
-        A.l[nt][h] = fmaf(x, iv[i], A.l[nt][h]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      float* x = &s[i >> 1][nt][2 * (i & 1)];
+      const uint64_t w = pack_f2(ex2_ftz(x[0] - A.m[nt][0]), ex2_ftz(x[1] - A.m[nt][1]));
+      // 8193 w - 8192 w, the first rounded to 24 bits: w to 11
+      const uint64_t r = ffma2(pack_f2(-8192.f, -8192.f), w, ffma2(pack_f2(8192.f, 8192.f), w, w));
+      x[0] = lo_f2(r);
+      x[1] = hi_f2(r);
+      A.l[nt][0] = fmaf(x[0], iv[i], A.l[nt][0]);
+      A.l[nt][1] = fmaf(x[1], iv[i], A.l[nt][1]);
     }
-    // the weights in fp16: off by 2^-11 of themselves, which the output's own rounding hides
+    // the weights in fp16: as they are from 2^-14 on, to 2^-25 below
 #pragma unroll
     for (int gk = 0; gk < 2; ++gk) {
       pb[gk][nt][0] = movmatrix_t(pack_half2(s[gk][nt][0], s[gk][nt][1]));

@@ -363,3 +363,30 @@ def test_chunked_prompt_16bit():
         k, v = (pool[pt[0, i].long()].flatten(0, 1)[:L].double().cpu() for i in (0, 1))
         want = ref.attend(q[0].cpu(), k, v, lists[0].cpu(), SCALE)[0]
         assert float((out[0].cpu().double() - want).abs().max()) <= (2e-3 if dtype == torch.float16 else 2e-2)
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("Hq,Hkv,S", [(8, 1, 1), (16, 1, 1), (32, 4, 1300), (12, 2, 2500), (48, 4, 700)])
+def test_one_key_decides(dtype, Hq, Hkv, S):
+    """Two listed keys with the same values, in different steps of a warp, the second heavier by 2^0.5 to 2^7.9.  Whatever
+    the weights, the output is the values themselves, which the output's type holds exactly: numerator and denominator
+    have to use the same weights (fp32 leaves 2^-20, an output's half step is 2^-12 at least)."""
+    gap, topK = (1024, 1100) if S == 1 else (32, 60)  # a warp's next step (one pair: 8 CTAs share a list)
+    c = make(dtype, Hq, Hkv, S, (max(S, 300),), None, topK, 16, seed=40 + Hq)
+    c["lists"][:] = -1
+    c["lists"][:, :, 0], c["lists"][:, :, gap + 8] = 3, 200
+    c["scale"][:] = 1.0
+    codes = c["pool"].view(torch.uint8)
+    k = [int(c["pt"][0, 0, j // 128]) for j in (3, 200)]
+    v = [int(c["pt"][0, 1, j // 128]) for j in (3, 200)]
+    codes[k[0], 3] = 0
+    codes[k[1], 200 - 128] = 0
+    codes[k[1], 200 - 128, :, 0] = 0x38  # 1.0
+    codes[v[1], 200 - 128] = codes[v[0], 3]
+    c["scale"][v[0]] = c["scale"][v[1]] = 2.0 ** -7
+    g = torch.Generator().manual_seed(Hq)
+    c["q"][..., 0] = (0.5 + 7.4 * torch.rand(c["q"].shape[:-1], generator=g)).to(dtype)
+    out = run(c, scale=math.log(2.0))  # q[0] is the heavier key's weight in powers of two
+    want = (ref.E4M3[codes[v[0], 3].long()] * 2.0 ** -7).to(dtype)[None, None].repeat_interleave(Hq // Hkv, 2)
+    n = c["n"][0]
+    assert torch.equal(out[:, :n], want.expand(1, n, -1, -1))
