@@ -109,7 +109,8 @@ __device__ __forceinline__ void norm_rotate(Chunks& x, const Chunks& w, float ep
   float m = mean_square<D>(x) + eps;
   if constexpr (kBf16) {  // squares past fp32's range, or below it beside a small eps: the same on scaled values
     if (__any_sync(kFull, m == INFINITY || m < 0x1p-90f)) {
-      const float f = m == INFINITY ? 0x1p-64f : m < 0x1p-90f ? 0x1p100f : 1.0f;
+      // 2^-70: 128 squares of the largest bf16 stay below 2^123, and the largest value that gets here stays above 2^-10
+      const float f = m == INFINITY ? 0x1p-70f : m < 0x1p-90f ? 0x1p100f : 1.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         x.a[k] = fmul2(x.a[k], pack_f2(f, f));

@@ -434,3 +434,24 @@ def test_values_halfway_between_codes(dtype, block):
     _, e = torch.frexp(x)
     step = torch.ldexp(torch.ones_like(x), e - 4)  # every value lies in the normal range
     assert torch.equal(got, torch.round(x / step) * step)
+
+
+@pytest.mark.parametrize("D", (64, 128))
+@pytest.mark.parametrize("block", (0, 16, 32))
+def test_largest_bf16_values(D, block):
+    """q and k rows of bf16's largest values: all of a row, half of it, one element, and rows at 2^64 and 2^120 beside
+    them.  The sum of the squares passes fp32's range by far, the norm does not."""
+    c = make(torch.bfloat16, D, 4, 2, 40, (40,), None, block, seed=31)
+    top = float(torch.finfo(torch.bfloat16).max)
+    g = torch.Generator().manual_seed(32)
+    x = c["qkv"][0, :, :6]
+    sign = torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0)
+    big = sign * top * (1 - torch.rand(x.shape, generator=g) / 2)
+    big[0:4] = sign[0:4] * top
+    big[4:8, :, ::2] = 1.0
+    big[8:12, :, 1:] = x[8:12, :, 1:].float()
+    big[12:16] = x[12:16].float() * 2.0 ** 64
+    big[16:20] = x[16:20].float() * 2.0 ** 120
+    c["qkv"][0, :, :6] = big.bfloat16()
+    assert bool(torch.isfinite(c["qkv"]).all())
+    check(c, 32, run(c, 32))
