@@ -222,8 +222,8 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float& x = s[i >> 1][nt][2 * (i & 1) + h];
-        if constexpr (kBf16) x *= qs[nt][h];
-        x = fmaf(x, ks[i], lv[i]);
+        // bf16: the K scale first, so that nothing but a logit itself can overflow
+        x = kBf16 ? fmaf(x * ks[i], qs[nt][h], lv[i]) : fmaf(x, ks[i], lv[i]);
       }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -316,7 +316,8 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
         for (int w = 0; w < 4; ++w) m = max(m, max(word(raw[i], w) & 0x7fff, (word(raw[i], w) >> 16) & 0x7fff));
       m = max(m, __shfl_xor_sync(kFull, m, 1));
       m = max(m, __shfl_xor_sync(kFull, m, 2));
-      // exponent e of the largest: scaled by 2^(14 - e), in two steps that stay normal; none for 0, inf and NaN
+      // exponent e of the largest: scaled by 2^(14 - e), or 2^114 where that is less, so that the inverse is a normal
+      // number; not for 0, inf and NaN
       const int e = static_cast<int>(m >> 7) - 127;
       if (m != 0 && e < 128) {
         const int k = 14 - max(e, -100);

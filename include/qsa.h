@@ -515,7 +515,8 @@ QSA_API qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* params);
  * use it NaN.
  * Arithmetic: codes enter the products exactly (fp16), bf16 queries as fp16
  * after a power-of-two scaling per row and head that keeps every value within
- * 2^-38 of the row's largest; products accumulate in fp32, the softmax is
+ * 2^-38 of the row's largest (2^-139, for a row all below 2^-100); products
+ * accumulate in fp32, whose range the logits have to keep to, the softmax is
  * fp32, each probability times its V scale is rounded to fp16 relative to the
  * largest such product, and the output is rounded once.  Repeated calls give
  * identical bits.

@@ -390,3 +390,24 @@ def test_one_key_decides(dtype, Hq, Hkv, S):
     want = (ref.E4M3[codes[v[0], 3].long()] * 2.0 ** -7).to(dtype)[None, None].repeat_interleave(Hq // Hkv, 2)
     n = c["n"][0]
     assert torch.equal(out[:, :n], want.expand(1, n, -1, -1))
+
+
+@pytest.mark.parametrize("e,kscale,scale", [
+    (60, 2.0 ** -48, 2.0 ** -23), (118, 2.0 ** -48, 2.0 ** -81), (118, 2.0 ** -7, 2.0 ** -122), (120, 2.0 ** -20, 2.0 ** -111),
+    (-110, 2.0 ** 48, 2.0 ** 51), (-110, 2.0 ** -7, 2.0 ** 106), (0, 2.0 ** -48, 2.0 ** 37)])
+@pytest.mark.parametrize("Hkv,S", [(2, 2), (4, 1300)])
+def test_bf16_queries_of_any_size(e, kscale, scale, Hkv, S):
+    """Queries of about 2^e against K scales and an attentionScale that bring the logits back near 1."""
+    c = make(torch.bfloat16, 8 * Hkv, Hkv, S, (max(S, 400),), None, 140, 16, seed=50 + S)
+    c["q"] = (c["q"].float() * 2.0 ** e).bfloat16()
+    half = c["scale"].shape[0] // 2  # K pages, then V pages
+    c["scale"][:half] = kscale
+    out = run(c, scale=scale)
+    L = int(c["ctx"][0])
+    k, v = (ref.dequantised(c["pool"], c["scale"], c["pt"][0, i], L) for i in (0, 1))
+    rows = list(range(2)) if S == 2 else list(range(0, S, 97)) + [S - 1]
+    want, mean_abs, dots = ref.attend(c["q"][0, rows], k, v, c["lists"][0, rows], scale)
+    assert 0.1 < float(dots.max()) < 1e4
+    bar = ref.attend_bar(want, mean_abs, dots, c["lists"][0, 0], c["scale"][half:], out.dtype)
+    err = (out[0, rows].double() - want).abs()
+    assert bool((err <= bar).all()), float((err / bar).max())
