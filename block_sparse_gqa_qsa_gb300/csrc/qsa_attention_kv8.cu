@@ -356,7 +356,7 @@ constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kPad + 2) *
 
 // What a CTA (or cluster) works on: a row of the call and successive KV heads.
 struct Row {
-  int kvh, b, t, L, n;  // first KV head, sequence, row, its length, its live rows
+  int kvh, b, t, L, n;  // first KV head, sequence, row, the tokens that its page table holds, its live rows
   size_t bt, head0;     // list row; first query head
 };
 // The place of work item `id` with `heads` KV heads each; its lengths are read by row_lengths.
@@ -371,8 +371,9 @@ __device__ __forceinline__ Row row_of(const PagedArgs& a, int id, int heads) {
   return r;
 }
 __device__ __forceinline__ void row_lengths(const PagedArgs& a, Row& r) {
-  r.L = max(0, min(a.ctx[r.b], a.maxPagesPerSeq * kTokensPerPage));
-  r.n = max(0, min(a.newLen ? a.newLen[r.b] : a.S, min(a.S, r.L)));
+  const int L = max(0, a.ctx[r.b]);
+  r.L = min(L, a.maxPagesPerSeq * kTokensPerPage);
+  r.n = max(0, min(a.newLen ? a.newLen[r.b] : a.S, min(a.S, L)));
 }
 
 // From list entries to pool rows, free of branches: what an entry cannot name is looked up at 0 and dropped.

@@ -506,10 +506,10 @@ QSA_API qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* params);
  * newLengths NULL: min(seqLen, L)) and query head h (KV head g = h /
  * (numQHeads / numKVHeads)):
  *   o[b,t,h] = sum_{j in list} softmax_j(attentionScale * q[b,t,h] . k[j,g]) v[j,g]
- * over the entries j of indices[b,t,:] inside [0, L); k and v are the cached
- * values code * scale.  Causality lives in the list, an entry named twice
- * counts twice, and rows t >= n and rows whose list names nothing are exact
- * zeros.  The lists are those of qsa_indexer_decode (seqLen 1) or
+ * over the entries j of indices[b,t,:] inside [0, L) and on the page table's
+ * maxPagesPerSeq pages; k and v are the cached values code * scale.  Causality
+ * lives in the list, an entry named twice counts twice, and rows t >= n and
+ * rows whose list names nothing are exact zeros.  The lists are those of qsa_indexer_decode (seqLen 1) or
  * qsa_indexer_prefill (a whole prompt).  A scale outside [2^-48, 2^48] is read
  * as the nearer bound (NaN as the lower); a NaN code makes the outputs that
  * use it NaN.
@@ -525,7 +525,7 @@ QSA_API qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* params);
  * workspace, and calls may run concurrently.
  * status (may be NULL): bits as for qsa_sparse_decode -- 2: a named token's
  * page id lies outside [0, numFlatPages); 4: an entry other than -1 lies
- * outside [0, L).  Such entries are skipped.
+ * outside [0, L) or behind the page table.  Such entries are skipped.
  * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1,
  * numQHeads not a multiple of numKVHeads, poolHeadDim < headDim or a scaleBlock
  * that is not a power of two in 1..128; QSA_ERR_UNSUPPORTED for headDim other

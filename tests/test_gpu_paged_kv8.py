@@ -411,3 +411,23 @@ def test_bf16_queries_of_any_size(e, kscale, scale, Hkv, S):
     bar = ref.attend_bar(want, mean_abs, dots, c["lists"][0, 0], c["scale"][half:], out.dtype)
     err = (out[0, rows].double() - want).abs()
     assert bool((err <= bar).all()), float((err / bar).max())
+
+
+@pytest.mark.parametrize("Hq,Hkv,S,L,new,pages", [(8, 2, 300, 300, None, 2), (8, 2, 20, 300, (20,), 2),
+                                                  (16, 4, 1300, 1300, None, 5), (8, 2, 1, 300, None, 1)])
+def test_rows_behind_the_page_table(Hq, Hkv, S, L, new, pages):
+    """A length past the page table: every live row is computed from the entries that the table holds, as the append
+    writes every live row's dense output; entries behind the table are skipped and reported."""
+    c = make(torch.float16, Hq, Hkv, S, (L,), new, 90, 16, seed=60 + S)
+    c["pt"] = c["pt"][:, :, :pages].contiguous()
+    named = torch.where(c["lists"] < 128 * pages, c["lists"], torch.full_like(c["lists"], -1))
+    named[0, -1, 0] = 5
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = run(dict(c, lists=named), status=status)
+    check(c, want, lists=named)
+    assert int(status) == 0 and bool(want[0, -1].view(torch.int16).any())
+    behind = named.clone()
+    behind[0, -1, 1:4] = torch.tensor([128 * pages, L - 1, -1], dtype=torch.int32)
+    named[0, -1, 1:4] = -1
+    assert torch.equal(run(dict(c, lists=behind), status=status), run(dict(c, lists=named)))
+    assert int(status) == 4
