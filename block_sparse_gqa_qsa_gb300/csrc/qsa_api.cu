@@ -171,8 +171,9 @@ qsa_status_t append_kv_entry(const QsaAppendKvParams* p, const char* fn, bool bf
   if (p->batchSize < 1 || p->seqLen < 1 || p->numQHeads < 1 || p->numKVHeads < 1 || p->headDim < 1 ||
       p->numFlatPages < 1 || p->maxPagesPerSeq < 1)
     return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
-  if (p->rotDim < 0 || p->rotDim > p->headDim || (p->rotDim & 1) || !(p->ropeTheta > 0.f) || !(p->rmsNormEps >= 0.f))
-    return fail(QSA_ERR_INVALID_ARG, "%s: rotDim must be even and <= headDim; theta > 0, eps >= 0", fn);
+  if (p->rotDim < 0 || p->rotDim > p->headDim || (p->rotDim & 1) || !(p->ropeTheta > 0.f) || !(p->rmsNormEps >= 0.f) ||
+      std::isinf(p->rmsNormEps))
+    return fail(QSA_ERR_INVALID_ARG, "%s: rotDim must be even and <= headDim; theta > 0, eps >= 0 and finite", fn);
   if (p->poolHeadDim < p->headDim) return fail(QSA_ERR_INVALID_ARG, "%s: poolHeadDim < headDim", fn);
   if (kv8) {
     if (!p->kvScale) return fail(QSA_ERR_INVALID_ARG, "%s: kvScale is NULL", fn);

@@ -458,8 +458,8 @@ QSA_API size_t qsa_gather_scratch_elems(int32_t batchSize, int32_t numKVHeads, i
  * [0, numFlatPages), or its position behind the page table; that row of the
  * pool is not written (its dense outputs are).
  * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1, an odd
- * rotDim or rotDim > headDim, theta <= 0, eps < 0, poolHeadDim < headDim, a
- * scaleBlock that is not a power of two in 1..128 (8-bit) or kvScale /
+ * rotDim or rotDim > headDim, theta <= 0, eps < 0 or infinite, poolHeadDim <
+ * headDim, a scaleBlock that is not a power of two in 1..128 (8-bit) or kvScale /
  * scaleBlock given for a 16-bit pool; QSA_ERR_UNSUPPORTED for headDim not
  * 64/128, rotDim not a multiple of 16, pool rows (poolHeadDim elements) not a
  * multiple of 16 bytes, a tensor not 16-byte aligned (kvScale and the int32

@@ -159,3 +159,11 @@ def test_packed_params_are_the_structs(qb):
         values = [i + 1 for i in range(len(cls._fields_))]
         got = cls.from_buffer_copy(pack.pack(*values))
         assert pack.size == ctypes.sizeof(cls) and [getattr(got, f) for f, _ in cls._fields_] == values
+
+
+def test_append_refuses_an_infinite_eps(qb):
+    """x / sqrt(mean + inf) is 0 and inf * 0 is not: no such norm is computed."""
+    for fn in APPEND16 + APPEND8:
+        kw = dict(kvScale=None, scaleBlock=0) if fn in APPEND16 else {}
+        assert getattr(qb.lib(), fn)(ctypes.byref(append_params(qb, rmsNormEps=float("inf"), **kw))) == INVALID
+        assert b"eps" in qb.lib().qsa_last_error_message()
