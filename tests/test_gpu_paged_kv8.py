@@ -431,3 +431,41 @@ def test_rows_behind_the_page_table(Hq, Hkv, S, L, new, pages):
     named[0, -1, 1:4] = -1
     assert torch.equal(run(dict(c, lists=behind), status=status), run(dict(c, lists=named)))
     assert int(status) == 4
+
+
+@pytest.mark.parametrize("dtype", (torch.float16, torch.bfloat16))
+@pytest.mark.parametrize("Hq,Hkv,S,topK", [(8, 2, 1, 2051), (24, 2, 1, 2051), (16, 4, 1300, 400), (12, 6, 900, 400),
+                                           (24, 2, 1300, 400)])
+def test_every_entry_counts_once(dtype, Hq, Hkv, S, topK):
+    """Each entry of a long list by itself: in sequence b the token 128 b + d has one nonzero value, in dim d, so an output
+    is one entry's probability times that value.  Relative bar: fp16 weights in numerator and denominator (2^-11 each),
+    logits off by D 2^-23 of their terms, twice, the output's half step, and 2^-18 for the rest; a missing or doubled
+    entry is off by 1.  Weights stay in fp16's normal range and outputs too (logits within 1.5 of each other)."""
+    L = topK - 40  # the rest of the list is holes
+    B = -(-L // 128)
+    if S > 1:
+        B = min(B, 3)
+    c = make(dtype, Hq, Hkv, S, (max(L, S),) * B, None, topK, 16, seed=70 + Hq + S)
+    g = torch.Generator().manual_seed(Hq)
+    order = torch.rand((B, S, topK), generator=g).argsort(-1).to(torch.int32)
+    c["lists"] = torch.where(order < L, order, torch.full_like(order, -1))
+    half = c["scale"].shape[0] // 2
+    c["scale"][:half] = 2.0 ** -7
+    c["scale"][half:] = 1.0
+    codes = c["pool"].view(torch.uint8)
+    codes[half:] = 0
+    for b in range(B):
+        d = torch.arange(min(128, L - 128 * b))
+        codes[int(c["pt"][b, 1, b]), d, :, d] = 0x7e  # 448
+    out = run(c, scale=0.004).double()
+    G = Hq // Hkv
+    for b in range(B):
+        k = ref.dequantised(c["pool"], c["scale"], c["pt"][b, 0], L)
+        z = 0.004 * torch.einsum("thgd,lhd->thgl", c["q"][b].double().view(S, Hkv, G, D), k)
+        assert float((z.amax(-1) - z.amin(-1)).max()) < 1.5
+        m = min(128, L - 128 * b)
+        want = 448 * torch.softmax(z, -1)[..., 128 * b:128 * b + m].reshape(S, Hq, m)
+        terms = 0.004 * (c["q"][b].double().abs().sum(-1).max() * k.abs().max())
+        bar = 2 * 2.0 ** -11 + 2 * D * 2.0 ** -23 * float(terms) + torch.finfo(dtype).eps / 2 + 2.0 ** -18
+        assert bar < 0.02 and float(((out[b, :, :, :m] - want).abs() / want).max()) <= bar
+        assert not out[b, :, :, m:].any()
