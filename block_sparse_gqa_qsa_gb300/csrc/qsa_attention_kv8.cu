@@ -341,10 +341,11 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
 
 constexpr int kPad = kD + 4;  // floats of a head in the merge buffers
 
-// Resident CTAs per SM.  Many rows: the register budget decides (5 at 96 registers spill and took 1333 us for an 8192-row
-// prompt against 1275 with 4; 16-head groups at 168 registers 2008 against 1928 with 2).  Split: two tiles of each kind per
-// warp (69 KB a CTA) rather than a fourth CTA with one: decode of 8, 16, 38, 64, 200 sequences with 4 KV heads took 7.0,
-// 9.7, 18.3, 26.4, 70.6 us instead of 7.5, 10.5, 19.8, 29.1, 78.1, of 32 sequences 17.1 either way.
+// Resident CTAs per SM.  Many rows: the register budget decides.  With 4, groups up to 8 keep a little of a lane in local
+// memory (four fp16 heads 28 bytes, four or two bf16 heads 8 and 16); 5 at 96 registers spill far more and took 1333 us
+// for an 8192-row prompt against 1275 with 4; 16-head groups at 168 registers 2008 against 1928 with 2.  Split: two tiles of
+// each kind per warp (69 KB a CTA) rather than a fourth CTA with one: decode of 8, 16, 38, 64, 200 sequences with 4 KV heads
+// took 7.0, 9.7, 18.3, 26.4, 70.6 us instead of 7.5, 10.5, 19.8, 29.1, 78.1, of 32 sequences 17.1 either way.
 template <int NT>
 constexpr int kSplitCtasPerSm = NT == 1 ? 3 : 2;
 template <int NT>
@@ -859,9 +860,10 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();  // CTAs resident at once
   // A warp per pair from two waves of such CTAs on: 2 x 700 rows of 4 heads (2.3 waves) took 202 us instead of 224, 2 x 350
   // (1.2 waves) 146 instead of 127.  With 2 heads 4096 rows (3.4 waves) 294 instead of 301, 8192 618 instead of 657, 12
-  // query heads each 887 instead of 987, but 1100 + 1100 rows (1.8 waves) 213 instead of 198.  (Two warps per pair, four
-  // heads: 223 us where one took 223.  Lists of their own per warp, for odd numbers of heads: 406 us where the split form
-  // took 332, 8192 rows of one head.)
+  // query heads each 887 instead of 987, but 1100 + 1100 rows (1.8 waves) 213 instead of 198.  (All taken
+  // before the sums' weights were rounded too, which adds 1 to 3 % to either form: 202 is 205 now, 618 626, 887 911.  Two
+  // warps per pair, four heads: 223 us where one took 223.  Lists of their own per warp, for odd numbers of heads: 406 us
+  // where the split form took 332, 8192 rows of one head.)
   if (a.Hkv % 2 == 0 && pairs / kWarps >= 2 * slots)
     return a.Hkv % 4 == 0 ? rows_go<NT, kBf16, 4>(a, pairs, st) : rows_go<NT, kBf16, 2>(a, pairs, st);
   // Otherwise as many CTAs per pair as leave all clusters resident at once, at most one per 128 entries of the list.

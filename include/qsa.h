@@ -509,16 +509,18 @@ QSA_API qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* params);
  * over the entries j of indices[b,t,:] inside [0, L) and on the page table's
  * maxPagesPerSeq pages; k and v are the cached values code * scale.  Causality
  * lives in the list, an entry named twice counts twice, and rows t >= n and
- * rows whose list names nothing are exact zeros.  The lists are those of qsa_indexer_decode (seqLen 1) or
- * qsa_indexer_prefill (a whole prompt).  A scale outside [2^-48, 2^48] is read
- * as the nearer bound (NaN as the lower); a NaN code makes the outputs that
- * use it NaN.
+ * rows whose list names nothing are exact zeros.  qsa_indexer_decode makes the
+ * lists of single rows (seqLen 1), qsa_indexer_prefill those of whole prompts;
+ * lists for several rows behind cached tokens are the caller's own.  A scale
+ * outside [2^-48, 2^48] is read as the nearer bound (NaN as the lower); a NaN
+ * code makes the outputs that use it NaN.
  * Arithmetic: codes enter the products exactly (fp16), bf16 queries as fp16
  * after a power-of-two scaling per row and head that keeps every value within
  * 2^-38 of the row's largest (2^-139, for a row all below 2^-100); products
  * accumulate in fp32, whose range the logits have to keep to, the softmax is
- * fp32, each probability times its V scale is rounded to fp16 relative to the
- * largest such product, and the output is rounded once.  Repeated calls give
+ * fp32, each probability times its V scale is rounded to 11 bits for numerator
+ * and denominator alike (in the numerator to 2^-25 of the largest such product
+ * at least, fp16's range), and the output is rounded once.  Repeated calls give
  * identical bits.
  * When there are few (row, KV head) pairs, a list is split over the CTAs of a
  * cluster (at most 8), which join their partial results on chip: there is no

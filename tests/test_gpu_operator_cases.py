@@ -4,7 +4,8 @@ Bars.  q of an append and the values of a 16-bit pool: one step of the type plus
 2^-18 / 448 plus 2^-22 of it, and a block that grew may have grown by one power of two less or more where its largest
 value meets 448 scales within that; a code: one e4m3 step (2^-3 of the value, 2^-9 at least) where its scale is the
 64-bit form's, half a step for each of two roundings.  Attention: `paged_cache_ref.attend_bar`, with the weighted mean of
-|v| from the 64-bit form over the codes' magnitudes, and 2^5 for the terms of a logit (unit normals: 7 on average, K scales up to 4 times theirs)."""
+|v| from the 64-bit form over the codes' magnitudes, and 2^5 for the terms of a logit (unit normals: 7 on average, K
+scales up to 4 times theirs)."""
 from __future__ import annotations
 
 import importlib.util
