@@ -222,7 +222,7 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float& x = s[i >> 1][nt][2 * (i & 1) + h];
-        // bf16: the K scale first, so that nothing but a logit itself can overflow
+        // bf16: the K scale first (the product is below 2^31, so with scales below 2^96 only a logit itself overflows)
         x = kBf16 ? fmaf(x * ks[i], qs[nt][h], lv[i]) : fmaf(x, ks[i], lv[i]);
       }
 #pragma unroll

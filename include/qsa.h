@@ -517,10 +517,11 @@ QSA_API qsa_status_t qsa_append_kv8_bf16(const QsaAppendKvParams* params);
  * Arithmetic: codes enter the products exactly (fp16), bf16 queries as fp16
  * after a power-of-two scaling per row and head that keeps every value within
  * 2^-38 of the row's largest (2^-139, for a row all below 2^-100); products
- * accumulate in fp32, whose range the logits have to keep to, the softmax is
- * fp32, each probability times its V scale is rounded to 11 bits for numerator
- * and denominator alike (in the numerator to 2^-25 of the largest such product
- * at least, fp16's range), and the output is rounded once.  Repeated calls give
+ * accumulate in fp32, whose range the logits have to keep to (with bf16 queries
+ * attentionScale * K scale stays below 2^96 too), the softmax is fp32, each
+ * probability times its V scale is rounded to 11 bits for numerator and
+ * denominator alike (in the numerator to 2^-25 of the largest such product at
+ * least, fp16's range), and the output is rounded once.  Repeated calls give
  * identical bits.
  * When there are few (row, KV head) pairs, a list is split over the CTAs of a
  * cluster (at most 8), which join their partial results on chip: there is no
