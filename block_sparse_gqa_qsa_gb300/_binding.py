@@ -22,6 +22,8 @@ QSA_OK, QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_WORKSPACE, QSA_ERR_CUD
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
+_f64 = ctypes.c_double
 _f32 = ctypes.c_float
 _sz = ctypes.c_size_t
 
@@ -110,6 +112,43 @@ class QsaSparsePagedKv8Params(ctypes.Structure):
                 ("attentionScale", _f32), ("stream", _vp), ("status", _vp)]
 
 
+class QsaRotaryParams(ctypes.Structure):
+    _fields_ = [("x", _vp), ("y", _vp), ("positions", _vp), ("invFreq", _vp), ("xTokenStride", _i64),
+                ("xHeadStride", _i64), ("yTokenStride", _i64), ("yHeadStride", _i64), ("numTokens", _i32),
+                ("numHeads", _i32), ("headDim", _i32), ("rotDim", _i32), ("interleaved", _i32), ("inverse", _i32),
+                ("magnitude", _f32), ("stream", _vp)]
+
+
+class QsaStoreKv4Params(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("contextLengths", _vp), ("newLengths", _vp), ("kOut", _vp), ("vOut", _vp),
+                ("kvPool", _vp), ("pageTable", _vp), ("status", _vp), ("kTokenStride", _i64), ("vTokenStride", _i64),
+                ("batchSize", _i32), ("seqLen", _i32), ("numKVHeads", _i32), ("headDim", _i32), ("poolRowBytes", _i32),
+                ("numFlatPages", _i32), ("maxPagesPerSeq", _i32), ("stream", _vp)]
+
+
+class QsaSparsePagedKv4Params(ctypes.Structure):
+    _fields_ = [("qPtr", _vp), ("kvPool", _vp), ("pageTable", _vp), ("indices", _vp), ("contextLengths", _vp),
+                ("newLengths", _vp), ("oPtr", _vp), ("lse", _vp), ("status", _vp), ("batchSize", _i32), ("seqLen", _i32),
+                ("numQHeads", _i32), ("numKVHeads", _i32), ("headDim", _i32), ("poolRowBytes", _i32),
+                ("numFlatPages", _i32), ("maxPagesPerSeq", _i32), ("topK", _i32), ("attentionScale", _f32),
+                ("stream", _vp)]
+
+
+class QsaSparseWeightsKv4Params(ctypes.Structure):
+    _fields_ = [("qPtr", _vp), ("kvPool", _vp), ("pageTable", _vp), ("indices", _vp), ("contextLengths", _vp),
+                ("newLengths", _vp), ("lse", _vp), ("weights", _vp), ("total", _vp), ("status", _vp), ("batchSize", _i32),
+                ("seqLen", _i32), ("numQHeads", _i32), ("numKVHeads", _i32), ("headDim", _i32), ("poolRowBytes", _i32),
+                ("numFlatPages", _i32), ("maxPagesPerSeq", _i32), ("topK", _i32), ("totalLen", _i32),
+                ("attentionScale", _f32), ("stream", _vp)]
+
+
+class QsaEvictKv4Params(ctypes.Structure):
+    _fields_ = [("kvPool", _vp), ("pageTable", _vp), ("contextLengths", _vp), ("total", _vp), ("kept", _vp),
+                ("keptLengths", _vp), ("totalOut", _vp), ("status", _vp), ("batchSize", _i32), ("numKVHeads", _i32),
+                ("headDim", _i32), ("poolRowBytes", _i32), ("numFlatPages", _i32), ("maxPagesPerSeq", _i32),
+                ("totalLen", _i32), ("budget", _i32), ("sinks", _i32), ("recent", _i32), ("stream", _vp)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -140,7 +179,17 @@ def lib() -> ctypes.CDLL:
                              ("qsa_append_kv8", QsaAppendKvParams),
                              ("qsa_append_kv8_bf16", QsaAppendKvParams),
                              ("qsa_sparse_paged_kv8", QsaSparsePagedKv8Params),
-                             ("qsa_sparse_paged_kv8_bf16", QsaSparsePagedKv8Params)):
+                             ("qsa_sparse_paged_kv8_bf16", QsaSparsePagedKv8Params),
+                             ("qsa_rotary", QsaRotaryParams),
+                             ("qsa_rotary_bf16", QsaRotaryParams),
+                             ("qsa_rotary_f32", QsaRotaryParams),
+                             ("qsa_store_kv4", QsaStoreKv4Params),
+                             ("qsa_store_kv4_bf16", QsaStoreKv4Params),
+                             ("qsa_sparse_paged_kv4", QsaSparsePagedKv4Params),
+                             ("qsa_sparse_paged_kv4_bf16", QsaSparsePagedKv4Params),
+                             ("qsa_sparse_weights_kv4", QsaSparseWeightsKv4Params),
+                             ("qsa_sparse_weights_kv4_bf16", QsaSparseWeightsKv4Params),
+                             ("qsa_evict_kv4", QsaEvictKv4Params)):
                 f = getattr(L, name)
                 f.argtypes = [ctypes.POINTER(st)]
                 f.restype = ctypes.c_int
@@ -172,6 +221,8 @@ def lib() -> ctypes.CDLL:
             L.qsa_last_error_message.restype = ctypes.c_char_p
             L.qsa_last_device_error.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(_i32)]
             L.qsa_last_device_error.restype = ctypes.c_int
+            L.qsa_rotary_frequencies.argtypes = [_i32, _i32] + [_f64] * 5 + [_vp]
+            L.qsa_rotary_frequencies.restype = ctypes.c_int
             L.qsa_debug_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
             L.qsa_debug_set_wait_limit_ns.restype = None
             _lib = L
@@ -576,5 +627,189 @@ def sparse_paged_kv8(q, pool, kv_scale, page_table, indices, ctx, out, *, scale,
         nflat, pages, topK, 128 // nblk, scale, _raw_stream(stream, dev),
         0 if status is None else _arg(status, _I32, "status", dev))
     r = _packed("qsa_sparse_paged_kv8_bf16" if bf16 else "qsa_sparse_paged_kv8")(packed)
+    if r:
+        _check(r)
+
+
+# --------------------------------------------------------- rotary positions
+_ROTARY_PACK = struct.Struct("@4P4q6ifP")
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "blend": 3, "ramp": 4}
+_ROTARY_FN = {_F16: "qsa_rotary", _BF16: "qsa_rotary_bf16", torch.float32: "qsa_rotary_f32"}
+
+
+def rotary_frequencies(rot, *, theta, scaling="plain", factor=1.0, original_length=0.0, low_turns=1.0, high_turns=32.0):
+    """qsa_rotary_frequencies: the rot/2 angles per position of `rotary`, a float64 tensor on the host.  scaling: "plain",
+    "linear", "base", "blend" or "ramp" (QSA_ROTARY_*)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"rotary_frequencies: scaling must be one of {sorted(ROTARY_SCALINGS)}")
+    out = torch.empty(max(rot, 0) // 2, dtype=torch.float64)
+    _check(lib().qsa_rotary_frequencies(ROTARY_SCALINGS[scaling], rot, theta, factor, original_length, low_turns, high_turns,
+                                        out.data_ptr() or None))
+    return out
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between tokens of [tokens, heads, D], or of [B, S, heads, D] whose tokens are evenly spaced."""
+    if t.dim() == 3:
+        return t.stride(0)
+    B, S = t.shape[:2]
+    if S == 1:
+        return t.stride(0)
+    if B > 1 and t.stride(0) != S * t.stride(1):
+        raise ValueError(f"{name}: sequences must follow each other evenly (stride {S * t.stride(1)}, got {t.stride(0)})")
+    return t.stride(1)
+
+
+def rotary(x, positions, out, inv_freq, *, interleaved=False, inverse=False, magnitude=1.0, stream=None):
+    """qsa_rotary (fp16), qsa_rotary_bf16 or qsa_rotary_f32: the heads of x [tokens, heads, D] or [B, S, heads, D] turned
+    by positions int32 [tokens] or [B, S] (negative: padding, left alone) into out, which may be x.  inv_freq: rot/2
+    angles per position, float64 on the host (see rotary_frequencies).  x and out may be views whose rows are contiguous.
+    The gradient is the same call with inverse=True."""
+    et = x.dtype
+    fn = _ROTARY_FN.get(et)
+    if fn is None:
+        raise ValueError("rotary: x must be float16, bfloat16 or float32")
+    if x.dim() not in (3, 4) or out.shape != x.shape or positions.shape != x.shape[:-2]:
+        raise ValueError("rotary: x and out are [tokens, heads, D] or [B, S, heads, D], positions [tokens] or [B, S]")
+    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or inv_freq.device.type != "cpu" or \
+            not inv_freq.is_contiguous():
+        raise ValueError("rotary: inv_freq must be a contiguous float64 vector on the host")
+    dev = _current_device(x)
+    if out.dtype is not et or not (x.get_device() == out.get_device() == dev):
+        raise ValueError(f"rotary: out must be {et}, and x and out on the current device cuda:{dev}")
+    D = x.shape[-1]
+    if (D > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1)):
+        raise ValueError("rotary: the rows of x and out must be contiguous")
+    if x.numel() == 0:
+        raise ValueError("rotary: x is empty")
+    heads = x.shape[-2]
+    packed = _ROTARY_PACK.pack(
+        x.data_ptr(), out.data_ptr(), _arg(positions, _I32, "positions", dev), inv_freq.data_ptr(),
+        _token_stride(x, "x"), x.stride(-2), _token_stride(out, "out"), out.stride(-2), x.numel() // (heads * D), heads, D,
+        2 * inv_freq.numel(), interleaved, inverse, magnitude, _raw_stream(stream, dev))
+    r = _packed(fn)(packed)
+    if r:
+        _check(r)
+
+
+# -------------------------------------------------------------- 4-bit cache
+_STORE4_PACK = struct.Struct("@9P2q7iP")
+_PAGED4_PACK = struct.Struct("@9P9ifP")
+_WEIGHTS4_PACK = struct.Struct("@10P10ifP")
+_EVICT4_PACK = struct.Struct("@8P10iP")
+KV4_ROW_BYTES = 80
+_U8 = torch.uint8
+
+
+def _pool4(pool, page_table, name):
+    """(flat pages, KV heads, row bytes, pages per sequence) of a 4-bit pool uint8 [flat, 128, heads, bytes] and its table."""
+    if pool.dim() != 4 or page_table.dim() != 3 or pool.shape[1] != 128 or page_table.shape[1] != 2:
+        raise ValueError(f"{name}: pool is uint8 [pages, 128, heads, bytes], page_table [B, 2, pages]")
+    return pool.shape[0], pool.shape[2], pool.shape[3], page_table.shape[2]
+
+
+def _opt(t, dtype, name, device):
+    return 0 if t is None else _arg(t, dtype, name, device)
+
+
+def store_kv4(k, v, ctx, pool, page_table, *, new_lengths=None, k_out=None, v_out=None, status=None, stream=None):
+    """qsa_store_kv4 (fp16) or qsa_store_kv4_bf16: the new tokens of k and v [B,S,Hkv,128] (views of packed projections
+    will do) into pool uint8 [numFlat,128,Hkv,rowBytes >= 80] through page_table [B,2,pages].  ctx int32 [B] holds cached
+    lengths, new_lengths int32 [B] how many of them are new (None: min(S, ctx)); k_out / v_out [B,S,Hkv,128] get the values
+    that the rows stand for."""
+    et = k.dtype
+    if et is not _F16 and et is not _BF16:
+        raise ValueError("store_kv4: k must be float16 or bfloat16")
+    nflat, Hkv, row, pages = _pool4(pool, page_table, "store_kv4")
+    if k.dim() != 4 or v.shape != k.shape or k.shape[2] != Hkv or ctx.shape != k.shape[:1] or \
+            page_table.shape[0] != k.shape[0] or (new_lengths is not None and new_lengths.shape != ctx.shape) or \
+            (k_out is not None and k_out.shape != k.shape) or (v_out is not None and v_out.shape != k.shape):
+        raise ValueError("store_kv4: shape mismatch")
+    B, S, _, D = k.shape
+    dev = _current_device(k)
+    if v.dtype is not et or not (k.get_device() == v.get_device() == dev):
+        raise ValueError(f"store_kv4: v must be {et}, and k and v on the current device cuda:{dev}")
+    for t, n in ((k, "k"), (v, "v")):
+        if t.stride(3) != 1 or (Hkv > 1 and t.stride(2) != D):
+            raise ValueError(f"store_kv4: the heads of a token of {n} must lie together")
+    packed = _STORE4_PACK.pack(
+        k.data_ptr(), v.data_ptr(), _arg(ctx, _I32, "contextLengths", dev), _opt(new_lengths, _I32, "new_lengths", dev),
+        _opt(k_out, et, "k_out", dev), _opt(v_out, et, "v_out", dev), _arg(pool, _U8, "pool", dev),
+        _arg(page_table, _I32, "pageTable", dev), _opt(status, _I32, "status", dev), _token_stride(k, "k"),
+        _token_stride(v, "v"), B, S, Hkv, D, row, nflat, pages, _raw_stream(stream, dev))
+    r = _packed("qsa_store_kv4_bf16" if et is _BF16 else "qsa_store_kv4")(packed)
+    if r:
+        _check(r)
+
+
+def _lists4(q, pool, page_table, indices, ctx, new_lengths, name):
+    """The sizes and addresses that the two readers of a 4-bit pool by lists share."""
+    et = q.dtype
+    if et is not _F16 and et is not _BF16:
+        raise ValueError(f"{name}: q must be float16 or bfloat16")
+    nflat, Hkv, row, pages = _pool4(pool, page_table, name)
+    if q.dim() != 4 or indices.dim() != 3:
+        raise ValueError(f"{name}: q has 4 dimensions, indices 3")
+    B, S, Hq, D = q.shape
+    if indices.shape[:2] != (B, S) or ctx.shape != (B,) or page_table.shape[0] != B or \
+            (new_lengths is not None and new_lengths.shape != (B,)):
+        raise ValueError(f"{name}: shape mismatch")
+    dev = _current_device(q)
+    ptrs = (_arg(q, et, "q", dev), _arg(pool, _U8, "pool", dev), _arg(page_table, _I32, "pageTable", dev),
+            _arg(indices, _I32, "indices", dev), _arg(ctx, _I32, "contextLengths", dev),
+            _opt(new_lengths, _I32, "new_lengths", dev))
+    return et, dev, ptrs, (B, S, Hq, Hkv, D, row, nflat, pages, indices.shape[2])
+
+
+def sparse_paged_kv4(q, pool, page_table, indices, ctx, out, *, scale, new_lengths=None, lse=None, status=None, stream=None):
+    """qsa_sparse_paged_kv4 (fp16) or qsa_sparse_paged_kv4_bf16: q/out [B,S,Hq,128], pool uint8
+    [numFlat,128,Hkv,rowBytes >= 80], indices int32 [B,S,topK], ctx int32 [B] cached lengths, new_lengths int32 [B] query
+    rows (None: min(S, ctx)); scale multiplies q . k; lse float32 [B,S,Hq] gets the log-sum-exp of the scaled logits."""
+    et, dev, ptrs, sizes = _lists4(q, pool, page_table, indices, ctx, new_lengths, "sparse_paged_kv4")
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+        raise ValueError("sparse_paged_kv4: shape mismatch")
+    packed = _PAGED4_PACK.pack(*ptrs, _arg(out, et, "out", dev), _opt(lse, _F32, "lse", dev),
+                               _opt(status, _I32, "status", dev), *sizes, scale, _raw_stream(stream, dev))
+    r = _packed("qsa_sparse_paged_kv4_bf16" if et is _BF16 else "qsa_sparse_paged_kv4")(packed)
+    if r:
+        _check(r)
+
+
+def sparse_weights_kv4(q, pool, page_table, indices, ctx, lse, weights, total=None, *, scale, new_lengths=None, status=None,
+                       stream=None):
+    """qsa_sparse_weights_kv4 (fp16) or qsa_sparse_weights_kv4_bf16: behind sparse_paged_kv4 with the same q, lists and
+    lengths and the lse it left: weights float32 [B,S,Hkv,topK] gets every list entry's attention weight, summed over the
+    query heads of a KV head, and total float32 [B,Hkv,tokens] (None: no totals) gathers them by token."""
+    et, dev, ptrs, sizes = _lists4(q, pool, page_table, indices, ctx, new_lengths, "sparse_weights_kv4")
+    B, S, _, Hkv = sizes[:4]
+    if lse.shape != q.shape[:3] or weights.shape != (B, S, Hkv, sizes[8]) or \
+            (total is not None and (total.dim() != 3 or total.shape[:2] != (B, Hkv))):
+        raise ValueError("sparse_weights_kv4: shape mismatch")
+    packed = _WEIGHTS4_PACK.pack(*ptrs, _arg(lse, _F32, "lse", dev), _arg(weights, _F32, "weights", dev),
+                                 _opt(total, _F32, "total", dev), _opt(status, _I32, "status", dev), *sizes,
+                                 0 if total is None else total.shape[2], scale, _raw_stream(stream, dev))
+    r = _packed("qsa_sparse_weights_kv4_bf16" if et is _BF16 else "qsa_sparse_weights_kv4")(packed)
+    if r:
+        _check(r)
+
+
+def evict_kv4(pool, page_table, ctx, total, kept, kept_lengths, total_out=None, *, sinks=0, recent=0, status=None,
+              stream=None):
+    """qsa_evict_kv4: cuts every sequence of pool uint8 [numFlat,128,Hkv,rowBytes >= 80] back to budget = kept.shape[2]
+    tokens per KV head, by total float32 [B,Hkv,tokens]; the first `sinks` and the last `recent` always stay.  kept int32
+    [B,Hkv,budget] gets the tokens now in each slot (-1 behind the last), kept_lengths int32 [B] the new lengths, total_out
+    (may be total) their totals, zeros behind them."""
+    nflat, Hkv, row, pages = _pool4(pool, page_table, "evict_kv4")
+    B = page_table.shape[0]
+    if total.dim() != 3 or total.shape[:2] != (B, Hkv) or kept.dim() != 3 or kept.shape[:2] != (B, Hkv) or \
+            ctx.shape != (B,) or kept_lengths.shape != (B,) or (total_out is not None and total_out.shape != total.shape):
+        raise ValueError("evict_kv4: shape mismatch")
+    dev = _current_device(pool)
+    packed = _EVICT4_PACK.pack(
+        _arg(pool, _U8, "pool", dev), _arg(page_table, _I32, "pageTable", dev), _arg(ctx, _I32, "contextLengths", dev),
+        _arg(total, _F32, "total", dev), _arg(kept, _I32, "kept", dev), _arg(kept_lengths, _I32, "kept_lengths", dev),
+        _opt(total_out, _F32, "total_out", dev), _opt(status, _I32, "status", dev), B, Hkv, 128, row, nflat, pages,
+        total.shape[2], kept.shape[2], sinks, recent, _raw_stream(stream, dev))
+    r = _packed("qsa_evict_kv4")(packed)
     if r:
         _check(r)

@@ -234,6 +234,136 @@ qsa_status_t sparse_paged_kv8_entry(const QsaSparsePagedKv8Params* p, const char
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
+// Whether rows of `len` elements, heads headStride and tokens tokenStride apart, lie apart from each other.
+bool rows_apart(long long tokens, long long heads, long long len, int64_t tokenStride, int64_t headStride) {
+  if (heads == 1) return tokens == 1 || tokenStride >= len;
+  if (tokens == 1) return headStride >= len;
+  // (heads and tokens below 2^31, so that the products stay below 2^63 for the strides that the first tests let through)
+  if (headStride >= len && headStride <= tokenStride / (heads - 1) && tokenStride >= (heads - 1) * headStride + len) return true;
+  return tokenStride >= len && tokenStride <= headStride / (tokens - 1) && headStride >= (tokens - 1) * tokenStride + len;
+}
+
+qsa_status_t rotary_entry(const QsaRotaryParams* p, const char* fn, int elem) {
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->x || !p->y || !p->positions || !p->invFreq) return fail(QSA_ERR_INVALID_ARG, "%s: a pointer is NULL", fn);
+  if (p->numTokens < 1 || p->numHeads < 1 || p->headDim < 1)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
+  if (p->rotDim < 2 || (p->rotDim & 1) || p->rotDim > p->headDim)
+    return fail(QSA_ERR_INVALID_ARG, "%s: rotDim %d must be even, >= 2 and <= headDim", fn, p->rotDim);
+  if (p->xTokenStride < 0 || p->xHeadStride < 0 || p->yTokenStride < 0 || p->yHeadStride < 0)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a stride is negative", fn);
+  if (!rows_apart(p->numTokens, p->numHeads, p->headDim, p->yTokenStride, p->yHeadStride))
+    return fail(QSA_ERR_INVALID_ARG, "%s: rows of y overlap under its strides", fn);
+  if (p->x == p->y && ((p->numTokens > 1 && p->xTokenStride != p->yTokenStride) ||
+                       (p->numHeads > 1 && p->xHeadStride != p->yHeadStride)))
+    return fail(QSA_ERR_INVALID_ARG, "%s: in place, x and y need the same strides", fn);
+  if (!std::isfinite(p->magnitude)) return fail(QSA_ERR_INVALID_ARG, "%s: magnitude is not finite", fn);
+  if (p->rotDim > 2 * qsa::kRotaryMaxPairs)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: rotDim %d > %d", fn, p->rotDim, 2 * qsa::kRotaryMaxPairs);
+  const size_t size = elem == 2 ? 4 : 2;
+  if (!aligned(p->x, size) || !aligned(p->y, size) || !aligned(p->positions, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: x and y must be aligned to their elements, positions to 4 bytes", fn);
+  // (two factors below 2^31 first, so that nothing overflows)
+  if (static_cast<long long>(p->numTokens) * p->numHeads > 0x7fffffffLL ||
+      static_cast<long long>(p->numTokens) * p->numHeads * p->headDim > 0x7fffffffLL)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: numTokens * numHeads * headDim must stay below 2^31", fn);
+  qsa::RotaryTurns rt;
+  for (int i = 0; i < p->rotDim / 2; ++i) {
+    double x = p->invFreq[i] / 6.283185307179586;
+    if (!std::isfinite(x)) return fail(QSA_ERR_INVALID_ARG, "%s: a frequency is not finite", fn);
+    x -= std::floor(x);
+    // a negative frequency's fraction may round to a whole turn
+    rt.turn[i] = x >= 1.0 ? 0 : static_cast<unsigned long long>(x * 18446744073709551616.0);
+  }
+  const cudaError_t e = qsa::launch_rotary(*p, rt, elem);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+qsa_status_t store_kv4_entry(const QsaStoreKv4Params* p, const char* fn, bool bf16) {
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->k || !p->v || !p->contextLengths || !p->kvPool || !p->pageTable)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+  if (p->batchSize < 1 || p->seqLen < 1 || p->numKVHeads < 1 || p->headDim < 1 || p->numFlatPages < 1 ||
+      p->maxPagesPerSeq < 1)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
+  const long long row = static_cast<long long>(p->numKVHeads) * p->headDim;
+  const bool several = p->batchSize > 1 || p->seqLen > 1;
+  if (several && (p->kTokenStride < row || p->vTokenStride < row))
+    return fail(QSA_ERR_INVALID_ARG, "%s: a token stride is below numKVHeads * headDim", fn);
+  if (p->poolRowBytes < QSA_KV4_ROW_BYTES)
+    return fail(QSA_ERR_INVALID_ARG, "%s: poolRowBytes < %d", fn, QSA_KV4_ROW_BYTES);
+  if (p->headDim != 128) return fail(QSA_ERR_UNSUPPORTED, "%s: headDim %d is not 128", fn, p->headDim);
+  if (p->poolRowBytes % 16 || (several && (p->kTokenStride % 8 || p->vTokenStride % 8)))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: poolRowBytes and token strides must be whole 16-byte chunks", fn);
+  if (!aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->kOut, 16) || !aligned(p->vOut, 16) ||
+      !aligned(p->kvPool, 16) || !aligned(p->contextLengths, 4) || !aligned(p->newLengths, 4) ||
+      !aligned(p->pageTable, 4) || !aligned(p->status, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: k, v, kOut, vOut and kvPool must be 16-byte aligned, the others 4", fn);
+  if (static_cast<long long>(p->batchSize) * p->seqLen > 0x7fffffffLL ||
+      static_cast<long long>(p->batchSize) * p->seqLen * p->numKVHeads > 0x7ffffffLL ||
+      static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numKVHeads) * p->poolRowBytes > 0x7fffffffLL)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen * numKVHeads, maxPagesPerSeq, numFlatPages or a pool row "
+                                     "too large", fn);
+  const cudaError_t e = qsa::launch_store_kv4(*p, bf16);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+// What the two readers of a 4-bit pool by lists check alike.
+template <typename P>
+qsa_status_t check_paged_kv4(const P* p, const char* fn) {
+  if (p->batchSize < 1 || p->seqLen < 1 || p->numQHeads < 1 || p->numKVHeads < 1 || p->headDim < 1 || p->topK < 1 ||
+      p->numFlatPages < 1 || p->maxPagesPerSeq < 1)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
+  if (p->numQHeads % p->numKVHeads) return fail(QSA_ERR_INVALID_ARG, "%s: numQHeads %% numKVHeads != 0", fn);
+  if (p->poolRowBytes < QSA_KV4_ROW_BYTES)
+    return fail(QSA_ERR_INVALID_ARG, "%s: poolRowBytes < %d", fn, QSA_KV4_ROW_BYTES);
+  if (!qsa_sparse_prefill_can_implement(p->numQHeads, p->numKVHeads, p->headDim))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: needs headDim 128 and a GQA group of at most 16", fn);
+  if (p->poolRowBytes % 16)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: poolRowBytes %d is not a multiple of 16", fn, p->poolRowBytes);
+  if (p->topK > (1 << 24)) return fail(QSA_ERR_UNSUPPORTED, "%s: topK > %d", fn, 1 << 24);
+  if (!aligned(p->qPtr, 16) || !aligned(p->kvPool, 16) || !aligned(p->pageTable, 4) || !aligned(p->indices, 4) ||
+      !aligned(p->contextLengths, 4) || !aligned(p->newLengths, 4) || !aligned(p->lse, 4) || !aligned(p->status, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: q and kvPool must be 16-byte aligned, the others 4", fn);
+  if (static_cast<long long>(p->batchSize) * p->seqLen > 0x7fffffffLL ||
+      static_cast<long long>(p->batchSize) * p->seqLen * p->numKVHeads > 0x7fffffffLL ||
+      static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numKVHeads) * p->poolRowBytes > 0x7fffffffLL)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * seqLen * numKVHeads, maxPagesPerSeq, numFlatPages or a pool row "
+                                     "too large", fn);
+  return QSA_OK;
+}
+
+qsa_status_t sparse_paged_kv4_entry(const QsaSparsePagedKv4Params* p, const char* fn, bool bf16) {
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->qPtr || !p->kvPool || !p->pageTable || !p->indices || !p->contextLengths || !p->oPtr)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a tensor pointer is NULL", fn);
+  const qsa_status_t s = check_paged_kv4(p, fn);
+  if (s != QSA_OK) return s;
+  if (!aligned(p->oPtr, 16)) return fail(QSA_ERR_UNSUPPORTED, "%s: o must be 16-byte aligned", fn);
+  const cudaError_t e = qsa::launch_sparse_paged_kv4(*p, bf16);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
+qsa_status_t sparse_weights_kv4_entry(const QsaSparseWeightsKv4Params* p, const char* fn, bool bf16) {
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->qPtr || !p->kvPool || !p->pageTable || !p->indices || !p->contextLengths || !p->lse || !p->weights)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a tensor pointer is NULL", fn);
+  if (p->totalLen < 0 || (p->total == nullptr) != (p->totalLen == 0))
+    return fail(QSA_ERR_INVALID_ARG, "%s: total needs totalLen >= 1, without it totalLen is 0", fn);
+  const qsa_status_t s = check_paged_kv4(p, fn);
+  if (s != QSA_OK) return s;
+  if (!aligned(p->weights, 4) || !aligned(p->total, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: weights and total must be 4-byte aligned", fn);
+  if (static_cast<long long>(p->batchSize) * p->numKVHeads > 65535)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * numKVHeads > 65535", fn);
+  const cudaError_t e = qsa::launch_sparse_weights_kv4(*p, bf16);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -456,6 +586,88 @@ qsa_status_t qsa_sparse_paged_kv8(const QsaSparsePagedKv8Params* p) {
 }
 qsa_status_t qsa_sparse_paged_kv8_bf16(const QsaSparsePagedKv8Params* p) {
   return sparse_paged_kv8_entry(p, "qsa_sparse_paged_kv8_bf16", true);
+}
+
+qsa_status_t qsa_rotary(const QsaRotaryParams* p) { return rotary_entry(p, "qsa_rotary", 0); }
+qsa_status_t qsa_rotary_bf16(const QsaRotaryParams* p) { return rotary_entry(p, "qsa_rotary_bf16", 1); }
+qsa_status_t qsa_rotary_f32(const QsaRotaryParams* p) { return rotary_entry(p, "qsa_rotary_f32", 2); }
+
+qsa_status_t qsa_rotary_frequencies(int32_t scaling, int32_t rot, double theta, double factor, double length,
+                                    double lowTurns, double highTurns, double* out) {
+  const char* fn = "qsa_rotary_frequencies";
+  if (!out) return fail(QSA_ERR_INVALID_ARG, "%s: invFreq is NULL", fn);
+  if (scaling < QSA_ROTARY_PLAIN || scaling > QSA_ROTARY_RAMP)
+    return fail(QSA_ERR_INVALID_ARG, "%s: unknown scaling %d", fn, scaling);
+  if (rot < (scaling == QSA_ROTARY_BASE ? 4 : 2) || (rot & 1))
+    return fail(QSA_ERR_INVALID_ARG, "%s: rotDim %d must be even and >= 2 (base scaling: 4)", fn, rot);
+  if (!(theta > 1.0) || !std::isfinite(theta)) return fail(QSA_ERR_INVALID_ARG, "%s: theta must be finite and > 1", fn);
+  if (scaling != QSA_ROTARY_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(QSA_ERR_INVALID_ARG, "%s: factor must be finite and >= 1", fn);
+  if (scaling >= QSA_ROTARY_BLEND && (!(length >= 1.0) || !std::isfinite(length) || !(lowTurns > 0.0) ||
+                                      !(highTurns > lowTurns) || !std::isfinite(highTurns)))
+    return fail(QSA_ERR_INVALID_ARG, "%s: needs originalLength >= 1 and 0 < lowTurns < highTurns", fn);
+  const double turn = 6.283185307179586;
+  const double base = scaling == QSA_ROTARY_BASE ? theta * std::pow(factor, rot / (rot - 2.0)) : theta;
+  // the (fractional) pair that turns n times in the original length
+  auto pair_of = [&](double n) { return 0.5 * rot * std::log(length / (turn * n)) / std::log(theta); };
+  const double first = scaling == QSA_ROTARY_RAMP ? std::floor(pair_of(highTurns)) : 0.0;
+  const double last = scaling == QSA_ROTARY_RAMP ? std::ceil(pair_of(lowTurns)) : 0.0;
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot);
+    double keep = 1.0;  // the share of the unscaled frequency
+    if (scaling == QSA_ROTARY_LINEAR) keep = 0.0;
+    if (scaling == QSA_ROTARY_BLEND) keep = (length * f / turn - lowTurns) / (highTurns - lowTurns);
+    if (scaling == QSA_ROTARY_RAMP) keep = (last - i) / (last - first);  // last > first: floor(a) < ceil(b) for a < b
+    keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+    out[i] = keep * f + (1.0 - keep) * f / (keep == 1.0 ? 1.0 : factor);
+  }
+  return ok();
+}
+
+qsa_status_t qsa_store_kv4(const QsaStoreKv4Params* p) { return store_kv4_entry(p, "qsa_store_kv4", false); }
+qsa_status_t qsa_store_kv4_bf16(const QsaStoreKv4Params* p) { return store_kv4_entry(p, "qsa_store_kv4_bf16", true); }
+qsa_status_t qsa_sparse_paged_kv4(const QsaSparsePagedKv4Params* p) {
+  return sparse_paged_kv4_entry(p, "qsa_sparse_paged_kv4", false);
+}
+qsa_status_t qsa_sparse_paged_kv4_bf16(const QsaSparsePagedKv4Params* p) {
+  return sparse_paged_kv4_entry(p, "qsa_sparse_paged_kv4_bf16", true);
+}
+qsa_status_t qsa_sparse_weights_kv4(const QsaSparseWeightsKv4Params* p) {
+  return sparse_weights_kv4_entry(p, "qsa_sparse_weights_kv4", false);
+}
+qsa_status_t qsa_sparse_weights_kv4_bf16(const QsaSparseWeightsKv4Params* p) {
+  return sparse_weights_kv4_entry(p, "qsa_sparse_weights_kv4_bf16", true);
+}
+
+qsa_status_t qsa_evict_kv4(const QsaEvictKv4Params* p) {
+  const char* fn = "qsa_evict_kv4";
+  if (!p) return fail(QSA_ERR_INVALID_ARG, "%s: params is NULL", fn);
+  if (!p->kvPool || !p->pageTable || !p->contextLengths || !p->total || !p->kept || !p->keptLengths)
+    return fail(QSA_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+  if (p->batchSize < 1 || p->numKVHeads < 1 || p->headDim < 1 || p->numFlatPages < 1 || p->maxPagesPerSeq < 1 ||
+      p->totalLen < 1 || p->budget < 1)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sizes must be >= 1", fn);
+  if (p->sinks < 0 || p->recent < 0 || static_cast<long long>(p->sinks) + p->recent > p->budget)
+    return fail(QSA_ERR_INVALID_ARG, "%s: sinks and recent must be >= 0 and together at most the budget", fn);
+  if (p->poolRowBytes < QSA_KV4_ROW_BYTES)
+    return fail(QSA_ERR_INVALID_ARG, "%s: poolRowBytes < %d", fn, QSA_KV4_ROW_BYTES);
+  if (p->keptLengths == p->contextLengths)
+    return fail(QSA_ERR_INVALID_ARG, "%s: keptLengths must not be contextLengths (which other heads still read)", fn);
+  if (p->headDim != 128) return fail(QSA_ERR_UNSUPPORTED, "%s: headDim %d is not 128", fn, p->headDim);
+  if (p->poolRowBytes % 16)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: poolRowBytes %d is not a multiple of 16", fn, p->poolRowBytes);
+  if (!aligned(p->kvPool, 16) || !aligned(p->pageTable, 4) || !aligned(p->contextLengths, 4) || !aligned(p->total, 4) ||
+      !aligned(p->kept, 4) || !aligned(p->keptLengths, 4) || !aligned(p->totalOut, 4) || !aligned(p->status, 4))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: kvPool must be 16-byte aligned, the others 4", fn);
+  if (static_cast<long long>(p->batchSize) * p->numKVHeads > 0x7ffffffLL ||
+      static_cast<long long>(p->maxPagesPerSeq) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numFlatPages) * qsa::kTokensPerPageHost > 0x7fffffffLL ||
+      static_cast<long long>(p->numKVHeads) * p->poolRowBytes > 0x7fffffffLL || p->totalLen > (1 << 24) ||
+      p->budget > (1 << 24))
+    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * numKVHeads, maxPagesPerSeq, numFlatPages, totalLen, budget or a "
+                                     "pool row too large", fn);
+  const cudaError_t e = qsa::launch_evict_kv4(*p);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }
 
 int32_t qsa_gather_scratch_pages(int32_t topK) { return topK < 1 ? 0 : qsa::gather_scratch_pages(topK); }

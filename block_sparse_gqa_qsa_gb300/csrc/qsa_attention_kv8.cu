@@ -32,104 +32,26 @@
 // order that makes its columns the second product's fragments of P^T.
 #include <algorithm>
 #include <atomic>
-#include <cfloat>
 #include <utility>
 
-#include "qsa_internal.h"
-#include "qsa_kv8.cuh"
+#include "qsa_paged.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kD = 128;
-constexpr int kStep = 32;                      // list entries of a warp's step
+constexpr int kThreads = kPagedThreads;
+constexpr int kWarps = kPagedWarps;
 constexpr int kTileBytes = kStep * kD;         // K (or V) rows of a step
 // A warp's shared memory in the split form: two K tiles, two V tiles, the pool rows of two steps' entries (K then V), the
 // values of a step's entries.
 constexpr int kRowsAt = 4 * kTileBytes;
 constexpr int kEntriesAt = kRowsAt + 2 * 2 * kStep * 4;
 constexpr int kWarpBytes = kEntriesAt + kStep * 16;
-constexpr int kMaxCluster = 8;
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct PagedArgs {
-  const void* q;
-  const uint8_t* pool;
-  const float* scale;
-  const int32_t* pageTable;
-  const int32_t* indices;
-  const int32_t* ctx;
-  const int32_t* newLen;  // may be null
-  void* o;
-  int32_t* status;  // may be null
-  int S, Hq, Hkv, G, poolHeadDim, numFlatPages, maxPagesPerSeq, topK;
-  int blockShift;  // log2(scaleBlock)
-  int split;       // CTAs per pair: the cluster size
-  float sl2;       // attentionScale * log2(e)
-};
-
-__device__ __forceinline__ float ex2_ftz(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ float cluster_ld(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr));
-  return v;
-}
-
-template <bool kBf16>
-__device__ __forceinline__ uint2 pack4(float4 v) {
-  return kBf16 ? make_uint2(pack_bf162(v.x, v.y), pack_bf162(v.z, v.w))
-               : make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
-}
 
 // Byte offset of 16-byte chunk c of key row r in a step's K tile (a lane group reads chunks 0..3 or 4..7 of two rows of
 // different parity) and V tile (ldmatrix reads one chunk of 8 successive rows): each access covers all banks once.
 __device__ __forceinline__ uint32_t k_off(int r, int c) { return r * kD + ((c ^ ((r & 1) << 2)) << 4); }
 __device__ __forceinline__ uint32_t v_off(int r, int c) { return r * kD + ((c ^ (r & 7)) << 4); }
-// Key of row g of an S^T fragment (row g + 8: two keys on), within its 16 keys.
-__device__ __forceinline__ int key_of(int g) { return 4 * (g >> 1) + (g & 1); }
-
-// 16-byte copy to dst + kOff.
-template <int kOff>
-__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;\n" ::"r"(dst), "l"(src), "n"(kOff) : "memory");
-}
-template <int kOff>
-__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void* src, bool pred) {
-  asm volatile("cp.async.cg.shared.global [%0 + %3], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(pred ? 16 : 0), "n"(kOff)
-               : "memory");
-}
-__device__ __forceinline__ float lg2_ftz(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_ftz(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // One lane's eight 16-byte copies of a gather: rows 4 i + (lane >> 3), i = 0..7, each at dst[i & 1] + 512 i.
 // base: the lane's chunk of pool row 0.  kAll: every row is named (row >= 0); otherwise the others are zeros.
 template <bool kAll, size_t... I>
@@ -143,30 +65,6 @@ __device__ __forceinline__ void copy_rows(const int (&row)[8], const uint32_t (&
      ...);
   }
 }
-
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// Two transposed 16 x 16 byte matrices (rows at the addresses of lanes 0..15 and 16..31): of each, the lane gets rows
-// 4 q .. 4 q + 3 of column g, then of column g + 8.
-__device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-// A warp's running state: O^T fragments, max and sum of its heads 8 nt + 2 q, 8 nt + 2 q + 1 (q = lane & 3).
-// Tile mt holds dims 16 mt + g and 16 mt + g + 8, g = lane >> 2.
-template <int NT>
-struct Acc {
-  float o[8][NT][4];
-  float m[NT][2];
-  float l[NT][2];
-};
 
 // S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + key_of(g) and 2 on, heads 8 nt + 2 q and + 1.
 template <int NT>
@@ -188,89 +86,6 @@ __device__ __forceinline__ void scores32(float (&s)[2][NT][4], uint32_t tile, co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(s[gk][nt], a, qf[nt][4 * half + w][0], qf[nt][4 * half + w][1]);
       }
-    }
-  }
-}
-
-// Online softmax of a step: s becomes the weights relative to the running maximum, returned in fp16 as the B
-// fragments of the second product.  The maximum moves only when a weight would pass 2^kHeadroom (the weights
-// are relative numbers: nothing is lost by their being up to 256 instead of 1), so that O is hardly ever
-// rescaled after a warp's first step.  The sums use the weights as the second product does, rounded to 11 bits: where
-// few keys decide, a rounding that only one of the two had would show in an fp16 output (up to 2^-11 of it, as much as
-// its half step).  The maximum starts at the lowest finite number, so that an entry that names nothing
-// (-inf) weighs 0 even before the first that does.  entries[i], of key i: x = K scale * attentionScale * log2(e),
-// y = log2(V scale), z = 1 / V scale; (0, -inf, 0) for an entry that names nothing.
-template <int NT, bool kBf16>
-__device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], const float (&qs)[NT][2],
-                                          const float4* entries, uint32_t (&pb)[2][NT][2]) {
-  constexpr float kHeadroom = 8.f;
-  const int key = key_of((threadIdx.x & 31) >> 2);
-  float ks[4], lv[4], iv[4];  // of the lane's keys
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 e = entries[key + 16 * (i >> 1) + 2 * (i & 1)];
-    ks[i] = e.x;
-    lv[i] = e.y;
-    iv[i] = e.z;
-  }
-  float mx[NT][2];
-  bool move = false;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float& x = s[i >> 1][nt][2 * (i & 1) + h];
-        // bf16: the K scale first (the product is below 2^31, so with scales below 2^96 only a logit itself overflows)
-        x = kBf16 ? fmaf(x * ks[i], qs[nt][h], lv[i]) : fmaf(x, ks[i], lv[i]);
-      }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mx[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx[nt][h] = fmaxf(mx[nt][h], __shfl_xor_sync(kFull, mx[nt][h], o));
-      move |= mx[nt][h] > A.m[nt][h] + kHeadroom;
-    }
-  }
-  if (__any_sync(kFull, move)) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float al[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float mn = fmaxf(A.m[nt][h], mx[nt][h]);
-        al[h] = ex2_ftz(A.m[nt][h] - mn);
-        A.m[nt][h] = mn;
-        A.l[nt][h] *= al[h];
-      }
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        A.o[mt][nt][0] *= al[0];
-        A.o[mt][nt][1] *= al[1];
-        A.o[mt][nt][2] *= al[0];
-        A.o[mt][nt][3] *= al[1];
-      }
-    }
-  }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float* x = &s[i >> 1][nt][2 * (i & 1)];
-      const uint64_t w = pack_f2(ex2_ftz(x[0] - A.m[nt][0]), ex2_ftz(x[1] - A.m[nt][1]));
-      // 8193 w - 8192 w, the first rounded to 24 bits: w to 11
-      const uint64_t r = ffma2(pack_f2(-8192.f, -8192.f), w, ffma2(pack_f2(8192.f, 8192.f), w, w));
-      x[0] = lo_f2(r);
-      x[1] = hi_f2(r);
-      A.l[nt][0] = fmaf(x[0], iv[i], A.l[nt][0]);
-      A.l[nt][1] = fmaf(x[1], iv[i], A.l[nt][1]);
-    }
-    // the weights in fp16: as they are from 2^-14 on, to 2^-25 below
-#pragma unroll
-    for (int gk = 0; gk < 2; ++gk) {
-      pb[gk][nt][0] = movmatrix_t(pack_half2(s[gk][nt][0], s[gk][nt][1]));
-      pb[gk][nt][1] = movmatrix_t(pack_half2(s[gk][nt][2], s[gk][nt][3]));
     }
   }
 }
@@ -339,8 +154,6 @@ __device__ __forceinline__ void load_q(const uint4* q, int G, uint32_t (&qf)[NT]
   }
 }
 
-constexpr int kPad = kD + 4;  // floats of a head in the merge buffers
-
 // Resident CTAs per SM.  Many rows: the register budget decides.  With 4, groups up to 8 keep a little of a lane in local
 // memory (four fp16 heads 28 bytes, four or two bf16 heads 8 and 16); 5 at 96 registers spill far more and took 1333 us
 // for an 8192-row prompt against 1275 with 4; 16-head groups at 168 registers 2008 against 1928 with 2.  Split: two tiles of
@@ -355,66 +168,6 @@ template <int NT>
 constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kPad + 2) * 4 ? kWarps * kWarpBytes
                                                                                : (kWarps + 1) * 8 * NT * (kPad + 2) * 4;
 
-// What a CTA (or cluster) works on: a row of the call and successive KV heads.
-struct Row {
-  int kvh, b, t, L, n;  // first KV head, sequence, row, the tokens that its page table holds, its live rows
-  size_t bt, head0;     // list row; first query head
-};
-// The place of work item `id` with `heads` KV heads each; its lengths are read by row_lengths.
-__device__ __forceinline__ Row row_of(const PagedArgs& a, int id, int heads) {
-  Row r;
-  const int per = a.Hkv / heads, rowid = id / per;
-  r.kvh = (id - rowid * per) * heads;
-  r.b = rowid / a.S;
-  r.t = a.S - 1 - (rowid - r.b * a.S);  // a sequence's rows from the last position down: the longest lists start first
-  r.bt = static_cast<size_t>(r.b) * a.S + r.t;
-  r.head0 = r.bt * a.Hq + static_cast<size_t>(r.kvh) * a.G;
-  return r;
-}
-__device__ __forceinline__ void row_lengths(const PagedArgs& a, Row& r) {
-  const int L = max(0, a.ctx[r.b]);
-  r.L = min(L, a.maxPagesPerSeq * kTokensPerPage);
-  r.n = max(0, min(a.newLen ? a.newLen[r.b] : a.S, min(a.S, L)));
-}
-
-// From list entries to pool rows, free of branches: what an entry cannot name is looked up at 0 and dropped.
-struct Pages {
-  int j, k, v;  // entry (-1: none), its page ids
-};
-struct PoolRows {
-  bool ok;   // the entry names a row
-  int k, v;  // its rows of the pool (0 for none)
-};
-struct List {
-  const PagedArgs& a;
-  const int32_t *entries, *ptK, *ptV;
-  int L, bad;
-  __device__ __forceinline__ List(const PagedArgs& args, const Row& r)
-      : a(args),
-        entries(args.indices + r.bt * args.topK),
-        ptK(args.pageTable + static_cast<size_t>(r.b) * 2 * args.maxPagesPerSeq),
-        ptV(ptK + args.maxPagesPerSeq),
-        L(0),
-        bad(0) {}
-  __device__ __forceinline__ int at(int slot) const { return slot < a.topK ? __ldg(entries + slot) : -1; }
-  __device__ __forceinline__ Pages pages_of(int j) {
-    const bool in = static_cast<unsigned>(j) < static_cast<unsigned>(L);
-    bad |= !in && j != -1 ? kErrBadIndex : 0;
-    const int page = in ? j >> 7 : 0;
-    return Pages{in ? j : -1, __ldg(ptK + page), __ldg(ptV + page)};
-  }
-  __device__ __forceinline__ PoolRows rows_of(const Pages& p) {
-    const bool pages = static_cast<unsigned>(p.k) < static_cast<unsigned>(a.numFlatPages) &&
-                       static_cast<unsigned>(p.v) < static_cast<unsigned>(a.numFlatPages);
-    const bool ok = p.j >= 0 && pages;
-    bad |= p.j >= 0 && !pages ? kErrBadPage : 0;
-    return PoolRows{ok, ok ? p.k * kTokensPerPage + (p.j & 127) : 0, ok ? p.v * kTokensPerPage + (p.j & 127) : 0};
-  }
-  __device__ __forceinline__ void report() {
-    bad = __reduce_or_sync(kFull, static_cast<unsigned>(bad));
-    if (bad && (threadIdx.x & 31) == 0 && a.status) atomicOr(a.status, bad);
-  }
-};
 // The scales of a pool row, from KV head kvh on.
 __device__ __forceinline__ const float* scales_of(const PagedArgs& a, int row, int kvh) {
   return a.scale + static_cast<size_t>(row >> a.blockShift) * a.Hkv + kvh;
@@ -452,17 +205,6 @@ __device__ __forceinline__ void gather_rows(const int* ids, unsigned mask, const
   cp_async_commit();
 }
 
-template <int NT>
-__device__ __forceinline__ void acc_init(Acc<NT>& A) {
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) A.o[mt][nt][0] = A.o[mt][nt][1] = A.o[mt][nt][2] = A.o[mt][nt][3] = 0.f;
-    A.m[nt][0] = A.m[nt][1] = -FLT_MAX;
-    A.l[nt][0] = A.l[nt][1] = 0.f;
-  }
-}
-
 // A warp's result to shared memory: o [8 NT heads][kPad] fp32 (kPad puts a fragment's writes in different banks), m, l [8 NT].
 template <int NT>
 __device__ __forceinline__ void stash(const Acc<NT>& A, float* o, float* m, float* l) {
@@ -487,34 +229,6 @@ __device__ __forceinline__ void stash(const Acc<NT>& A, float* o, float* m, floa
       }
     }
 }
-// Joins the warps' stashed results of head h: the lane's four dims relative to the largest maximum, which is returned
-// with the sum.
-template <int H>
-__device__ __forceinline__ float4 join(const float* o, const float* m, const float* l, int h, float& M, float& sum) {
-  M = -FLT_MAX;
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m[w * H + h]);
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int k = w * H + h;
-    const float f = exp2f(m[k] - M);
-    const float4 x = *reinterpret_cast<const float4*>(o + k * kPad + 4 * (threadIdx.x & 31));
-    sum += f * l[k];
-    r.x += f * x.x;
-    r.y += f * x.y;
-    r.z += f * x.z;
-    r.w += f * x.w;
-  }
-  return r;
-}
-template <bool kBf16>
-__device__ __forceinline__ uint2 normalised(const float4& o, float sum) {
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  return pack4<kBf16>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-}
-
 // Few (row, KV head) pairs: the warps of a CTA, and the CTAs of a cluster, share one pair's list.
 template <int NT, bool kBf16>
 __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv8_split_kernel(const PagedArgs a) {
@@ -906,6 +620,7 @@ cudaError_t launch_sparse_paged_kv8(const QsaSparsePagedKv8Params& p, bool bf16)
   while ((1 << a.blockShift) < p.scaleBlock) ++a.blockShift;
   a.split = 1;
   a.sl2 = p.attentionScale * kLog2e;
+  a.lse = nullptr;
   const long long pairs = static_cast<long long>(p.batchSize) * p.seqLen * p.numKVHeads;
   cudaStream_t st = static_cast<cudaStream_t>(p.stream);
   if (bf16) return a.G <= 8 ? paged_go<1, true>(a, pairs, st) : paged_go<2, true>(a, pairs, st);

@@ -59,6 +59,19 @@ constexpr int kRopeMaxRowBytes = 64 * 1024;  // one token's packed heads, staged
 cudaError_t launch_append_kv(const QsaAppendKvParams& p, const RopeFreqs& rf, bool bf16, bool kv8);
 cudaError_t launch_sparse_paged_kv8(const QsaSparsePagedKv8Params& p, bool bf16);
 
+// Rotary positions: turn[i] = frac(invFreq[i] / (2 pi)) * 2^64 (see RopeFreqs); elem: 0 fp16, 1 bf16, 2 fp32.
+constexpr int kRotaryMaxPairs = 128;
+struct RotaryTurns {
+  unsigned long long turn[kRotaryMaxPairs];
+};
+cudaError_t launch_rotary(const QsaRotaryParams& p, const RotaryTurns& rt, int elem);
+
+// 4-bit cache ---------------------------------------------------------------
+cudaError_t launch_store_kv4(const QsaStoreKv4Params& p, bool bf16);
+cudaError_t launch_sparse_paged_kv4(const QsaSparsePagedKv4Params& p, bool bf16);
+cudaError_t launch_sparse_weights_kv4(const QsaSparseWeightsKv4Params& p, bool bf16);
+cudaError_t launch_evict_kv4(const QsaEvictKv4Params& p);
+
 cudaError_t launch_gather(const QsaGatherParams& p);
 int gather_scratch_pages(int topK);
 int gather_max_row_chunks();  // 16-byte chunks of one K (or V) token row a warp copies

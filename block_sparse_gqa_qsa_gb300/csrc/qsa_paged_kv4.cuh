@@ -1,0 +1,127 @@
+// qsa_paged_kv4.cuh -- tiles of a 4-bit paged pool as the kernels that read it
+// by lists hold them: 32 gathered rows of K (and V), their scale chunks, and
+// the first product S^T = C^K Q^T.
+//
+// A row's value is c s_j t.  c s_j has at most 6 significant bits and lies in
+// fp16's range, so codes become f16 pairs by a conversion and an exact product
+// with their group's scale; t multiplies what comes out in fp32.
+#pragma once
+
+#include "qsa_kv4.cuh"
+#include "qsa_paged.cuh"
+
+namespace qsa {
+
+constexpr int kKv4CodeBytes = kStep * kKv4Codes;   // codes of a step's K (or V) rows
+constexpr int kKv4ScaleBytes = kStep * kKv4Chunk;  // their scale chunks
+
+// Place of a step's entry i among its 32 row ids: a lane gathers rows 8 i + (lane >> 2), which lie together.
+__device__ __forceinline__ int kv4_row_place(int i) { return (i & 7) * 4 + (i >> 3); }
+
+// A lane's shares of a gather: 16 bytes of the codes of rows 8 i + (lane >> 2), i = 0..3, to dst + 512 i, and its own
+// row's scale chunk.  Rows that no entry names (id -1) become zeros.
+__device__ __forceinline__ void kv4_copy_codes(const int* ids, unsigned mask, uint32_t dst, const uint8_t* base,
+                                               uint32_t rowBytes) {
+  const int4 r = *reinterpret_cast<const int4*>(ids + ((threadIdx.x & 31) >> 2) * 4);
+  auto src = [&](int row) { return base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes; };
+  if (mask == kFull) {
+    cp_async16_to<0>(dst, src(r.x));
+    cp_async16_to<512>(dst, src(r.y));
+    cp_async16_to<1024>(dst, src(r.z));
+    cp_async16_to<1536>(dst, src(r.w));
+  } else {
+    cp_async16_to<0>(dst, src(r.x), r.x >= 0);
+    cp_async16_to<512>(dst, src(r.y), r.y >= 0);
+    cp_async16_to<1024>(dst, src(r.z), r.z >= 0);
+    cp_async16_to<1536>(dst, src(r.w), r.w >= 0);
+  }
+}
+__device__ __forceinline__ void kv4_copy_scales(int row, uint32_t dst, const uint8_t* base, uint32_t rowBytes) {
+  cp_async16_to<0>(dst, base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes + kKv4Codes, row >= 0);
+}
+
+// S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + key_of(g) and 2 on, heads 8 nt + 2 q and + 1.  A lane
+// reads a key's 16 bytes q of codes, 32 dims with two scales: k-step w covers dims 32 q + 4 w .. + 3 of every q.  (Rows of
+// 64 bytes: two of different parity lie in different banks.)
+template <int NT>
+__device__ __forceinline__ void kv4_scores(float (&s)[2][NT][4], uint32_t codes, uint32_t scales,
+                                           const uint32_t (&qf)[NT][8][2]) {
+  const int lane = threadIdx.x & 31, key = key_of(lane >> 2), q = lane & 3;
+#pragma unroll
+  for (int gk = 0; gk < 2; ++gk) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[gk][nt][0] = s[gk][nt][1] = s[gk][nt][2] = s[gk][nt][3] = 0.f;
+    uint4 r[2];
+    uint32_t sc[2][2];  // (s, s) of a row's two groups
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 16 * gk + key + 2 * i;
+      r[i] = lds16(codes + row * kKv4Codes + q * 16);
+      uint32_t b, pair, none;
+      asm volatile("{\n .reg .b16 t;\n ld.shared.b16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n"
+                   : "=r"(b)
+                   : "r"(scales + row * kKv4Chunk + 2 * q));
+      e4m3_to_f16(b, pair, none);
+      sc[i][0] = __byte_perm(pair, 0, 0x1010);
+      sc[i][1] = __byte_perm(pair, 0, 0x3232);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t a[2][4];  // of k-steps 2 w, 2 w + 1
+      e2m1_to_f16(word(r[0], w), a[0][0], a[0][2], a[1][0], a[1][2]);
+      e2m1_to_f16(word(r[1], w), a[0][1], a[0][3], a[1][1], a[1][3]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[k][i] = hmul2(a[k][i], sc[i & 1][w >> 1]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[gk][nt], a[k], qf[nt][2 * w + k][0], qf[nt][2 * w + k][1]);
+      }
+    }
+  }
+}
+
+// The group's Q^T fragments: k-step w of a lane covers dims 32 q + 4 w .. + 3, as the K codes do.  bf16 values are scaled
+// by a power of two per head to fp16's upper range; qs gets its inverse for the lane's heads 2 q, 2 q + 1.
+template <int NT, bool kBf16>
+__device__ __forceinline__ void kv4_load_q(const uint4* q, int G, uint32_t (&qf)[NT][8][2], float (&qs)[NT][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int h = 8 * nt + g;
+    uint4 raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = h < G ? __ldg(q + h * (kD / 8) + 4 * c + i) : make_uint4(0, 0, 0, 0);
+    float up = 1.f, down = 1.f;
+    if constexpr (kBf16) {
+      uint32_t m = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max(m, max(word(raw[i], w) & 0x7fff, (word(raw[i], w) >> 16) & 0x7fff));
+      m = max(m, __shfl_xor_sync(kFull, m, 1));
+      m = max(m, __shfl_xor_sync(kFull, m, 2));
+      // exponent e of the largest: scaled by 2^(14 - e), or 2^114 where that is less, so that the inverse is a normal
+      // number; not for 0, inf and NaN
+      const int e = static_cast<int>(m >> 7) - 127;
+      if (m != 0 && e < 128) {
+        const int k = 14 - max(e, -100);
+        up = __int_as_float((127 + k) << 23);
+        down = __int_as_float((127 - k) << 23);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t v = word(raw[i], w);
+        if constexpr (kBf16) v = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+        // 16-byte piece i holds dims 32 c + 8 i + 2 w: k-step 2 i + w / 2
+        qf[nt][2 * i + (w >> 1)][w & 1] = v;
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(kFull, down, 4 * (2 * c + j));
+  }
+}
+
+}  // namespace qsa

@@ -563,6 +563,260 @@ typedef struct {
 QSA_API qsa_status_t qsa_sparse_paged_kv8(const QsaSparsePagedKv8Params* params);
 QSA_API qsa_status_t qsa_sparse_paged_kv8_bf16(const QsaSparsePagedKv8Params* params);
 
+/* ------------------------------------------------------- rotary positions */
+
+/* Rotary positions of any heads, at positions that the caller names: for a
+ * token at position p >= 0 and i < rotDim / 2, dims a = i, b = i + rotDim / 2
+ * of a head (interleaved: a = 2i, b = 2i + 1) become
+ *   y_a = magnitude * (x_a cos(p f_i) - x_b sin(p f_i))
+ *   y_b = magnitude * (x_b cos(p f_i) + x_a sin(p f_i))
+ * with f_i = invFreq[i] (angle negated: inverse).  Dims past rotDim are copied
+ * (as they are); a token at a negative position is padding: its row of y is left as it was.
+ * The gradient of a loss with respect to x is the same call with `inverse` on
+ * the gradient with respect to y.
+ * Arithmetic: the angle is an exact fraction of a turn (p times a 64-bit
+ * fixed-point f_i / (2 pi)), its cosine and sine and the rotation are fp32,
+ * the result is rounded once.
+ * y may be x itself with the same strides (only rotated dims are then read and
+ * written); otherwise the two must not overlap.  x and y may be views: heads
+ * of a packed projection, rows with padding.
+ * Errors: QSA_ERR_INVALID_ARG for a NULL pointer, sizes < 1, rotDim odd, < 2
+ * or > headDim, a negative stride, strides of y under which two of its rows
+ * overlap, x == y with different strides, a magnitude or frequency that is not
+ * finite; QSA_ERR_UNSUPPORTED for rotDim > 256, a tensor not aligned to its
+ * element (positions: 4), or numTokens * numHeads * headDim of 2^31 or more.
+ * Nothing is allocated; invFreq is read before the call returns. */
+typedef struct {
+  const void* x;                 /* [numTokens, numHeads, headDim], by the strides below                  */
+  void* y;                       /* out, same type and shape                                              */
+  const int32_t* positions;      /* int32 [numTokens]; negative: padding                                  */
+  const double* invFreq;         /* HOST memory: rotDim / 2 angles per position                           */
+  int64_t xTokenStride;          /* elements                                                              */
+  int64_t xHeadStride;
+  int64_t yTokenStride;
+  int64_t yHeadStride;
+  int32_t numTokens;
+  int32_t numHeads;
+  int32_t headDim;
+  int32_t rotDim;
+  int32_t interleaved;           /* 0: pairs (i, i + rotDim/2); else (2i, 2i + 1)                         */
+  int32_t inverse;               /* 0: by the angle; else back by it                                      */
+  float magnitude;               /* 1 for a plain rotation                                                */
+  void* stream;
+} QsaRotaryParams;
+
+QSA_API qsa_status_t qsa_rotary(const QsaRotaryParams* params);      /* fp16 */
+QSA_API qsa_status_t qsa_rotary_bf16(const QsaRotaryParams* params);
+QSA_API qsa_status_t qsa_rotary_f32(const QsaRotaryParams* params);
+
+/* Frequencies of qsa_rotary, written to HOST memory invFreq[rotDim / 2]:
+ * f_i = theta^(-2i/rotDim), scaled for contexts longer than the trained one
+ * by `scaling`:
+ *   QSA_ROTARY_PLAIN   f_i
+ *   QSA_ROTARY_LINEAR  f_i / factor
+ *   QSA_ROTARY_BASE    with theta * factor^(rotDim / (rotDim - 2)): the fastest pair keeps its
+ *                      frequency, the slowest is divided by the factor
+ *   QSA_ROTARY_BLEND   with n_i = originalLength f_i / (2 pi) turns in the trained length and
+ *                      s = clamp((n_i - lowTurns) / (highTurns - lowTurns), 0, 1):
+ *                      s f_i + (1 - s) f_i / factor
+ *   QSA_ROTARY_RAMP    the same with s linear in the pair's index between the pairs that turn
+ *                      highTurns (rounded down) and lowTurns (rounded up) times
+ * Errors: QSA_ERR_INVALID_ARG for a NULL pointer, an odd rotDim, rotDim < 2
+ * (QSA_ROTARY_BASE: < 4), an unknown scaling, theta <= 1 or not finite, factor < 1 or not finite,
+ * and for the last two originalLength < 1 or not 0 < lowTurns < highTurns. */
+enum { QSA_ROTARY_PLAIN = 0, QSA_ROTARY_LINEAR = 1, QSA_ROTARY_BASE = 2, QSA_ROTARY_BLEND = 3, QSA_ROTARY_RAMP = 4 };
+QSA_API qsa_status_t qsa_rotary_frequencies(int32_t scaling, int32_t rotDim, double theta, double factor,
+                                            double originalLength, double lowTurns, double highTurns, double* invFreq);
+
+/* ------------------------------------------------------------ 4-bit cache */
+
+/* A cached row of the 4-bit pool (one token, one KV head, K or V) is
+ * QSA_KV4_ROW_BYTES = 80 bytes for 128 values:
+ *   bytes 0..63   codes, e2m1 (0 0.5 1 1.5 2 3 4 6, bit 3 the sign), value 2i in the low half of byte i
+ *   bytes 64..71  scales s_j, e4m3, of values 16j .. 16j + 15
+ *   bytes 72..75  row scale t, fp32
+ *   bytes 76..79  zero
+ * and stands for code * s_j * t.  Rows stand alone: a token is stored, read and moved without its neighbours.
+ * A pool row may be wider (poolRowBytes); the library touches its leading 80 bytes only. */
+#define QSA_KV4_ROW_BYTES 80
+
+/* Stores the keys and values of new tokens in a 4-bit paged pool.  Sequence b
+ * has L = contextLengths[b] cached tokens, the last n of them new, with n =
+ * newLengths[b] cut to 0..min(seqLen, L) (newLengths NULL: min(seqLen, L)).
+ * Row t < n of k and v goes to the K and V pool row (page table row 0 and 1)
+ * of token L - n + t, as
+ *   t   = the smallest power of two with amax <= 2688 t, amax the row's largest finite magnitude, in [2^-48, 2^48]
+ *   s_j = amax_j / (6 t), rounded to the nearest e4m3 (ties to even)
+ *   code = x / (s_j t), rounded to the nearest e2m1 (ties to even, larger ones saturate at 6; a code has its
+ *          value's sign even where it is 0; where s_j is 0 so are the codes)
+ * exactly: the bytes do not depend on how the call is split.  16 values with
+ * an infinity or a NaN among them get s_j = NaN and codes 0.
+ * kOut / vOut (dense, NULL for none) get the values that the rows stand for,
+ * rounded to the inputs' type (saturating), and zeros in rows t >= n, so that
+ * a prompt's own attention can see what later steps will read.  k and v are never read
+ * past row n.
+ * status (may be NULL): bit 1 (value 2): a new token's page id lies outside
+ * [0, numFlatPages), or its position behind the page table; that row is not
+ * stored (its dense outputs are).
+ * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1, token
+ * strides < numKVHeads * headDim (with more than one token) or poolRowBytes <
+ * 80; QSA_ERR_UNSUPPORTED for headDim other than 128, poolRowBytes or a token
+ * stride that is not whole 16-byte chunks, k, v, kOut, vOut or kvPool not
+ * 16-byte aligned (the int32 tensors: 4), or sizes past int32 ids (batchSize
+ * * seqLen * numKVHeads * 16, maxPagesPerSeq * 128 and numFlatPages * 128 below 2^31). */
+typedef struct {
+  const void* k;                 /* fp16 or bf16 [B, S, numKVHeads, 128], tokens kTokenStride apart       */
+  const void* v;                 /* likewise, vTokenStride                                                */
+  const int32_t* contextLengths; /* int32 [B]: cached tokens, new ones included                           */
+  const int32_t* newLengths;     /* int32 [B], or NULL                                                    */
+  void* kOut;                    /* out [B, S, numKVHeads, 128] contiguous, type of k, or NULL            */
+  void* vOut;                    /* likewise                                                              */
+  void* kvPool;                  /* in/out bytes [numFlatPages, 128, numKVHeads, poolRowBytes]            */
+  const int32_t* pageTable;      /* int32 [B, 2, maxPagesPerSeq] (row 1: V page ids)                      */
+  int32_t* status;               /* optional device error word, or NULL                                   */
+  int64_t kTokenStride;          /* elements between tokens of k (token b * S + t); heads lie together    */
+  int64_t vTokenStride;
+  int32_t batchSize;
+  int32_t seqLen;                /* S: padded rows per sequence                                           */
+  int32_t numKVHeads;
+  int32_t headDim;               /* 128                                                                   */
+  int32_t poolRowBytes;          /* >= 80, multiple of 16                                                 */
+  int32_t numFlatPages;
+  int32_t maxPagesPerSeq;
+  void* stream;
+} QsaStoreKv4Params;
+
+QSA_API qsa_status_t qsa_store_kv4(const QsaStoreKv4Params* params);
+QSA_API qsa_status_t qsa_store_kv4_bf16(const QsaStoreKv4Params* params);
+
+/* Sparse GQA attention over a 4-bit paged cache: what qsa_sparse_paged_kv8
+ * computes, with the same lists, lengths, page table, padding, status bits
+ * and refusals, over the rows of qsa_store_kv4.  k and v are the values that
+ * the rows stand for; a row scale outside [2^-48, 2^48] is read as the nearer
+ * bound (NaN as the lower), a NaN group scale makes what uses it NaN.
+ * lse (fp32 [B, S, numQHeads], may be NULL): log sum_j exp(attentionScale * q
+ * . k_j) over the row's list, -infinity for rows t >= n and rows whose list
+ * names nothing: what qsa_sparse_weights_kv4 takes.
+ * Arithmetic: code * s_j enters the products exactly (fp16), the rest as in
+ * qsa_sparse_paged_kv8; lse sums the unrounded probabilities in fp32.  Repeated
+ * calls give identical bits.  No workspace; calls may run concurrently. */
+typedef struct {
+  const void* qPtr;              /* fp16 or bf16 [B, S, numQHeads, 128]                                   */
+  const void* kvPool;            /* bytes [numFlatPages, 128, numKVHeads, poolRowBytes]                   */
+  const int32_t* pageTable;      /* int32 [B, 2, maxPagesPerSeq] (row 1: V page ids)                      */
+  const int32_t* indices;        /* int32 [B, S, topK]; -1 names nothing                                  */
+  const int32_t* contextLengths; /* int32 [B]: cached tokens                                              */
+  const int32_t* newLengths;     /* int32 [B]: query rows, or NULL                                        */
+  void* oPtr;                    /* out [B, S, numQHeads, 128], type of q                                 */
+  float* lse;                    /* out fp32 [B, S, numQHeads], or NULL                                   */
+  int32_t* status;               /* optional device error word, or NULL                                   */
+  int32_t batchSize;
+  int32_t seqLen;                /* S: padded rows per sequence                                           */
+  int32_t numQHeads;
+  int32_t numKVHeads;            /* numQHeads / numKVHeads must be 1..16                                  */
+  int32_t headDim;               /* 128                                                                   */
+  int32_t poolRowBytes;          /* >= 80, multiple of 16                                                 */
+  int32_t numFlatPages;
+  int32_t maxPagesPerSeq;
+  int32_t topK;
+  float attentionScale;
+  void* stream;
+} QsaSparsePagedKv4Params;
+
+QSA_API qsa_status_t qsa_sparse_paged_kv4(const QsaSparsePagedKv4Params* params);
+QSA_API qsa_status_t qsa_sparse_paged_kv4_bf16(const QsaSparsePagedKv4Params* params);
+
+/* The attention weights behind a call of qsa_sparse_paged_kv4, and what every
+ * cached token has gathered of them: for row t < n, list entry e that names
+ * token j, and KV head g (query heads h of its group)
+ *   weights[b,t,g,e] = sum_h exp(attentionScale * q[b,t,h] . k[j,g] - lse[b,t,h])
+ *   total[b,g,j]    += the sum of weights[b,t,g,e] over the rows t and entries e that name j
+ * weights is 0 for entries that name nothing and in rows t >= n; a head whose lse is
+ * -infinity adds nothing.  lse, lists and lengths are those of the attention
+ * call.  A token at or past totalLen is not counted (its weights are written).
+ * total is read and written once per token that the call names; repeated
+ * calls on equal inputs give identical bits (a token's sum is formed in the
+ * order of the rows).  Calls that share `total` must not run concurrently.
+ * Arithmetic: products as in qsa_sparse_paged_kv4, fp32 exponentials and sums.
+ * status, errors and limits as for qsa_sparse_paged_kv4; total NULL with
+ * totalLen 0 counts nothing.  batchSize * numKVHeads is at most 65535. */
+typedef struct {
+  const void* qPtr;              /* fp16 or bf16 [B, S, numQHeads, 128]                                   */
+  const void* kvPool;            /* bytes [numFlatPages, 128, numKVHeads, poolRowBytes]                   */
+  const int32_t* pageTable;      /* int32 [B, 2, maxPagesPerSeq]                                          */
+  const int32_t* indices;        /* int32 [B, S, topK]; -1 names nothing                                  */
+  const int32_t* contextLengths; /* int32 [B]: cached tokens                                              */
+  const int32_t* newLengths;     /* int32 [B]: query rows, or NULL                                        */
+  const float* lse;              /* fp32 [B, S, numQHeads]                                                */
+  float* weights;                /* out fp32 [B, S, numKVHeads, topK]                                     */
+  float* total;                  /* in/out fp32 [B, numKVHeads, totalLen], or NULL                        */
+  int32_t* status;               /* optional device error word, or NULL                                   */
+  int32_t batchSize;
+  int32_t seqLen;
+  int32_t numQHeads;
+  int32_t numKVHeads;            /* numQHeads / numKVHeads must be 1..16                                  */
+  int32_t headDim;               /* 128                                                                   */
+  int32_t poolRowBytes;
+  int32_t numFlatPages;
+  int32_t maxPagesPerSeq;
+  int32_t topK;
+  int32_t totalLen;
+  float attentionScale;
+  void* stream;
+} QsaSparseWeightsKv4Params;
+
+QSA_API qsa_status_t qsa_sparse_weights_kv4(const QsaSparseWeightsKv4Params* params);
+QSA_API qsa_status_t qsa_sparse_weights_kv4_bf16(const QsaSparseWeightsKv4Params* params);
+
+/* Eviction from a 4-bit paged cache by accumulated attention weight.  Of the
+ * L = contextLengths[b] tokens of sequence b (cut to 128 * maxPagesPerSeq and
+ * to totalLen) every KV head keeps K = min(L, budget): with L > budget the
+ * first `sinks`, the last `recent`, and of the others the budget - sinks -
+ * recent with the largest total[b,g,j] (equal ones: the lowest j; NaN counts
+ * as lowest of all).  The kept tokens' K and V rows move, in order, to the
+ * sequence's first K slots, in place; heads choose for themselves, so that a
+ * slot may hold different tokens for different heads.  Outputs:
+ *   kept[b,g,i]     the token now in slot i, -1 for i >= K
+ *   keptLengths[b]  K, the sequence's new length
+ *   totalOut[b,g,i] total[b,g,kept[i]], 0 for i >= K (may be total itself, or NULL)
+ * Pool rows of slots K .. L - 1 are left as they were (some have moved up);
+ * no other byte of the pool is written.  New tokens go to slot K on
+ * (qsa_store_kv4 with the new lengths), rotated at their own positions
+ * (qsa_rotary), and lists name slots.  Sequences that share pages, the
+ * indexer's state in such a pool, and calls that share a pool concurrently
+ * are the caller's to keep apart.
+ * status (may be NULL): bit 1 (value 2): a page id of a moving row lies
+ * outside [0, numFlatPages); that row does not move.
+ * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1, sinks or
+ * recent < 0 or sinks + recent > budget, poolRowBytes < 80, keptLengths equal to
+ * contextLengths; QSA_ERR_UNSUPPORTED for headDim other than 128, poolRowBytes
+ * not a multiple of 16, kvPool not 16-byte aligned (the others 4), or sizes past int32 ids (batchSize *
+ * numKVHeads * 16, maxPagesPerSeq * 128, numFlatPages * 128 below 2^31, totalLen and budget at most 2^24).
+ * Nothing is allocated and no workspace is used. */
+typedef struct {
+  void* kvPool;                  /* in/out bytes [numFlatPages, 128, numKVHeads, poolRowBytes]            */
+  const int32_t* pageTable;      /* int32 [B, 2, maxPagesPerSeq]                                          */
+  const int32_t* contextLengths; /* int32 [B]                                                             */
+  const float* total;            /* fp32 [B, numKVHeads, totalLen]                                        */
+  int32_t* kept;                 /* out int32 [B, numKVHeads, budget]                                     */
+  int32_t* keptLengths;          /* out int32 [B]                                                         */
+  float* totalOut;               /* out fp32 [B, numKVHeads, totalLen], or NULL                           */
+  int32_t* status;               /* optional device error word, or NULL                                   */
+  int32_t batchSize;
+  int32_t numKVHeads;
+  int32_t headDim;               /* 128                                                                   */
+  int32_t poolRowBytes;
+  int32_t numFlatPages;
+  int32_t maxPagesPerSeq;
+  int32_t totalLen;
+  int32_t budget;                /* tokens kept per sequence and head                                     */
+  int32_t sinks;                 /* first tokens that are always kept                                     */
+  int32_t recent;                /* last tokens that are always kept                                      */
+  void* stream;
+} QsaEvictKv4Params;
+
+QSA_API qsa_status_t qsa_evict_kv4(const QsaEvictKv4Params* params);
+
 /* Workspace bytes of the indexers (0 when the sizes are invalid). */
 QSA_API size_t qsa_indexer_prefill_workspace_size(int32_t batchSize, int32_t seqLen, int32_t headDim,
                                           int32_t compressRatio);
