@@ -89,11 +89,11 @@ __device__ __forceinline__ void values32(Acc<NT>& A, uint32_t codes, uint32_t gr
       const uint4 sc = lds16(groups + (4 * (2 * m + c) + (lane & 3)) * 16);
 #pragma unroll
       for (int gk = 0; gk < 2; ++gk) {
-        const uint32_t x = r[2 * gk + c], y = x >> 4, z = x >> 8;
+        const uint32_t x = r[2 * gk + c], y = x << 4, z = x << 8;
         constexpr uint32_t kLow = 0x0f0f0f0f;
         uint32_t a[4];
-        e2m1_to_f16_02((x & kLow) | (y & ~kLow), a[0], a[2]);  // bytes 0 and 2: the low codes of keys 0, 1 and 2, 3
-        e2m1_to_f16_02((y & kLow) | (z & ~kLow), a[1], a[3]);  // the high ones
+        e2m1_to_f16_13((z & kLow) | (y & ~kLow), a[0], a[2]);  // bytes 1 and 3: the low codes of keys 0, 1 and 2, 3
+        e2m1_to_f16_13((y & kLow) | (x & ~kLow), a[1], a[3]);  // the high ones
         const uint32_t s0 = gk ? sc.z : sc.x, s1 = gk ? sc.w : sc.y;
         a[0] = hmul2(a[0], s0);
         a[1] = hmul2(a[1], s0);

@@ -117,7 +117,7 @@ struct Acc {
 // Online softmax of a step: s becomes the weights relative to the running maximum, returned in fp16 as the B
 // fragments of the second product.  The maximum moves only when a weight would pass 2^kHeadroom (the weights
 // are relative numbers: nothing is lost by their being up to 256 instead of 1), so that O is hardly ever
-// rescaled after a warp's first step.  The sums use the weights as the second product does, rounded to 11 bits: where
+// rescaled after a warp's first step, and a step's maximum over the lanes is formed only then.  The sums use the weights as the second product does, rounded to 11 bits: where
 // few keys decide, a rounding that only one of the two had would show in an fp16 output (up to 2^-11 of it, as much as
 // its half step).  The maximum starts at the lowest finite number, so that an entry that names nothing
 // (-inf) weighs 0 even before the first that does.  entries[i], of key i: x = K scale * attentionScale * log2(e),
@@ -152,8 +152,6 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       mx[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx[nt][h] = fmaxf(mx[nt][h], __shfl_xor_sync(kFull, mx[nt][h], o));
       move |= mx[nt][h] > A.m[nt][h] + kHeadroom;
     }
   }
@@ -163,6 +161,7 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
       float al[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        for (int o = 4; o < 32; o <<= 1) mx[nt][h] = fmaxf(mx[nt][h], __shfl_xor_sync(kFull, mx[nt][h], o));
         const float mn = fmaxf(A.m[nt][h], mx[nt][h]);
         al[h] = ex2_ftz(A.m[nt][h] - mn);
         A.m[nt][h] = mn;
