@@ -43,6 +43,7 @@ constexpr int kGroupsAt = 2 * kSetBytes;
 constexpr int kEntriesAt = kGroupsAt + kKv4ScaleBytes;
 constexpr int kRowsAt = kEntriesAt + kStep * 16;
 constexpr int kWarpBytes = kRowsAt + 2 * 2 * kStep * 4;
+// (behind the warps' tiles: the pair's queries)
 
 // What the softmax needs of an entry (see softmax32), from the scale chunks' row scales.
 __device__ __forceinline__ float4 entry_of(const PagedArgs& a, bool ok, uint32_t kscale, uint32_t vscale) {
@@ -113,8 +114,10 @@ template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
 // The tiles, and later the merge buffers: the warps' O, m, l and lse sums, then the CTA's.
 template <int NT>
-constexpr int kSmem = kWarps * kWarpBytes > (kWarps + 1) * 8 * NT * (kPad + 3) * 4 ? kWarps * kWarpBytes
-                                                                               : (kWarps + 1) * 8 * NT * (kPad + 3) * 4;
+constexpr int kTilesBytes = kWarps * kWarpBytes + kKv4QueryBytes<NT>;
+template <int NT>
+constexpr int kSmem = kTilesBytes<NT> > (kWarps + 1) * 8 * NT * (kPad + 3) * 4 ? kTilesBytes<NT>
+                                                                           : (kWarps + 1) * 8 * NT * (kPad + 3) * 4;
 
 // Where a lane's copies go in a tile set at `set`.
 struct SetDst {
@@ -237,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
   gather_values(0, cur);
   slot += hop;
   int j3 = list.at(slot);
-  uint32_t qf[NT][8][2];
-  float qs[NT][2];
-  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, qf, qs);
+  const uint32_t queries = smem_addr(smem + kWarps * kWarpBytes);
+  float qs[NT][2];  // (every warp writes the same queries)
+  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, queries, qs);
   unsigned next = resolve(p1, 1);
   p1 = list.pages_of(j2);
   __syncwarp();
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
       __syncwarp();
       entries[lane] = entry_of(a, cur >> lane & 1, at + kKScaleAt, at + kVScaleAt);
       transpose_scales(at + kVScaleAt, groups);
-      kv4_scores<NT>(s, at, at + kKScaleAt, qf);
+      kv4_scores<NT>(s, at, at + kKScaleAt, queries);
       __syncwarp();  // every lane is done with the K rows and both scales
       gather_keys(par, then);
       softmax32<NT, kBf16, kLse>(A, s, qs, entries, pb, ls);
@@ -344,9 +347,11 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
 // barrier of its own and leaves when it is done.
 constexpr int kRowsGroupsAt = kSetBytes;
 constexpr int kRowsEntriesAt = kRowsGroupsAt + kKv4ScaleBytes;
-constexpr int kRowsWarp = kRowsEntriesAt + kStep * 16;
+constexpr int kRowsQueriesAt = kRowsEntriesAt + kStep * 16;
 template <int NT>
-constexpr int kWarpTiles = kRowsWarp > 8 * NT * (kPad + 3) * 4 ? kRowsWarp : 8 * NT * (kPad + 3) * 4;  // later: O, m, l, lse
+constexpr int kRowsWarp = kRowsQueriesAt + kKv4QueryBytes<NT>;
+template <int NT>
+constexpr int kWarpTiles = kRowsWarp<NT> > 8 * NT * (kPad + 3) * 4 ? kRowsWarp<NT> : 8 * NT * (kPad + 3) * 4;  // later: O, m, l, lse
 template <int NT>
 constexpr int kIdsAt = kWarps * kWarpTiles<NT>;                    // [chunk % 3][warp's step][K, V][kStep] row ids
 template <int NT>
@@ -402,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
   float ls[NT][2] = {};
   put_rows(list.pages_of(j0), 0);
   Pages p1 = list.pages_of(j1);
-  uint32_t qf[NT][8][2];
+  const uint32_t queries = set + kRowsQueriesAt;
   float qs[NT][2];
-  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + (warp - w0) * a.G) * (kD / 8), a.G, qf, qs);
+  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + (warp - w0) * a.G) * (kD / 8), a.G, queries, qs);
   group_sync();
   unsigned mask = masks[0];  // of the current step, whose rows are gathered
   gather_k(ids_of(0, 0), mask, dst, 0, base, rowBytes);
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
         __syncwarp();
         entries[lane] = entry_of(a, mask >> lane & 1, set + kKScaleAt, set + kVScaleAt);
         transpose_scales(set + kVScaleAt, groups);
-        kv4_scores<NT>(s, set, set + kKScaleAt, qf);
+        kv4_scores<NT>(s, set, set + kKScaleAt, queries);
         __syncwarp();  // every lane is done with the K rows and both scales
         gather_k(nids, next, dst, 0, base, rowBytes);
         softmax32<NT, kBf16, kLse>(A, s, qs, entries, pb, ls);

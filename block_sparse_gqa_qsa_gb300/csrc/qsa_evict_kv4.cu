@@ -4,17 +4,20 @@
 // totals, `budget` in all; their rows move up, in order, in place.
 //
 // A cluster of CTAs takes one (sequence, head).
-// Selection: totals as 32-bit keys of the same order; three passes of digit
-// counts (11, 11, 10 bits), each CTA over its run of the tokens, joined in the
-// first CTA's shared memory, give the key of the last token kept and how many
-// of the tokens equal to it are; a pass in token order writes the list of kept
-// tokens.
+// Selection: totals become 32-bit keys of the same order, kept in shared memory
+// where a CTA's run of the tokens fits; three passes of digit counts (11, 11, 10
+// bits) give the key of the last token kept and how many of the tokens equal to
+// it are; a pass in token order writes the list of kept tokens.  A pass's counts
+// are summed over the cluster by every CTA for itself, 256 sums of eight digits
+// first, then the eight digits of the one that matters: reading all 2048 of 12
+// CTAs took 4 to 6 us a pass, adding them up in one CTA 7.
 // Moves: kept token i goes to slot i <= its own, so rows move in rounds of the
 // cluster: while a round's rows are read into shared memory, nothing that lies
 // behind the round's slots is written, and one cluster barrier per round, after
-// its reads and before its writes, is all the order that moving in place needs;
-// the next round's reads are on their way across it.  HBM bounds large calls
-// (every moved row is read and written once), the chain of passes small ones.
+// its reads and before its writes, is all the order that moving in place needs.
+// Two more rounds' rows are on their way across it, and the lists and pages of
+// two more behind those.  HBM bounds large calls (every moved row is read and
+// written once), the chain of passes small ones.
 #include <algorithm>
 #include <atomic>
 
@@ -27,9 +30,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kRows = 256;  // of a CTA's round: thread i of the lower half looks up K row i, of the upper half V row i
+constexpr int kBins = 2048;  // digits of 11 bits
+constexpr int kCoarse = 256;  // of 8 digits each
+constexpr int kRows = kThreads;  // of a CTA's round, each looked up by a thread: K rows, then as many V rows
 constexpr int kChunks = QSA_KV4_ROW_BYTES / 16;
+constexpr int kRounds = 3;  // rounds of rows in shared memory
+constexpr int kLooked = kRounds + 1;  // rounds whose places are
+constexpr int kKeys = 16384;  // tokens of a CTA's run whose keys fit shared memory
 constexpr int kMostCluster = 16;
 
 struct EvictArgs {
@@ -48,18 +55,19 @@ struct EvictArgs {
 struct Shared {
   union {
     struct {
-      int joined[3][kBins];  // of the cluster's first CTA: digit counts of each pass over all CTAs
-      int counts[kBins];     // this CTA's
+      alignas(16) int counts[3][kBins];  // of each pass's digits in this CTA's run
+      int coarse[3][kCoarse];            // and of eight digits each
+      uint32_t keys[kKeys];
     };
-    alignas(16) uint8_t rows[2][2][kRows][QSA_KV4_ROW_BYTES];  // of two rounds, K and V
+    alignas(16) uint8_t rows[kRounds][kRows][QSA_KV4_ROW_BYTES];
   };
   int scan[kWarps];
   int found[2];          // a pass's digit, and how many tokens with it are still to be kept
   int above[kWarps], equal[kWarps];  // tokens of each warp's run above and at the last key kept
   int runs[2];           // the CTA's sums of these
-  int src[3][2][kRows];  // pool rows of a round's moves (-1: none), K and V
-  int dst[3][2][kRows];
-  float value[3][kRows];  // and their totals
+  int src[kLooked][kRows];  // pool rows of a round's moves (-1: none)
+  int dst[kLooked][kRows];
+  float value[kLooked][kRows];  // and their totals
 };
 
 // Keys in the order of the totals: whole-number order of the bits of numbers >= 0, reversed below; -0 as 0, NaN lowest.
@@ -74,11 +82,13 @@ __device__ __forceinline__ int cluster_ld_int(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ void cluster_add(uint32_t addr, int v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+// A meeting of the cluster's threads that waits for no write: what a thread has read stays read, and what the moves write
+// is not read again in this kernel.  (A releasing arrival waits for the round before's rows to be written.)
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kv4_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) evict_kv4_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = a.cluster;
@@ -105,45 +115,66 @@ __global__ void __launch_bounds__(kThreads) evict_kv4_kernel(const EvictArgs a) 
   const int from = min(hi, lo + rank * share), to = min(hi, from + share);
   uint32_t last = 0;   // key of the last token kept, as far as it is known
   uint32_t known = 0;  // its known bits
-  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.joined[0][0])[i] = 0;
-  cluster_sync_all();  // the first CTA's counts are zero
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.counts[0][0])[i] = 0;
+  const bool held = share <= kKeys;
+  if (held)
+#pragma unroll 4
+    for (int j = from + tid; j < to; j += kThreads) sh.keys[j - from] = key_of_total(total[j]);
+  auto key_at = [&](int j) { return held ? sh.keys[j - from] : key_of_total(total[j]); };
+  __syncthreads();
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? kBins / 2 : kBins;
-    for (int i = tid; i < bins; i += kThreads) sh.counts[i] = 0;
-    __syncthreads();
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    int* counts = sh.counts[pass];
+    const uint32_t mask = pass == 2 ? kBins / 2 - 1 : kBins - 1;
+#pragma unroll 4
     for (int j = from + tid; j < to; j += kThreads) {
-      const uint32_t k = key_of_total(total[j]);
-      if ((k & known) == last) atomicAdd(&sh.counts[k >> shift & (bins - 1)], 1);
+      const uint32_t k = key_at(j);
+      if ((k & known) == last) atomicAdd(counts + (k >> shift & mask), 1);
     }
     __syncthreads();
-    const uint32_t joined = cluster_addr(smem_addr(sh.joined[pass]), 0);
-    for (int i = tid; i < bins; i += kThreads)
-      if (sh.counts[i]) cluster_add(joined + 4 * i, sh.counts[i]);
+    if (tid < kCoarse) {
+      const int4 x = *reinterpret_cast<const int4*>(counts + 8 * tid), y = *reinterpret_cast<const int4*>(counts + 8 * tid + 4);
+      sh.coarse[pass][tid] = (x.x + x.y + x.z + x.w) + (y.x + y.y + y.z + y.w);
+    }
     cluster_sync_all();  // all counts of this pass are in
-    // the digit at which the counts from above reach `need`
-    const int per = bins / kThreads, top = bins - 1 - tid * per;  // this thread's digits: top, top - 1, ..
-    int c[kBins / kThreads], sum = 0;
-#pragma unroll
-    for (int k = 0; k < kBins / kThreads; ++k) {
-      c[k] = k < per ? cluster_ld_int(joined + 4 * max(top - k, 0)) : 0;
-      sum += c[k];
+    // the digit, from above, at which the counts reach `need`: thread i < 256 sums the coarse count 255 - i
+    int sum = 0;
+    if (tid < kCoarse) {
+      const uint32_t mine = smem_addr(&sh.coarse[pass][kCoarse - 1 - tid]);
+#pragma unroll 4
+      for (int c = 0; c < N; ++c) sum += cluster_ld_int(cluster_addr(mine, c));
     }
     int all;
-    int before = cta_exclusive_scan<kThreads>(sum, sh.scan, all);
-    if (before < need && need <= before + sum)
+    const int before = cta_exclusive_scan<kThreads>(sum, sh.scan, all);
+    if (before < need && need <= before + sum) {
+      sh.found[0] = kCoarse - 1 - tid;
+      sh.found[1] = need - before;
+    }
+    __syncthreads();
+    if (need > 0 && warp == 0) {  // its eight digits: lane l sums digit 7 - l / 4 over every fourth CTA
+      const int fine = 8 * sh.found[0] + 7 - (lane >> 2);
+      int n = 0;
+      for (int c = lane & 3; c < N; c += 4) n += cluster_ld_int(cluster_addr(smem_addr(counts + fine), c));
+      n += __shfl_xor_sync(kFull, n, 1);
+      n += __shfl_xor_sync(kFull, n, 2);
+      int up = 0;  // of the digits above
 #pragma unroll
-      for (int k = 0; k < kBins / kThreads; ++k) {
-        if (before < need && need <= before + c[k]) {
-          sh.found[0] = top - k;
-          sh.found[1] = need - before;
-        }
-        before += c[k];
+      for (int o = 0; o < 8; ++o) {
+        const int x = __shfl_sync(kFull, n, 4 * o);
+        up += o < (lane >> 2) ? x : 0;
       }
+      const int left = sh.found[1] - up;
+      __syncwarp();
+      if ((lane & 3) == 0 && left > 0 && left <= n) {
+        sh.found[0] = fine;
+        sh.found[1] = left;
+      }
+    }
     __syncthreads();
     if (need > 0) {  // (none to keep: no digit was found)
       last |= static_cast<uint32_t>(sh.found[0]) << shift;
-      known |= static_cast<uint32_t>(bins - 1) << shift;
+      known |= mask << shift;
       need = sh.found[1];
     }
     __syncthreads();
@@ -154,8 +185,9 @@ __global__ void __launch_bounds__(kThreads) evict_kv4_kernel(const EvictArgs a) 
   const int run = share / kWarps / 32 * 32 + (share / 32 % kWarps ? 32 : 0);  // tokens of a warp, whole rounds of 32
   const int wfrom = min(to, from + warp * run), wto = min(to, wfrom + run);
   int above = 0, equal = 0;
+#pragma unroll 4
   for (int j = wfrom + lane; j < wto; j += 32) {
-    const uint32_t k = key_of_total(total[j]);
+    const uint32_t k = key_at(j);
     above += !none && k > last;
     equal += !none && k == last;
   }
@@ -188,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) evict_kv4_kernel(const EvictArgs a) 
   }
   for (int j0 = wfrom; j0 < wto; j0 += 32) {
     const int j = j0 + lane;
-    const uint32_t k = j < wto ? key_of_total(total[j]) : 0;
+    const uint32_t k = j < wto ? key_at(j) : 0;
     const bool up = !none && j < wto && k > last, eq = !none && j < wto && k == last;
     const unsigned ups = __ballot_sync(kFull, up), eqs = __ballot_sync(kFull, eq), before = (1u << lane) - 1;
     const int eqBefore = equal + __popc(eqs & before);
@@ -201,66 +233,84 @@ __global__ void __launch_bounds__(kThreads) evict_kv4_kernel(const EvictArgs a) 
   cluster_sync_all();  // the list is written, and no CTA reads another's shared memory any more
 
   // --- moves
-  const int rounds = (K + N * kRows - 1) / (N * kRows);
+  constexpr int perRound = kRows / 2;  // tokens of a CTA's round
+  const int plane = tid / perRound;    // of this thread's row
+  const int rounds = (K + N * perRound - 1) / (N * perRound);
   const size_t tokenBytes = static_cast<size_t>(a.Hkv) * a.rowBytes;
   uint8_t* base = a.pool + static_cast<size_t>(g) * a.rowBytes;
-  const int half = tid / kRows, row = tid % kRows;
-  const int32_t* pt = a.pageTable + (static_cast<size_t>(b) * 2 + half) * a.maxPagesPerSeq;
+  const int32_t* pt = a.pageTable + (static_cast<size_t>(b) * 2 + plane) * a.maxPagesPerSeq;
   bool bad = false;
-  auto look_up = [&](int round) {
-    const int i = (round * N + rank) * kRows + row, at = round % 3;
-    int src = -1, dst = -1;
-    if (i < K) {
-      const int j = *static_cast<volatile int32_t*>(kept + i);
-      if (half == 0) sh.value[at][row] = total[j];
-      if (j != i) {
-        const int from = pt[j >> 7], to = pt[i >> 7];
-        if (static_cast<unsigned>(from) < static_cast<unsigned>(a.numFlatPages) &&
-            static_cast<unsigned>(to) < static_cast<unsigned>(a.numFlatPages)) {
-          src = from * kTokensPerPage + (j & 127);
-          dst = to * kTokensPerPage + (i & 127);
-        } else {
-          bad = true;
-        }
-      }
-    }
-    sh.src[at][half][row] = src;
-    sh.dst[at][half][row] = dst;
+  auto slot_of = [&](int round) { return (round * N + rank) * perRound + (tid & (perRound - 1)); };
+  // The steps of looking a row up, a round apart: the token of a slot; its pages and total; the pool rows, to shared memory.
+  struct Looked {
+    int token, from, to;
+    float value;
   };
+  auto token_of = [&](int round) {
+    const int i = slot_of(round);
+    return i < K ? *static_cast<volatile int32_t*>(kept + i) : -1;
+  };
+  auto pages_of = [&](int round, int j) {
+    Looked x{j, -1, -1, 0.f};
+    if (j >= 0) {
+      x.from = pt[j >> 7];
+      x.to = pt[slot_of(round) >> 7];
+      if (plane == 0 && totalOut) x.value = total[j];
+    }
+    return x;
+  };
+  auto put = [&](int round, const Looked& x) {
+    const int i = slot_of(round), at = round % kLooked;
+    const bool moves = x.token >= 0 && x.token != i;
+    const bool ok = moves && static_cast<unsigned>(x.from) < static_cast<unsigned>(a.numFlatPages) &&
+                    static_cast<unsigned>(x.to) < static_cast<unsigned>(a.numFlatPages);
+    bad |= moves && !ok;
+    sh.src[at][tid] = ok ? x.from * kTokensPerPage + (x.token & 127) : -1;
+    sh.dst[at][tid] = ok ? x.to * kTokensPerPage + (i & 127) : -1;
+    sh.value[at][tid] = x.value;
+  };
+  constexpr int kCopies = kRows * kChunks / kThreads;  // 16-byte pieces of a round per thread
   auto read_rows = [&](int round) {  // one copy group
-    const int at = round % 3, buf = round & 1;
+    const int at = round % kLooked, buf = round % kRounds;
 #pragma unroll
-    for (int k = 0; k < 2 * kRows * kChunks / kThreads; ++k) {
-      const int e = k * kThreads + tid, r = e / kChunks, c = e - r * kChunks;  // r: K rows, then V rows
-      const int src = (&sh.src[at][0][0])[r];
-      if (src >= 0) cp_async16(smem_addr(&sh.rows[buf][0][0][0]) + e * 16, base + src * tokenBytes + c * 16, true);
+    for (int k = 0; k < kCopies; ++k) {
+      const int e = k * kThreads + tid, r = e / kChunks, c = e - r * kChunks;
+      const int src = sh.src[at][r];
+      if (src >= 0) cp_async16(smem_addr(&sh.rows[buf][0][0]) + e * 16, base + src * tokenBytes + c * 16, true);
     }
     cp_async_commit();
   };
   auto write_rows = [&](int round) {
-    const int at = round % 3, buf = round & 1;
+    const int at = round % kLooked, buf = round % kRounds;
 #pragma unroll
-    for (int k = 0; k < 2 * kRows * kChunks / kThreads; ++k) {
+    for (int k = 0; k < kCopies; ++k) {
       const int e = k * kThreads + tid, r = e / kChunks, c = e - r * kChunks;
-      const int dst = (&sh.dst[at][0][0])[r];
+      const int dst = sh.dst[at][r];
       if (dst >= 0)
-        *reinterpret_cast<uint4*>(base + dst * tokenBytes + c * 16) = *reinterpret_cast<const uint4*>(&sh.rows[buf][0][0][0] + e * 16);
+        *reinterpret_cast<uint4*>(base + dst * tokenBytes + c * 16) = *reinterpret_cast<const uint4*>(&sh.rows[buf][0][0] + e * 16);
     }
-    const int i = (round * N + rank) * kRows + row;
-    if (totalOut && half == 0 && i < K) totalOut[i] = sh.value[at][row];
+    const int i = slot_of(round);
+    if (totalOut && plane == 0 && i < K) totalOut[i] = sh.value[at][tid];
   };
-  look_up(0);
+  // (a round past the last has no token)
+  constexpr int kAhead = kRounds - 1;  // rounds of rows on their way
+  int token = token_of(kAhead);
+  Looked looked;
+#pragma unroll
+  for (int round = 0; round < kAhead; ++round) put(round, pages_of(round, token_of(round)));
+  looked = pages_of(kAhead, token);
+  token = token_of(kAhead + 1);
   __syncthreads();
-  read_rows(0);
+#pragma unroll
+  for (int round = 0; round < kAhead; ++round) read_rows(round);
   for (int round = 0; round < rounds; ++round) {
-    if (round + 1 < rounds) look_up(round + 1);
-    __syncthreads();  // the next round's rows are known, and the one before this is written
-    if (round + 1 < rounds)
-      read_rows(round + 1);
-    else
-      cp_async_commit();
-    cp_async_wait<1>();
-    cluster_sync_all();  // every CTA has read this round's rows and totals
+    put(round + kAhead, looked);
+    looked = pages_of(round + kAhead + 1, token);
+    token = token_of(round + kAhead + 2);
+    __syncthreads();  // the places of round + kAhead are known, round - 1 is written
+    read_rows(round + kAhead);
+    cp_async_wait<kAhead>();
+    cluster_meet();  // every CTA has read this round's rows and totals
     write_rows(round);
   }
   if (totalOut)
@@ -289,22 +339,22 @@ cudaError_t allow() {
   return cudaFuncSetAttribute(evict_kv4_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
-// The largest cluster, up to 16, that the current device takes; asked for once per device.
-int most_cluster() {
+// Clusters of `size` CTAs that the current device holds at once (a cluster's CTAs lie in one GPC), asked for once per device.
+int resident_clusters(int size) {
   constexpr int kDevices = 16;
-  static std::atomic<int> known[kDevices];  // 0: not asked yet
+  static std::atomic<int> known[kDevices][kMostCluster + 1];  // 0: not asked yet; -1: none
   int dev = 0;
   const bool cached = cudaGetDevice(&dev) == cudaSuccess && dev < kDevices;
-  int n = cached ? known[dev].load(std::memory_order_relaxed) : 0;
+  int n = cached ? known[dev][size].load(std::memory_order_relaxed) : 0;
   if (n == 0) {
-    n = 8;
     cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = config(1, kMostCluster, nullptr, &at);
-    int fit = 0;
-    if (allow() == cudaSuccess && cudaOccupancyMaxActiveClusters(&fit, evict_kv4_kernel, &cfg) == cudaSuccess && fit > 0)
-      n = kMostCluster;
-    (void)cudaGetLastError();  // a failed query is not the launch's error: this size is just not used
-    if (cached) known[dev].store(n, std::memory_order_relaxed);
+    const cudaLaunchConfig_t cfg = config(1, size, nullptr, &at);
+    if (allow() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, evict_kv4_kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();  // a failed query is not the launch's error: this size is just not used
+      n = 0;
+    }
+    n = n < 1 ? -1 : n;
+    if (cached) known[dev][size].store(n, std::memory_order_relaxed);
   }
   return n;
 }
@@ -330,9 +380,9 @@ cudaError_t launch_evict_kv4(const QsaEvictKv4Params& p) {
   a.sinks = p.sinks;
   a.recent = p.recent;
   const long long pairs = static_cast<long long>(p.batchSize) * p.numKVHeads;
-  // As many CTAs per (sequence, head) as about fill the GPU, with at least 1024 tokens each.
-  a.cluster = most_cluster();
-  while (a.cluster > 1 && (pairs * a.cluster > 2LL * sm_count() || (a.cluster - 1) * 1024LL >= p.totalLen)) a.cluster /= 2;
+  // As many CTAs per (sequence, head) as leave all clusters resident at once, with at least 1024 tokens each.
+  a.cluster = kMostCluster;
+  while (a.cluster > 1 && ((a.cluster - 1) * 1024LL >= p.totalLen || pairs > resident_clusters(a.cluster))) --a.cluster;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = config(pairs, a.cluster, static_cast<cudaStream_t>(p.stream), &at);
   // (the attributes are the context's: set with every launch, which costs less than asking whether they are)

@@ -40,51 +40,61 @@ __device__ __forceinline__ void kv4_copy_scales(int row, uint32_t dst, const uin
   cp_async16_to<0>(dst, base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes + kKv4Codes, row >= 0);
 }
 
+// The group's queries in shared memory as the scores read them: piece (4 nt + w) * 32 + lane holds the lane's B fragments
+// of k-steps 2 w and 2 w + 1.
+template <int NT>
+constexpr int kKv4QueryBytes = NT * 4 * 32 * 16;
+
 // S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + key_of(g) and 2 on, heads 8 nt + 2 q and + 1.  A lane
 // reads a key's 16 bytes q of codes, 32 dims with two scales: k-step w covers dims 32 q + 4 w .. + 3 of every q.  (Rows of
 // 64 bytes: two of different parity lie in different banks.)
 template <int NT>
-__device__ __forceinline__ void kv4_scores(float (&s)[2][NT][4], uint32_t codes, uint32_t scales,
-                                           const uint32_t (&qf)[NT][8][2]) {
+__device__ __forceinline__ void kv4_scores(float (&s)[2][NT][4], uint32_t codes, uint32_t scales, uint32_t queries) {
   const int lane = threadIdx.x & 31, key = key_of(lane >> 2), q = lane & 3;
+  uint4 r[4];
+  uint32_t sc[4][2];  // (s, s) of a row's two groups
 #pragma unroll
-  for (int gk = 0; gk < 2; ++gk) {
+  for (int i = 0; i < 4; ++i) {
+    const int row = 16 * (i >> 1) + key + 2 * (i & 1);
+    r[i] = lds16(codes + row * kKv4Codes + q * 16);
+    uint32_t b, pair, none;
+    asm volatile("{\n .reg .b16 t;\n ld.shared.b16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n"
+                 : "=r"(b)
+                 : "r"(scales + row * kKv4Chunk + 2 * q));
+    e4m3_to_f16(b, pair, none);
+    sc[i][0] = __byte_perm(pair, 0, 0x1010);
+    sc[i][1] = __byte_perm(pair, 0, 0x3232);
+  }
+#pragma unroll
+  for (int gk = 0; gk < 2; ++gk)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) s[gk][nt][0] = s[gk][nt][1] = s[gk][nt][2] = s[gk][nt][3] = 0.f;
-    uint4 r[2];
-    uint32_t sc[2][2];  // (s, s) of a row's two groups
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 16 * gk + key + 2 * i;
-      r[i] = lds16(codes + row * kKv4Codes + q * 16);
-      uint32_t b, pair, none;
-      asm volatile("{\n .reg .b16 t;\n ld.shared.b16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n"
-                   : "=r"(b)
-                   : "r"(scales + row * kKv4Chunk + 2 * q));
-      e4m3_to_f16(b, pair, none);
-      sc[i][0] = __byte_perm(pair, 0, 0x1010);
-      sc[i][1] = __byte_perm(pair, 0, 0x3232);
-    }
+  for (int w = 0; w < 4; ++w) {
+    uint4 b[NT];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int nt = 0; nt < NT; ++nt) b[nt] = lds16(queries + ((4 * nt + w) * 32 + lane) * 16);
+#pragma unroll
+    for (int gk = 0; gk < 2; ++gk) {
       uint32_t a[2][4];  // of k-steps 2 w, 2 w + 1
-      e2m1_to_f16(word(r[0], w), a[0][0], a[0][2], a[1][0], a[1][2]);
-      e2m1_to_f16(word(r[1], w), a[0][1], a[0][3], a[1][1], a[1][3]);
+      e2m1_to_f16(word(r[2 * gk], w), a[0][0], a[0][2], a[1][0], a[1][2]);
+      e2m1_to_f16(word(r[2 * gk + 1], w), a[0][1], a[0][3], a[1][1], a[1][3]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[k][i] = hmul2(a[k][i], sc[i & 1][w >> 1]);
+        for (int i = 0; i < 4; ++i) a[k][i] = hmul2(a[k][i], sc[2 * gk + (i & 1)][w >> 1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(s[gk][nt], a[k], qf[nt][2 * w + k][0], qf[nt][2 * w + k][1]);
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[gk][nt], a[k], k ? b[nt].z : b[nt].x, k ? b[nt].w : b[nt].y);
       }
     }
   }
 }
 
-// The group's Q^T fragments: k-step w of a lane covers dims 32 q + 4 w .. + 3, as the K codes do.  bf16 values are scaled
-// by a power of two per head to fp16's upper range; qs gets its inverse for the lane's heads 2 q, 2 q + 1.
+// Puts the group's queries at `queries` (a warp's work, seen by the warp after a __syncwarp): k-step w of a lane covers dims
+// 32 q + 4 w .. + 3, as the K codes do.  bf16 values are scaled by a power of two per head to fp16's upper range; qs gets
+// its inverse for the lane's heads 2 q, 2 q + 1.
 template <int NT, bool kBf16>
-__device__ __forceinline__ void kv4_load_q(const uint4* q, int G, uint32_t (&qf)[NT][8][2], float (&qs)[NT][2]) {
+__device__ __forceinline__ void kv4_load_q(const uint4* q, int G, uint32_t queries, float (&qs)[NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -111,14 +121,17 @@ __device__ __forceinline__ void kv4_load_q(const uint4* q, int G, uint32_t (&qf)
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {  // 16 bytes i hold dims 32 c + 8 i .. + 7: k-steps 2 i and 2 i + 1, two words each
+      uint32_t v[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t v = word(raw[i], w);
-        if constexpr (kBf16) v = pack_half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
-        // 16-byte piece i holds dims 32 c + 8 i + 2 w: k-step 2 i + w / 2
-        qf[nt][2 * i + (w >> 1)][w & 1] = v;
+        v[w] = word(raw[i], w);
+        if constexpr (kBf16) v[w] = pack_half2(__uint_as_float(v[w] << 16) * up, __uint_as_float(v[w] & 0xffff0000u) * up);
       }
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(queries + ((4 * nt + i) * 32 + lane) * 16), "r"(v[0]),
+                   "r"(v[1]), "r"(v[2]), "r"(v[3])
+                   : "memory");
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(kFull, down, 4 * (2 * c + j));
   }

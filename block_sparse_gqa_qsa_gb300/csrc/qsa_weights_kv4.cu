@@ -40,7 +40,7 @@ struct WeightArgs {
 template <int NT, bool kBf16>
 __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const WeightArgs w) {
   const PagedArgs& a = w.a;
-  __shared__ __align__(128) uint8_t smem[kWarps * kWarpBytes];
+  __shared__ __align__(128) uint8_t smem[kWarps * kWarpBytes + kKv4QueryBytes<NT>];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Row r = row_of(a, static_cast<int>(blockIdx.x), 1);
   List list(a, r);
@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
   unsigned cur = gather(list.pages_of(j0), 0);
   Pages p1 = list.pages_of(j1);
   int j2 = count > 2 ? list.at(first + 2 * kStep + lane) : -1;
-  uint32_t qf[NT][8][2];
-  float qs[NT][2], l2[NT][2];
-  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, qf, qs);
+  const uint32_t queries = smem_addr(smem + kWarps * kWarpBytes);
+  float qs[NT][2], l2[NT][2];  // (every warp writes the same queries)
+  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, queries, qs);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
       float s[2][NT][4];
       cp_async_wait<1>();
       __syncwarp();
-      kv4_scores<NT>(s, tile, tile + kKv4CodeBytes, qf);
+      kv4_scores<NT>(s, tile, tile + kKv4CodeBytes, queries);
       float sum[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
