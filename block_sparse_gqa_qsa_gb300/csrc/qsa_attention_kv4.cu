@@ -20,8 +20,10 @@
 // as N.  For the second, ldmatrix transposes 16 x 16 bytes, so a register holds
 // four keys of one byte column, i.e. of two dims: its low codes are row g of an
 // MMA tile, its high codes row g + 8, and a tile's 16 dims are one scale group.
-// The V scales are transposed the same way once per step and read back as f16
-// pairs of keys.
+// Two registers, 16 keys apart, are paired key by key with two shifts and two
+// selections for 16 codes; S^T has its rows in the order that makes P's pairs the
+// same ones.  The V scales are transposed the same way once per step and read
+// back as f16 pairs of keys.
 #include <algorithm>
 #include <atomic>
 
@@ -41,18 +43,18 @@ constexpr int kSetBytes = kVScaleAt + kKv4ScaleBytes;
 // entries, the pool rows of two steps' entries (K then V).
 constexpr int kGroupsAt = 2 * kSetBytes;
 constexpr int kEntriesAt = kGroupsAt + kKv4ScaleBytes;
-constexpr int kRowsAt = kEntriesAt + kStep * 16;
+constexpr int kRowsAt = kEntriesAt + kStep * 8;
 constexpr int kWarpBytes = kRowsAt + 2 * 2 * kStep * 4;
 // (behind the warps' tiles: the pair's queries)
 
 // What the softmax needs of an entry (see softmax32), from the scale chunks' row scales.
-__device__ __forceinline__ float4 entry_of(const PagedArgs& a, bool ok, uint32_t kscale, uint32_t vscale) {
-  const int off = (threadIdx.x & 31) * kKv4Chunk + 8;
+__device__ __forceinline__ float2 entry_of(const PagedArgs& a, bool ok, uint32_t kscale, uint32_t vscale) {
+  const int lane = threadIdx.x & 31;
   float tk, tv;
-  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(tk) : "r"(kscale + off));
-  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(tv) : "r"(vscale + off));
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(tk) : "r"(kscale + kv4_k_scale(lane) * kKv4Chunk + 8));
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(tv) : "r"(vscale + lane * kKv4Chunk + 8));
   tv = read_scale(tv);
-  return ok ? make_float4(read_scale(tk) * a.sl2, lg2_ftz(tv), rcp_ftz(tv), 0.f) : make_float4(0.f, -INFINITY, 0.f, 0.f);
+  return ok ? make_float2(read_scale(tk) * a.sl2, lg2_ftz(tv)) : make_float2(0.f, -INFINITY);
 }
 
 // Two transposed 16 x 16 byte matrices (rows at the addresses of lanes 0..15 and 16..31): of each, the lane gets rows
@@ -63,14 +65,15 @@ __device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr));
 }
 
-// A step's V scales by group: piece 4 j + q of `groups` gets group j's scales of keys 4 q .. 4 q + 3 and 16 on, in f16.
+// A step's V scales by group: piece 4 j + q of `groups` gets group j's scales of keys 4 q + i and 4 q + i + 16, i = 0..3, as
+// f16 pairs.
 // (Columns 8 and on of the scale chunks, the row scales, are dropped.)
 __device__ __forceinline__ void transpose_scales(uint32_t vscale, uint32_t groups) {
   const int lane = threadIdx.x & 31;
   uint32_t r[4], p[4];
   ldsm_bytes_t(vscale + lane * kKv4Chunk, r);
-  e4m3_to_f16(r[0], p[0], p[1]);
-  e4m3_to_f16(r[2], p[2], p[3]);
+  e4m3_to_f16(__byte_perm(r[0], r[2], 0x5140), p[0], p[1]);
+  e4m3_to_f16(__byte_perm(r[0], r[2], 0x7362), p[2], p[3]);
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(groups + lane * 16), "r"(p[0]), "r"(p[1]), "r"(p[2]),
                "r"(p[3])
                : "memory");
@@ -81,25 +84,23 @@ template <int NT>
 __device__ __forceinline__ void values32(Acc<NT>& A, uint32_t codes, uint32_t groups, const uint32_t (&pb)[2][NT][2]) {
   const int lane = threadIdx.x & 31;
   const uint32_t row = codes + lane * kKv4Codes + ((lane >> 1 & 3) << 4);
+  uint32_t next[4];
+  ldsm_bytes_t(row, next);
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    uint32_t r[4];
-    ldsm_bytes_t(row ^ (m << 4), r);
+    const uint32_t r[4] = {next[0], next[1], next[2], next[3]};
+    if (m < 3) ldsm_bytes_t(row ^ ((m + 1) << 4), next);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const uint4 sc = lds16(groups + (4 * (2 * m + c) + (lane & 3)) * 16);
+      constexpr uint32_t kLow = 0x0f0f0f0f;
+      uint32_t lo[4], hi[4];  // of keys 4 q + i and 4 q + i + 16
+      e2m1_to_f16((r[c] & kLow) | (r[2 + c] << 4 & ~kLow), lo[0], lo[1], lo[2], lo[3]);
+      e2m1_to_f16((r[c] >> 4 & kLow) | (r[2 + c] & ~kLow), hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
       for (int gk = 0; gk < 2; ++gk) {
-        const uint32_t x = r[2 * gk + c], y = x << 4, z = x << 8;
-        constexpr uint32_t kLow = 0x0f0f0f0f;
-        uint32_t a[4];
-        e2m1_to_f16_13((z & kLow) | (y & ~kLow), a[0], a[2]);  // bytes 1 and 3: the low codes of keys 0, 1 and 2, 3
-        e2m1_to_f16_13((y & kLow) | (x & ~kLow), a[1], a[3]);  // the high ones
         const uint32_t s0 = gk ? sc.z : sc.x, s1 = gk ? sc.w : sc.y;
-        a[0] = hmul2(a[0], s0);
-        a[1] = hmul2(a[1], s0);
-        a[2] = hmul2(a[2], s1);
-        a[3] = hmul2(a[3], s1);
+        const uint32_t a[4] = {hmul2(lo[2 * gk], s0), hmul2(hi[2 * gk], s0), hmul2(lo[2 * gk + 1], s1), hmul2(hi[2 * gk + 1], s1)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(A.o[2 * m + c][nt], a, pb[gk][nt][0], pb[gk][nt][1]);
       }
@@ -126,7 +127,7 @@ struct SetDst {
     const int lane = threadIdx.x & 31;
     k = set + lane * 16;
     v = set + kVAt + (lane >> 2) * kKv4Codes + (((lane & 3) ^ (lane >> 3)) << 4);  // chunk c of row r at c ^ (r / 2 % 4)
-    ks = set + kKScaleAt + lane * kKv4Chunk;
+    ks = set + kKScaleAt + kv4_k_scale(lane) * kKv4Chunk;
     vs = set + kVScaleAt + lane * kKv4Chunk;
   }
 };
@@ -135,7 +136,7 @@ __device__ __forceinline__ void gather_k(const int* ids, unsigned mask, const Se
                                          uint32_t rowBytes) {
   if (mask) {
     const int lane = threadIdx.x & 31, at = kv4_row_place(lane);
-    kv4_copy_codes(ids, mask, dst.k + off, base + (lane & 3) * 16, rowBytes);
+    kv4_copy_codes<true>(ids, mask, dst.k + off, base + (lane & 3) * 16, rowBytes);
     kv4_copy_scales(ids[at], dst.ks + off, base, rowBytes);
     kv4_copy_scales(ids[kStep + at], dst.vs + off, base, rowBytes);
   }
@@ -143,7 +144,7 @@ __device__ __forceinline__ void gather_k(const int* ids, unsigned mask, const Se
 }
 __device__ __forceinline__ void gather_v(const int* ids, unsigned mask, const SetDst& dst, uint32_t off, const uint8_t* base,
                                          uint32_t rowBytes) {
-  if (mask) kv4_copy_codes(ids + kStep, mask, dst.v + off, base + (threadIdx.x & 3) * 16, rowBytes);
+  if (mask) kv4_copy_codes<false>(ids + kStep, mask, dst.v + off, base + (threadIdx.x & 3) * 16, rowBytes);
   cp_async_commit();
 }
 
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
   }
   uint8_t* mine = smem + warp * kWarpBytes;
   const uint32_t set = smem_addr(mine), groups = set + kGroupsAt;
-  float4* entries = reinterpret_cast<float4*>(mine + kEntriesAt);
+  float2* entries = reinterpret_cast<float2*>(mine + kEntriesAt);
   int* ids = reinterpret_cast<int*>(mine + kRowsAt);  // [step & 1][K, V][kv4_row_place]
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
   const uint8_t* base = a.pool + static_cast<size_t>(r.kvh) * a.poolHeadDim;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
       kv4_scores<NT>(s, at, at + kKScaleAt, queries);
       __syncwarp();  // every lane is done with the K rows and both scales
       gather_keys(par, then);
-      softmax32<NT, kBf16, kLse>(A, s, qs, entries, pb, ls);
+      softmax32<NT, kBf16, kLse>(A, s, qs, entries + kv4_first_key(lane), pb, ls);
       cp_async_wait<3>();  // the V codes
       __syncwarp();
       values32<NT>(A, at + kVAt, groups, pb);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
 // barrier of its own and leaves when it is done.
 constexpr int kRowsGroupsAt = kSetBytes;
 constexpr int kRowsEntriesAt = kRowsGroupsAt + kKv4ScaleBytes;
-constexpr int kRowsQueriesAt = kRowsEntriesAt + kStep * 16;
+constexpr int kRowsQueriesAt = kRowsEntriesAt + kStep * 8;
 template <int NT>
 constexpr int kRowsWarp = kRowsQueriesAt + kKv4QueryBytes<NT>;
 template <int NT>
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
   }
   uint8_t* mine = smem + warp * kWarpTiles<NT>;
   const uint32_t set = smem_addr(mine), groups = set + kRowsGroupsAt;
-  float4* entries = reinterpret_cast<float4*>(mine + kRowsEntriesAt);
+  float2* entries = reinterpret_cast<float2*>(mine + kRowsEntriesAt);
   int* ids = reinterpret_cast<int*>(smem + kIdsAt<NT>) + w0 * 2 * kStep;
   unsigned* masks = reinterpret_cast<unsigned*>(smem + kMasksAt<NT>) + w0;
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
         kv4_scores<NT>(s, set, set + kKScaleAt, queries);
         __syncwarp();  // every lane is done with the K rows and both scales
         gather_k(nids, next, dst, 0, base, rowBytes);
-        softmax32<NT, kBf16, kLse>(A, s, qs, entries, pb, ls);
+        softmax32<NT, kBf16, kLse>(A, s, qs, entries + kv4_first_key(lane), pb, ls);
         cp_async_wait<1>();  // the V codes; the next K rows may be in flight
         __syncwarp();
         values32<NT>(A, set + kVAt, groups, pb);

@@ -19,12 +19,6 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t& p0, uint32_t& 
       : "=r"(p0), "=r"(p1), "=r"(p2), "=r"(p3)
       : "r"(w));
 }
-// Bytes 1 and 3 alone.
-__device__ __forceinline__ void e2m1_to_f16_13(uint32_t w, uint32_t& p1, uint32_t& p3) {
-  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %2;\n cvt.rn.f16x2.e2m1x2 %0, b;\n cvt.rn.f16x2.e2m1x2 %1, d;\n}\n"
-      : "=r"(p1), "=r"(p3)
-      : "r"(w));
-}
 // Eight fp32 values as e2m1 codes (value i in nibble i), to nearest even, saturating at 6.
 __device__ __forceinline__ uint32_t f32_to_e2m1(const float (&x)[8]) {
   uint32_t w;

@@ -121,21 +121,35 @@ struct Acc {
 // few keys decide, a rounding that only one of the two had would show in an fp16 output (up to 2^-11 of it, as much as
 // its half step).  The maximum starts at the lowest finite number, so that an entry that names nothing
 // (-inf) weighs 0 even before the first that does.  entries[i], of key i: x = K scale * attentionScale * log2(e),
-// y = log2(V scale), z = 1 / V scale; (0, -inf, 0) for an entry that names nothing.
+// y = log2(V scale), z = 1 / V scale; (0, -inf, 0) for an entry that names nothing.  (Entries of two values, 4-bit pool:
+// those of the lane's four keys lie together at `entries`; z = 2^-y, kept finite where it meets a weight of 0.)
 // kLse: ls gathers the sums of the weights as they are before the rounding.
-template <int NT, bool kBf16, bool kLse = false>
+template <int NT, bool kBf16, bool kLse = false, typename Entry>
 __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], const float (&qs)[NT][2],
-                                          const float4* entries, uint32_t (&pb)[2][NT][2],
+                                          const Entry* entries, uint32_t (&pb)[2][NT][2],
                                           float (*ls)[2] = nullptr) {
   constexpr float kHeadroom = 8.f;
-  const int key = key_of((threadIdx.x & 31) >> 2);
   float ks[4], lv[4], iv[4];  // of the lane's keys
+  if constexpr (sizeof(Entry) == sizeof(float4)) {
+    const int key = key_of((threadIdx.x & 31) >> 2);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 e = entries[key + 16 * (i >> 1) + 2 * (i & 1)];
-    ks[i] = e.x;
-    lv[i] = e.y;
-    iv[i] = e.z;
+    for (int i = 0; i < 4; ++i) {
+      const Entry e = entries[key + 16 * (i >> 1) + 2 * (i & 1)];
+      ks[i] = e.x;
+      lv[i] = e.y;
+      iv[i] = e.z;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 e = reinterpret_cast<const float4*>(entries)[i];
+      ks[2 * i] = e.x;
+      lv[2 * i] = e.y;
+      ks[2 * i + 1] = e.z;
+      lv[2 * i + 1] = e.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) iv[i] = fminf(ex2_ftz(-lv[i]), 0x1p126f);
   }
   float mx[NT][2];
   bool move = false;

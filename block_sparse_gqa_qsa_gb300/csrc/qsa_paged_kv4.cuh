@@ -15,29 +15,42 @@ namespace qsa {
 constexpr int kKv4CodeBytes = kStep * kKv4Codes;   // codes of a step's K (or V) rows
 constexpr int kKv4ScaleBytes = kStep * kKv4Chunk;  // their scale chunks
 
+// First of the four keys of a step (i = 0..3 behind it) that are rows of a lane's S^T fragments: key i is row g of tile i
+// (g = lane >> 2; tile 2 gk is rows 0..7, tile 2 gk + 1 rows 8..15 of MMA gk).  Rows 2 q and 2 q + 1 of a tile, which the
+// transposed fragment of P holds as a pair, are keys 16 apart: what the V codes of two registers pair at once.
+__device__ __forceinline__ int kv4_first_key(int lane) { return 4 * (lane >> 3) + 16 * (lane >> 2 & 1); }
+// Place of row r of a step's K codes (rows 16 apart lie in different banks) and of its K scale chunk (so do rows 4 apart).
+__device__ __forceinline__ int kv4_k_row(int r) { return r ^ (r >> 4); }
+__device__ __forceinline__ int kv4_k_scale(int r) { return (r & 3) * 8 + (r >> 2); }
+
 // Place of a step's entry i among its 32 row ids: a lane gathers rows 8 i + (lane >> 2), which lie together.
 __device__ __forceinline__ int kv4_row_place(int i) { return (i & 7) * 4 + (i >> 3); }
 
-// A lane's shares of a gather: 16 bytes of the codes of rows 8 i + (lane >> 2), i = 0..3, to dst + 512 i, and its own
-// row's scale chunk.  Rows that no entry names (id -1) become zeros.
+// A lane's shares of a gather: 16 bytes of the codes of rows 8 i + (lane >> 2), i = 0..3, to dst + 512 i (K codes: dst ^ 64
+// from row 16 on, see kv4_k_row), and its own row's scale chunk.  Rows that no entry names (id -1) become zeros.  (The path of steps that name fewer than 32 rows is a
+// loop, so that the compiler branches: as predicated instructions it took a twentieth of the attention's issue slots.)
+template <bool kKeys>
 __device__ __forceinline__ void kv4_copy_codes(const int* ids, unsigned mask, uint32_t dst, const uint8_t* base,
                                                uint32_t rowBytes) {
-  const int4 r = *reinterpret_cast<const int4*>(ids + ((threadIdx.x & 31) >> 2) * 4);
-  auto src = [&](int row) { return base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes; };
+  ids += ((threadIdx.x & 31) >> 2) * 4;
   if (mask == kFull) {
+    const int4 r = *reinterpret_cast<const int4*>(ids);
+    auto src = [&](int row) { return base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * rowBytes; };
     cp_async16_to<0>(dst, src(r.x));
     cp_async16_to<512>(dst, src(r.y));
-    cp_async16_to<1024>(dst, src(r.z));
-    cp_async16_to<1536>(dst, src(r.w));
+    const uint32_t upper = kKeys ? dst ^ 64 : dst;
+    cp_async16_to<1024>(upper, src(r.z));
+    cp_async16_to<1536>(upper, src(r.w));
   } else {
-    cp_async16_to<0>(dst, src(r.x), r.x >= 0);
-    cp_async16_to<512>(dst, src(r.y), r.y >= 0);
-    cp_async16_to<1024>(dst, src(r.z), r.z >= 0);
-    cp_async16_to<1536>(dst, src(r.w), r.w >= 0);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int row = ids[i];
+      cp_async16((kKeys && i > 1 ? dst ^ 64 : dst) + 512 * i, base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes, row >= 0);
+    }
   }
 }
 __device__ __forceinline__ void kv4_copy_scales(int row, uint32_t dst, const uint8_t* base, uint32_t rowBytes) {
-  cp_async16_to<0>(dst, base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes + kKv4Codes, row >= 0);
+  cp_async16(dst, base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * rowBytes + kKv4Codes, row >= 0);
 }
 
 // The group's queries in shared memory as the scores read them: piece (4 nt + w) * 32 + lane holds the lane's B fragments
@@ -45,22 +58,20 @@ __device__ __forceinline__ void kv4_copy_scales(int row, uint32_t dst, const uin
 template <int NT>
 constexpr int kKv4QueryBytes = NT * 4 * 32 * 16;
 
-// S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys 16 gk + key_of(g) and 2 on, heads 8 nt + 2 q and + 1.  A lane
-// reads a key's 16 bytes q of codes, 32 dims with two scales: k-step w covers dims 32 q + 4 w .. + 3 of every q.  (Rows of
-// 64 bytes: two of different parity lie in different banks.)
+// S^T = C^K Q^T of a step's 32 keys: s[gk][nt] holds keys kv4_first_key + 2 gk and + 2 gk + 1, heads 8 nt + 2 q and + 1.
+// A lane reads a key's 16 bytes q of codes, 32 dims with two scales: k-step w covers dims 32 q + 4 w .. + 3 of every q.
 template <int NT>
 __device__ __forceinline__ void kv4_scores(float (&s)[2][NT][4], uint32_t codes, uint32_t scales, uint32_t queries) {
-  const int lane = threadIdx.x & 31, key = key_of(lane >> 2), q = lane & 3;
+  const int lane = threadIdx.x & 31, key = kv4_first_key(lane), q = lane & 3;
   uint4 r[4];
   uint32_t sc[4][2];  // (s, s) of a row's two groups
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = 16 * (i >> 1) + key + 2 * (i & 1);
-    r[i] = lds16(codes + row * kKv4Codes + q * 16);
+    r[i] = lds16(codes + kv4_k_row(key + i) * kKv4Codes + q * 16);
     uint32_t b, pair, none;
     asm volatile("{\n .reg .b16 t;\n ld.shared.b16 t, [%1];\n cvt.u32.u16 %0, t;\n}\n"
                  : "=r"(b)
-                 : "r"(scales + row * kKv4Chunk + 2 * q));
+                 : "r"(scales + kv4_k_scale(key + i) * kKv4Chunk + 2 * q));
     e4m3_to_f16(b, pair, none);
     sc[i][0] = __byte_perm(pair, 0, 0x1010);
     sc[i][1] = __byte_perm(pair, 0, 0x3232);

@@ -68,8 +68,8 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
     __syncwarp();
     if (mask) {
       const uint32_t tile = tiles + par * kTileBytes;
-      kv4_copy_codes(at, mask, tile + lane * 16, base + (lane & 3) * 16, rowBytes);
-      kv4_copy_scales(rows.ok ? rows.k : -1, tile + kKv4CodeBytes + lane * kKv4Chunk, base, rowBytes);
+      kv4_copy_codes<true>(at, mask, tile + lane * 16, base + (lane & 3) * 16, rowBytes);
+      kv4_copy_scales(rows.ok ? rows.k : -1, tile + kKv4CodeBytes + kv4_k_scale(lane) * kKv4Chunk, base, rowBytes);
     }
     cp_async_commit();
     return mask;
@@ -88,8 +88,7 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
       const float l = h < a.G ? __ldg(w.lse + r.head0 + h) : INFINITY;
       l2[nt][j] = l == -INFINITY ? INFINITY : l * kLog2e;
     }
-  const int g = lane >> 2, q = lane & 3;
-  const int mine = 16 * (q >> 1) + key_of(g) + 2 * (q & 1);  // the entry whose sum this lane keeps
+  const int q = lane & 3, key = kv4_first_key(lane), mine = key + q;  // the entry whose sum this lane keeps
   for (int i = 0; i < count; ++i) {
     const int par = i & 1;
     const unsigned next = gather(p1, par ^ 1);
@@ -107,9 +106,8 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
       float sum[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = 16 * (k >> 1) + key_of(g) + 2 * (k & 1);
         float tk;
-        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(tk) : "r"(tile + kKv4CodeBytes + row * kKv4Chunk + 8));
+        asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(tk) : "r"(tile + kKv4CodeBytes + kv4_k_scale(key + k) * kKv4Chunk + 8));
         const float ks = read_scale(tk) * a.sl2;
         sum[k] = 0.f;
 #pragma unroll
