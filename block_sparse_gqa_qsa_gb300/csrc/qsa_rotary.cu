@@ -28,7 +28,8 @@ struct RotaryArgs {
   const int32_t* positions;
   long long xToken, xHead, yToken, yHead;  // elements
   int heads, rot;
-  int rotVectors, vectors;  // per head: vectors (or pairs of vectors) that turn, all that a call touches
+  int rotVectors, vectors;  // per head: vectors (or pairs of vectors) that turn, and with those that are copied
+  int copyBytes;            // of a vector that is copied: 16, or V elements
   int headGroups;           // threads that share a (token, vector): thread g takes heads g, g + headGroups, ..
   unsigned units;           // tokens * headGroups * vectors
   float magnitude;
@@ -48,6 +49,20 @@ struct __align__(sizeof(T) * V) Vec {
   T v[V];
 };
 
+// Vector `at` of the heads g, g + groups, .. from x to y.
+template <typename W, typename T>
+__device__ __forceinline__ void copy_heads(const T* x, T* y, int at, long long xHop, long long yHop, int g, int heads, int groups) {
+  for (int h = g; h < heads; h += kBatch * groups, x += kBatch * xHop, y += kBatch * yHop) {
+    W v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (h + k * groups < heads) v[k] = reinterpret_cast<const W*>(x + k * xHop)[at];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (h + k * groups < heads) reinterpret_cast<W*>(y + k * yHop)[at] = v[k];
+  }
+}
+
 // kInter: pairs (2i, 2i + 1), else (i, i + rot / 2).  V elements a vector; interleaved with V = 1 a vector is one pair's
 // two elements, read one by one.
 template <typename T, int V, bool kInter>
@@ -66,9 +81,13 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   T* y = static_cast<T*>(a.y) + token * a.yToken + g * a.yHead;
   const long long xHop = a.xHead * a.headGroups, yHop = a.yHead * a.headGroups;
   if (c >= static_cast<unsigned>(a.rotVectors)) {  // behind rotDim: copied (out of place only)
-    const int at = a.rot + static_cast<int>(c - a.rotVectors) * V;
-    for (int h = g; h < a.heads; h += a.headGroups, x += xHop, y += yHop)
-      *reinterpret_cast<Vector*>(y + at) = *reinterpret_cast<const Vector*>(x + at);
+    x += a.rot;
+    y += a.rot;
+    const int at = static_cast<int>(c) - a.rotVectors;
+    if (V * sizeof(T) < 16 && a.copyBytes == 16)
+      copy_heads<uint4>(x, y, at, xHop, yHop, g, a.heads, a.headGroups);
+    else
+      copy_heads<Vector>(x, y, at, xHop, yHop, g, a.heads, a.headGroups);
     return;
   }
   const int at = kSingle ? 2 * c : c * V, partner = at + (kSingle ? 1 : a.rot / 2);
@@ -106,6 +125,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
   }
 }
 
+// Whether addresses and strides of x and y are multiples of v elements.
+bool lies_on(const QsaRotaryParams& p, int v, size_t size) {
+  const auto ok = [&](const void* q, int64_t token, int64_t head) {
+    return reinterpret_cast<uintptr_t>(q) % (v * size) == 0 && (p.numTokens == 1 || token % v == 0) &&
+           (p.numHeads == 1 || head % v == 0);
+  };
+  return ok(p.x, p.xTokenStride, p.xHeadStride) && ok(p.y, p.yTokenStride, p.yHeadStride);
+}
+
 template <typename T, int V>
 cudaError_t rotary_go(const QsaRotaryParams& p, const RotaryTurns& rt) {
   RotaryArgs a;
@@ -119,7 +147,11 @@ cudaError_t rotary_go(const QsaRotaryParams& p, const RotaryTurns& rt) {
   a.heads = p.numHeads;
   a.rot = p.rotDim;
   a.rotVectors = p.interleaved && V > 1 ? p.rotDim / V : p.rotDim / 2 / V;
-  a.vectors = a.rotVectors + (p.x == p.y ? 0 : (p.headDim - p.rotDim) / V);
+  constexpr int kWide = 16 / sizeof(T);
+  const int rest = p.x == p.y ? 0 : p.headDim - p.rotDim;
+  const bool wide = rest % kWide == 0 && p.rotDim % kWide == 0 && lies_on(p, kWide, sizeof(T));
+  a.copyBytes = wide ? 16 : V * sizeof(T);
+  a.vectors = a.rotVectors + rest * static_cast<int>(sizeof(T)) / a.copyBytes;
   a.magnitude = p.magnitude;
   a.inverse = p.inverse != 0;
   std::copy(rt.turn, rt.turn + kRotaryMaxPairs, a.turn);
@@ -139,14 +171,8 @@ cudaError_t rotary_go(const QsaRotaryParams& p, const RotaryTurns& rt) {
 
 // Whether vectors of v elements cut every rotated half (pair row) and every row's rest, at aligned addresses.
 bool fits(const QsaRotaryParams& p, int v, size_t size) {
-  const bool copies = p.x != p.y;
   const int piece = p.interleaved ? p.rotDim : p.rotDim / 2;
-  if (piece % v || (copies && (p.headDim - p.rotDim) % v)) return false;
-  const auto ok = [&](const void* q, int64_t token, int64_t head) {
-    return reinterpret_cast<uintptr_t>(q) % (v * size) == 0 && (p.numTokens == 1 || token % v == 0) &&
-           (p.numHeads == 1 || head % v == 0);
-  };
-  return ok(p.x, p.xTokenStride, p.xHeadStride) && ok(p.y, p.yTokenStride, p.yHeadStride);
+  return piece % v == 0 && (p.x == p.y || (p.headDim - p.rotDim) % v == 0) && lies_on(p, v, size);
 }
 
 template <typename T>

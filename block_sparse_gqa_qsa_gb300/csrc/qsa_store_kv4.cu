@@ -7,9 +7,15 @@
 // are asked for), so HBM bounds a large call and latency a small one.  Eight
 // lanes take a row, one 16-value group each; the row's maximum and its eight
 // scale bytes are joined with shuffles, so a row is written as 64 bytes of
-// codes and one 16-byte scale chunk.  The quotients are exact where they meet
-// a border: t is a power of two and s_j has 4 significant bits, so x / (s_j t)
-// of a 16-bit x is halfway between two codes exactly or off by 2^-12 of it.
+// codes and one 16-byte scale chunk.
+//
+// Quotients that meet a border between two codes (or scales) exactly have to be
+// seen as such.  t is a power of two, s_j has 4 significant bits and x at most 11,
+// so a quotient lies on a border or 2^-11 of itself away from it; a product with
+// a reciprocal, off by 2^-22, is rounded to 2^-16 (codes: an addend of 192) or to
+// 16 bits (scales), which puts it back on the border and no other one there.
+// (Two divisions and a corrected quotient instead: 50 us for 4 x 16384 ragged
+// rows of 4 heads, issue slots 77 % busy.)
 #include <algorithm>
 
 #include "qsa_internal.h"
@@ -35,35 +41,32 @@ struct StoreArgs {
   unsigned rows;  // 2 B S Hkv
 };
 
+// Words i = 0..7 of a group: values 2 i and 2 i + 1.
+__device__ __forceinline__ uint32_t word_of(const uint4 (&r)[2], int i) {
+  const uint4& q = r[i >> 2];
+  return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+}
 template <bool kBf16>
-__device__ __forceinline__ void unpack16(const uint4 (&r)[2], float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint4& q = r[i >> 2];
-    const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-    if constexpr (kBf16) {
-      x[2 * i] = __uint_as_float(w << 16);
-      x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-
-// The smallest power of two t in [2^-48, 2^48] with amax <= 2688 t.  (amax / 2688 has no rounding that reaches a power of
-// two from above: amax has at most 11 significant bits.)
-__device__ __forceinline__ float row_scale(float amax) {
-  const float r = __fdiv_rn(amax, 2688.0f);
-  if (!(r > kScaleLo)) return kScaleLo;
-  if (r > kScaleHi) return kScaleHi;
-  const uint32_t bits = __float_as_uint(r);
-  return __uint_as_float((bits + 0x7fffffu) & 0x7f800000u);
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
-
-// A scale may round up, so that fp16's largest values are held as up to 1/16 more (bf16's end far above 2688 2^48).
-__device__ __forceinline__ float saturated(float x) { return x > 65504.f ? 65504.f : x < -65504.f ? -65504.f : x; }
+// Two values times u, rounded to the type, saturating (a scale may round up, so that fp16's largest values are held as up to
+// 1/16 more); NaN stays NaN.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_saturated(float lo, float hi) {
+  uint32_t d;
+  if constexpr (kBf16)  // bf16's end lies far above 2688 2^48
+    d = pack_bf162(lo, hi);
+  else
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;\n" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads) store_kv4_kernel(const StoreArgs a) {
@@ -97,34 +100,45 @@ __global__ void __launch_bounds__(kThreads) store_kv4_kernel(const StoreArgs a) 
     if ((p >> 7) < a.maxPagesPerSeq)
       page = __ldg(a.pageTable + (static_cast<size_t>(b) * 2 + plane) * a.maxPagesPerSeq + (p >> 7));
   }
-  float x[16];
-  unpack16<kBf16>(raw, x);
-  float amax = 0.f;  // of the group's finite values
-  bool finite = true;
+  // the group's largest magnitude, as bits (their order is that of the magnitudes)
+  constexpr uint32_t kInf = kBf16 ? 0x7f80 : 0x7c00;
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float m = fabsf(x[i]);
-    finite &= m < INFINITY;
-    amax = fmaxf(amax, m < INFINITY ? m : 0.f);
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, word_of(raw, i) & 0x7fff7fff);
+  m = max(m & 0xffff, m >> 16);
+  const bool finite = m < kInf;
+  if (!finite) {  // of the finite ones
+    m = 0;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t x = word_of(raw, i >> 1) >> (16 * (i & 1)) & 0x7fff;
+      m = max(m, x < kInf ? x : 0u);
+    }
   }
-  float top = amax;
+  const float amax = unpack2<kBf16>(m).x;
+  uint32_t top = m;
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  const float ts = row_scale(top);
-  uint32_t s8 = f32_to_e4m3(__fdiv_rn(amax, kE2m1Max * ts), 0.f, 0.f, 0.f);  // saturates at 448
+  for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+  // t = 2^k, k the smallest with top <= 2688 2^k: the bits of a float count up with it, 2^23 to a power of two
+  const int above = __float_as_int(unpack2<kBf16>(top).x) - __float_as_int(2688.0f);
+  const int k = min(48, max(-48, (above + 0x7fffff) >> 23));
+  const float ts = __int_as_float((127 + k) << 23), tinv = __int_as_float((127 - k) << 23);
+  const float want = amax * tinv * (1.0f / kE2m1Max);
+  uint32_t s8 = f32_to_e4m3(fmaf(-256.f, want, fmaf(256.f, want, want)), 0.f, 0.f, 0.f);  // saturates at 448
   uint32_t lo, hi;
   e4m3_to_f16(s8, lo, hi);
   const float s = __low2float(*reinterpret_cast<const __half2*>(&lo));
   const float unit = s * ts;  // exact
-  const float inv = s == 0.f ? 0.f : __frcp_rn(unit);
+  const float inv = s == 0.f ? 0.f : rcp_approx(unit);
   uint32_t code[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y = x[8 * w + i], f = y * inv;
-      q[i] = copysignf(fmaf(fmaf(f, -unit, y), inv, f), y);  // the quotient with its remainder's share
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<kBf16>(word_of(raw, 4 * w + i));
+      const uint64_t r = ffma2(pack_f2(x.x, x.y), pack_f2(inv, inv), pack_f2(192.f, 192.f));
+      q[2 * i] = copysignf(lo_f2(r) - 192.f, x.x);
+      q[2 * i + 1] = copysignf(hi_f2(r) - 192.f, x.y);
     }
     code[w] = finite ? f32_to_e2m1(q) : 0;
   }
@@ -152,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) store_kv4_kernel(const StoreArgs a) 
       for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c[i]));
         const float u = finite ? unit : NAN;
-        v[4 * w + i] = kBf16 ? pack_bf162(f.x * u, f.y * u) : pack_half2(saturated(f.x * u), saturated(f.y * u));
+        v[4 * w + i] = pack_saturated<kBf16>(f.x * u, f.y * u);
       }
     }
     dense[0] = make_uint4(v[0], v[1], v[2], v[3]);

@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
 
 // total += the weights of a sequence's rows, in the order of the rows, for the tokens [lo, lo + range) of a (sequence, head).
 constexpr int kSumThreads = 512;
-constexpr int kAhead = 5;  // entries of a thread that are loaded a row ahead
+constexpr int kPer = 5;    // entries of a thread that are loaded ahead
+constexpr int kAhead = 4;  // rows that they are loaded ahead
 
 struct SumArgs {
   const int32_t* indices;
@@ -160,33 +161,31 @@ __global__ void __launch_bounds__(kSumThreads) sum_weights_kernel(const SumArgs 
   auto add = [&](int j, float w) {  // (entries that name nothing have weight 0)
     if (static_cast<unsigned>(j - lo) < static_cast<unsigned>(range)) atomicAdd(acc + (j - lo), w);
   };
-  int j[kAhead];
-  float w[kAhead];
-  auto load = [&](int t) {
+  int j[kAhead][kPer];
+  float w[kAhead][kPer];
+  auto load = [&](int t, int (&jt)[kPer], float (&wt)[kPer]) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < kPer; ++k) {
       const int e = threadIdx.x + k * kSumThreads;
       const bool in = t < n && e < a.topK;
-      j[k] = in ? __ldg(list + static_cast<size_t>(t) * a.topK + e) : -1;
-      w[k] = in ? __ldg(weight + t * hop + e) : 0.f;
+      jt[k] = in ? __ldg(list + static_cast<size_t>(t) * a.topK + e) : -1;
+      wt[k] = in ? __ldg(weight + t * hop + e) : 0.f;
     }
   };
-  load(0);
-  for (int t = 0; t < n; ++t) {
-    __syncthreads();  // the rows before this one are in
-    int jt[kAhead];
-    float wt[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      jt[k] = j[k];
-      wt[k] = w[k];
+  for (int i = 0; i < kAhead; ++i) load(i, j[i], w[i]);
+  for (int t0 = 0; t0 < n; t0 += kAhead)
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int t = t0 + i;
+      __syncthreads();  // the rows before this one are in
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) add(j[i][k], w[i][k]);
+      load(t + kAhead, j[i], w[i]);
+      if (t < n)
+        for (int e = threadIdx.x + kPer * kSumThreads; e < a.topK; e += kSumThreads)
+          add(__ldg(list + static_cast<size_t>(t) * a.topK + e), __ldg(weight + t * hop + e));
     }
-    load(t + 1);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) add(jt[k], wt[k]);
-    for (int e = threadIdx.x + kAhead * kSumThreads; e < a.topK; e += kSumThreads)
-      add(__ldg(list + static_cast<size_t>(t) * a.topK + e), __ldg(weight + t * hop + e));
-  }
   __syncthreads();
   float* total = a.total + (static_cast<size_t>(b) * a.Hkv + g) * a.totalLen + lo;
   for (int i = threadIdx.x; i < range; i += kSumThreads)
