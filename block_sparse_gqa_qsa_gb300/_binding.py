@@ -648,16 +648,13 @@ def rotary_frequencies(rot, *, theta, scaling="plain", factor=1.0, original_leng
     return out
 
 
-def _token_stride(t: torch.Tensor, name: str) -> int:
+def _token_stride(shape, strides, name: str) -> int:
     """Elements between tokens of [tokens, heads, D], or of [B, S, heads, D] whose tokens are evenly spaced."""
-    if t.dim() == 3:
-        return t.stride(0)
-    B, S = t.shape[:2]
-    if S == 1:
-        return t.stride(0)
-    if B > 1 and t.stride(0) != S * t.stride(1):
-        raise ValueError(f"{name}: sequences must follow each other evenly (stride {S * t.stride(1)}, got {t.stride(0)})")
-    return t.stride(1)
+    if len(shape) == 3 or shape[1] == 1:
+        return strides[0]
+    if shape[0] > 1 and strides[0] != shape[1] * strides[1]:
+        raise ValueError(f"{name}: sequences must follow each other evenly (stride {shape[1] * strides[1]}, got {strides[0]})")
+    return strides[1]
 
 
 def rotary(x, positions, out, inv_freq, *, interleaved=False, inverse=False, magnitude=1.0, stream=None):
@@ -669,25 +666,24 @@ def rotary(x, positions, out, inv_freq, *, interleaved=False, inverse=False, mag
     fn = _ROTARY_FN.get(et)
     if fn is None:
         raise ValueError("rotary: x must be float16, bfloat16 or float32")
-    if x.dim() not in (3, 4) or out.shape != x.shape or positions.shape != x.shape[:-2]:
+    shape, xs, ys, pairs = x.shape, x.stride(), out.stride(), inv_freq.shape
+    if len(shape) not in (3, 4) or out.shape != shape or positions.shape != shape[:-2]:
         raise ValueError("rotary: x and out are [tokens, heads, D] or [B, S, heads, D], positions [tokens] or [B, S]")
-    if inv_freq.dim() != 1 or inv_freq.dtype is not torch.float64 or inv_freq.device.type != "cpu" or \
-            not inv_freq.is_contiguous():
+    if len(pairs) != 1 or inv_freq.dtype is not torch.float64 or not inv_freq.is_cpu or not inv_freq.is_contiguous():
         raise ValueError("rotary: inv_freq must be a contiguous float64 vector on the host")
     dev = _current_device(x)
     if out.dtype is not et or not (x.get_device() == out.get_device() == dev):
         raise ValueError(f"rotary: out must be {et}, and x and out on the current device cuda:{dev}")
-    D = x.shape[-1]
-    if (D > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1)):
+    heads, D = shape[-2:]
+    tokens = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    if D > 1 and not (xs[-1] == ys[-1] == 1):
         raise ValueError("rotary: the rows of x and out must be contiguous")
-    if x.numel() == 0:
+    if not (tokens and heads and D):
         raise ValueError("rotary: x is empty")
-    heads = x.shape[-2]
-    packed = _ROTARY_PACK.pack(
+    r = _packed(fn)(_ROTARY_PACK.pack(
         x.data_ptr(), out.data_ptr(), _arg(positions, _I32, "positions", dev), inv_freq.data_ptr(),
-        _token_stride(x, "x"), x.stride(-2), _token_stride(out, "out"), out.stride(-2), x.numel() // (heads * D), heads, D,
-        2 * inv_freq.numel(), interleaved, inverse, magnitude, _raw_stream(stream, dev))
-    r = _packed(fn)(packed)
+        _token_stride(shape, xs, "x"), xs[-2], _token_stride(shape, ys, "out"), ys[-2], tokens, heads, D, 2 * pairs[0],
+        interleaved, inverse, magnitude, _raw_stream(stream, dev)))
     if r:
         _check(r)
 
@@ -702,14 +698,15 @@ _U8 = torch.uint8
 
 
 def _pool4(pool, page_table, name):
-    """(flat pages, KV heads, row bytes, pages per sequence) of a 4-bit pool uint8 [flat, 128, heads, bytes] and its table."""
-    if pool.dim() != 4 or page_table.dim() != 3 or pool.shape[1] != 128 or page_table.shape[1] != 2:
+    """(flat pages, KV heads, row bytes, B, pages per sequence) of a 4-bit pool uint8 [flat, 128, heads, bytes] and its table."""
+    try:
+        flat, tpp, heads, row = pool.shape
+        B, two, pages = page_table.shape
+    except ValueError:
+        raise ValueError(f"{name}: pool has 4 dimensions, page_table 3") from None
+    if tpp != 128 or two != 2:
         raise ValueError(f"{name}: pool is uint8 [pages, 128, heads, bytes], page_table [B, 2, pages]")
-    return pool.shape[0], pool.shape[2], pool.shape[3], page_table.shape[2]
-
-
-def _opt(t, dtype, name, device):
-    return 0 if t is None else _arg(t, dtype, name, device)
+    return flat, heads, row, B, pages
 
 
 def store_kv4(k, v, ctx, pool, page_table, *, new_lengths=None, k_out=None, v_out=None, status=None, stream=None):
@@ -720,24 +717,25 @@ def store_kv4(k, v, ctx, pool, page_table, *, new_lengths=None, k_out=None, v_ou
     et = k.dtype
     if et is not _F16 and et is not _BF16:
         raise ValueError("store_kv4: k must be float16 or bfloat16")
-    nflat, Hkv, row, pages = _pool4(pool, page_table, "store_kv4")
-    if k.dim() != 4 or v.shape != k.shape or k.shape[2] != Hkv or ctx.shape != k.shape[:1] or \
-            page_table.shape[0] != k.shape[0] or (new_lengths is not None and new_lengths.shape != ctx.shape) or \
-            (k_out is not None and k_out.shape != k.shape) or (v_out is not None and v_out.shape != k.shape):
+    nflat, Hkv, row, ptb, pages = _pool4(pool, page_table, "store_kv4")
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    if len(shape) != 4 or v.shape != shape or shape[2] != Hkv or ptb != shape[0] or ctx.shape != (ptb,) or \
+            (new_lengths is not None and new_lengths.shape != (ptb,)) or \
+            (k_out is not None and k_out.shape != shape) or (v_out is not None and v_out.shape != shape):
         raise ValueError("store_kv4: shape mismatch")
-    B, S, _, D = k.shape
+    B, S, _, D = shape
     dev = _current_device(k)
     if v.dtype is not et or not (k.get_device() == v.get_device() == dev):
         raise ValueError(f"store_kv4: v must be {et}, and k and v on the current device cuda:{dev}")
-    for t, n in ((k, "k"), (v, "v")):
-        if t.stride(3) != 1 or (Hkv > 1 and t.stride(2) != D):
-            raise ValueError(f"store_kv4: the heads of a token of {n} must lie together")
-    packed = _STORE4_PACK.pack(
-        k.data_ptr(), v.data_ptr(), _arg(ctx, _I32, "contextLengths", dev), _opt(new_lengths, _I32, "new_lengths", dev),
-        _opt(k_out, et, "k_out", dev), _opt(v_out, et, "v_out", dev), _arg(pool, _U8, "pool", dev),
-        _arg(page_table, _I32, "pageTable", dev), _opt(status, _I32, "status", dev), _token_stride(k, "k"),
-        _token_stride(v, "v"), B, S, Hkv, D, row, nflat, pages, _raw_stream(stream, dev))
-    r = _packed("qsa_store_kv4_bf16" if et is _BF16 else "qsa_store_kv4")(packed)
+    if not (ks[3] == vs[3] == 1) or (Hkv > 1 and not (ks[2] == vs[2] == D)):
+        raise ValueError("store_kv4: the heads of a token of k and v must lie together")
+    r = _packed("qsa_store_kv4_bf16" if et is _BF16 else "qsa_store_kv4")(_STORE4_PACK.pack(
+        k.data_ptr(), v.data_ptr(), _arg(ctx, _I32, "contextLengths", dev),
+        0 if new_lengths is None else _arg(new_lengths, _I32, "new_lengths", dev),
+        0 if k_out is None else _arg(k_out, et, "k_out", dev), 0 if v_out is None else _arg(v_out, et, "v_out", dev),
+        _arg(pool, _U8, "pool", dev), _arg(page_table, _I32, "pageTable", dev),
+        0 if status is None else _arg(status, _I32, "status", dev), _token_stride(shape, ks, "k"),
+        _token_stride(shape, vs, "v"), B, S, Hkv, D, row, nflat, pages, _raw_stream(stream, dev)))
     if r:
         _check(r)
 
@@ -747,18 +745,26 @@ def _lists4(q, pool, page_table, indices, ctx, new_lengths, name):
     et = q.dtype
     if et is not _F16 and et is not _BF16:
         raise ValueError(f"{name}: q must be float16 or bfloat16")
-    nflat, Hkv, row, pages = _pool4(pool, page_table, name)
-    if q.dim() != 4 or indices.dim() != 3:
-        raise ValueError(f"{name}: q has 4 dimensions, indices 3")
-    B, S, Hq, D = q.shape
-    if indices.shape[:2] != (B, S) or ctx.shape != (B,) or page_table.shape[0] != B or \
-            (new_lengths is not None and new_lengths.shape != (B,)):
+    nflat, Hkv, row, ptb, pages = _pool4(pool, page_table, name)
+    try:
+        B, S, Hq, D = q.shape
+        ib, is_, topK = indices.shape
+    except ValueError:
+        raise ValueError(f"{name}: q has 4 dimensions, indices 3") from None
+    if ib != B or is_ != S or ctx.shape != (B,) or ptb != B or (new_lengths is not None and new_lengths.shape != (B,)):
         raise ValueError(f"{name}: shape mismatch")
     dev = _current_device(q)
-    ptrs = (_arg(q, et, "q", dev), _arg(pool, _U8, "pool", dev), _arg(page_table, _I32, "pageTable", dev),
-            _arg(indices, _I32, "indices", dev), _arg(ctx, _I32, "contextLengths", dev),
-            _opt(new_lengths, _I32, "new_lengths", dev))
-    return et, dev, ptrs, (B, S, Hq, Hkv, D, row, nflat, pages, indices.shape[2])
+    if pool.dtype is not _U8 or page_table.dtype is not _I32 or indices.dtype is not _I32 or ctx.dtype is not _I32 or \
+            not (q.get_device() == pool.get_device() == page_table.get_device() == indices.get_device() ==
+                 ctx.get_device() == dev) or \
+            not (q.is_contiguous() and pool.is_contiguous() and page_table.is_contiguous() and indices.is_contiguous() and
+                 ctx.is_contiguous()):
+        for t, d, n in ((q, et, "q"), (pool, _U8, "pool"), (page_table, _I32, "pageTable"), (indices, _I32, "indices"),
+                        (ctx, _I32, "contextLengths")):
+            _arg(t, d, n, dev)
+    ptrs = (q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), indices.data_ptr(), ctx.data_ptr(),
+            0 if new_lengths is None else _arg(new_lengths, _I32, "new_lengths", dev))
+    return et, dev, ptrs, (B, S, Hq, Hkv, D, row, nflat, pages, topK)
 
 
 def sparse_paged_kv4(q, pool, page_table, indices, ctx, out, *, scale, new_lengths=None, lse=None, status=None, stream=None):
@@ -766,11 +772,11 @@ def sparse_paged_kv4(q, pool, page_table, indices, ctx, out, *, scale, new_lengt
     [numFlat,128,Hkv,rowBytes >= 80], indices int32 [B,S,topK], ctx int32 [B] cached lengths, new_lengths int32 [B] query
     rows (None: min(S, ctx)); scale multiplies q . k; lse float32 [B,S,Hq] gets the log-sum-exp of the scaled logits."""
     et, dev, ptrs, sizes = _lists4(q, pool, page_table, indices, ctx, new_lengths, "sparse_paged_kv4")
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+    if out.shape != sizes[:3] + (sizes[4],) or (lse is not None and lse.shape != sizes[:3]):
         raise ValueError("sparse_paged_kv4: shape mismatch")
-    packed = _PAGED4_PACK.pack(*ptrs, _arg(out, et, "out", dev), _opt(lse, _F32, "lse", dev),
-                               _opt(status, _I32, "status", dev), *sizes, scale, _raw_stream(stream, dev))
-    r = _packed("qsa_sparse_paged_kv4_bf16" if et is _BF16 else "qsa_sparse_paged_kv4")(packed)
+    r = _packed("qsa_sparse_paged_kv4_bf16" if et is _BF16 else "qsa_sparse_paged_kv4")(_PAGED4_PACK.pack(
+        *ptrs, _arg(out, et, "out", dev), 0 if lse is None else _arg(lse, _F32, "lse", dev),
+        0 if status is None else _arg(status, _I32, "status", dev), *sizes, scale, _raw_stream(stream, dev)))
     if r:
         _check(r)
 
@@ -781,14 +787,15 @@ def sparse_weights_kv4(q, pool, page_table, indices, ctx, lse, weights, total=No
     lengths and the lse it left: weights float32 [B,S,Hkv,topK] gets every list entry's attention weight, summed over the
     query heads of a KV head, and total float32 [B,Hkv,tokens] (None: no totals) gathers them by token."""
     et, dev, ptrs, sizes = _lists4(q, pool, page_table, indices, ctx, new_lengths, "sparse_weights_kv4")
-    B, S, _, Hkv = sizes[:4]
-    if lse.shape != q.shape[:3] or weights.shape != (B, S, Hkv, sizes[8]) or \
-            (total is not None and (total.dim() != 3 or total.shape[:2] != (B, Hkv))):
+    B, S, Hq, Hkv = sizes[:4]
+    counted = None if total is None else total.shape
+    if lse.shape != (B, S, Hq) or weights.shape != (B, S, Hkv, sizes[8]) or \
+            (counted is not None and (len(counted) != 3 or counted[:2] != (B, Hkv))):
         raise ValueError("sparse_weights_kv4: shape mismatch")
-    packed = _WEIGHTS4_PACK.pack(*ptrs, _arg(lse, _F32, "lse", dev), _arg(weights, _F32, "weights", dev),
-                                 _opt(total, _F32, "total", dev), _opt(status, _I32, "status", dev), *sizes,
-                                 0 if total is None else total.shape[2], scale, _raw_stream(stream, dev))
-    r = _packed("qsa_sparse_weights_kv4_bf16" if et is _BF16 else "qsa_sparse_weights_kv4")(packed)
+    r = _packed("qsa_sparse_weights_kv4_bf16" if et is _BF16 else "qsa_sparse_weights_kv4")(_WEIGHTS4_PACK.pack(
+        *ptrs, _arg(lse, _F32, "lse", dev), _arg(weights, _F32, "weights", dev),
+        0 if total is None else _arg(total, _F32, "total", dev), 0 if status is None else _arg(status, _I32, "status", dev),
+        *sizes, 0 if counted is None else counted[2], scale, _raw_stream(stream, dev)))
     if r:
         _check(r)
 
@@ -799,17 +806,17 @@ def evict_kv4(pool, page_table, ctx, total, kept, kept_lengths, total_out=None, 
     tokens per KV head, by total float32 [B,Hkv,tokens]; the first `sinks` and the last `recent` always stay.  kept int32
     [B,Hkv,budget] gets the tokens now in each slot (-1 behind the last), kept_lengths int32 [B] the new lengths, total_out
     (may be total) their totals, zeros behind them."""
-    nflat, Hkv, row, pages = _pool4(pool, page_table, "evict_kv4")
-    B = page_table.shape[0]
-    if total.dim() != 3 or total.shape[:2] != (B, Hkv) or kept.dim() != 3 or kept.shape[:2] != (B, Hkv) or \
-            ctx.shape != (B,) or kept_lengths.shape != (B,) or (total_out is not None and total_out.shape != total.shape):
+    nflat, Hkv, row, B, pages = _pool4(pool, page_table, "evict_kv4")
+    shape, slots = total.shape, kept.shape
+    if len(shape) != 3 or shape[:2] != (B, Hkv) or len(slots) != 3 or slots[:2] != (B, Hkv) or \
+            ctx.shape != (B,) or kept_lengths.shape != (B,) or (total_out is not None and total_out.shape != shape):
         raise ValueError("evict_kv4: shape mismatch")
     dev = _current_device(pool)
-    packed = _EVICT4_PACK.pack(
+    r = _packed("qsa_evict_kv4")(_EVICT4_PACK.pack(
         _arg(pool, _U8, "pool", dev), _arg(page_table, _I32, "pageTable", dev), _arg(ctx, _I32, "contextLengths", dev),
         _arg(total, _F32, "total", dev), _arg(kept, _I32, "kept", dev), _arg(kept_lengths, _I32, "kept_lengths", dev),
-        _opt(total_out, _F32, "total_out", dev), _opt(status, _I32, "status", dev), B, Hkv, 128, row, nflat, pages,
-        total.shape[2], kept.shape[2], sinks, recent, _raw_stream(stream, dev))
-    r = _packed("qsa_evict_kv4")(packed)
+        0 if total_out is None else _arg(total_out, _F32, "total_out", dev),
+        0 if status is None else _arg(status, _I32, "status", dev), B, Hkv, 128, row, nflat, pages, shape[2], slots[2], sinks,
+        recent, _raw_stream(stream, dev)))
     if r:
         _check(r)
