@@ -142,8 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kv4_kernel(const EvictArgs 
     int sum = 0;
     if (tid < kCoarse) {
       const uint32_t mine = smem_addr(&sh.coarse[pass][kCoarse - 1 - tid]);
-#pragma unroll 4
-      for (int c = 0; c < N; ++c) sum += cluster_ld_int(cluster_addr(mine, c));
+      int n[kMostCluster];
+#pragma unroll
+      for (int c = 0; c < kMostCluster; ++c) n[c] = c < N ? cluster_ld_int(cluster_addr(mine, c)) : 0;
+#pragma unroll
+      for (int c = 0; c < kMostCluster; ++c) sum += n[c];
     }
     int all;
     const int before = cta_exclusive_scan<kThreads>(sum, sh.scan, all);
@@ -198,26 +201,26 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kv4_kernel(const EvictArgs 
     sh.equal[warp] = equal;
   }
   __syncthreads();
-  if (tid == 0) {
-    int x = 0, y = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      x += sh.above[w];
-      y += sh.equal[w];
+  // lane w < 16: warp w's counts; then lane c: CTA c's
+  above = lane < kWarps ? sh.above[lane] : 0;
+  equal = lane < kWarps ? sh.equal[lane] : 0;
+  if (warp == 0) {
+    const int x = __reduce_add_sync(kFull, above), y = __reduce_add_sync(kFull, equal);
+    if (lane == 0) {
+      sh.runs[0] = x;
+      sh.runs[1] = y;
     }
-    sh.runs[0] = x;
-    sh.runs[1] = y;
   }
+  above = lane < warp ? above : 0;
+  equal = lane < warp ? equal : 0;
   cluster_sync_all();  // every CTA's sums are in
-  above = equal = 0;   // now: of the tokens before this warp's run
-  for (int c = 0; c < rank; ++c) {
-    const uint32_t runs = cluster_addr(smem_addr(sh.runs), c);
+  if (lane < rank) {
+    const uint32_t runs = cluster_addr(smem_addr(sh.runs), lane);
     above += cluster_ld_int(runs);
     equal += cluster_ld_int(runs + 4);
   }
-  for (int w = 0; w < warp; ++w) {
-    above += sh.above[w];
-    equal += sh.equal[w];
-  }
+  above = __reduce_add_sync(kFull, above);  // now: of the tokens before this warp's run
+  equal = __reduce_add_sync(kFull, equal);
   for (int j0 = wfrom; j0 < wto; j0 += 32) {
     const int j = j0 + lane;
     const uint32_t k = j < wto ? key_at(j) : 0;
