@@ -11,7 +11,7 @@
 // Two kernels share the arithmetic.  With few (row, KV head) pairs, a CTA of 4
 // warps takes one, or a cluster of up to 8 CTAs shares it, the list dealt out
 // to the warps in steps of 32 entries; with many, a CTA takes four KV heads of a
-// row (or two of two rows), a warp each, and resolves a list once for its heads.
+// row, a warp each, and resolves a list once for its heads.
 // A warp runs its steps by itself: the 32 K and V rows of 80 bytes are gathered
 // with cp.async into its own tiles, the K rows' codes together with both rows'
 // scale chunks, the V rows' codes after them.
@@ -108,9 +108,11 @@ __device__ __forceinline__ void values32(Acc<NT>& A, uint32_t codes, uint32_t gr
   }
 }
 
-// Resident CTAs per SM that the registers allow.
+// Resident CTAs per SM that the registers allow.  Many rows: 5 and 6 (96 and 80 registers, little of a lane in local memory)
+// took 1654 and 1774 us for an 8192-row prompt where 4 took 1650.  Split: decode of 16, 32, 64, 200 sequences with 4 KV heads
+// 11.9, 17.7, 26.6, 64.1 us with 3, 12.9, 19.0, 27.7, 68.9 with 4.
 template <int NT>
-constexpr int kSplitCtasPerSm = NT == 1 ? 4 : 2;
+constexpr int kSplitCtasPerSm = NT == 1 ? 3 : 2;
 template <int NT>
 constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
 // The tiles, and later the merge buffers: the warps' O, m, l and lse sums, then the CTA's.
@@ -341,11 +343,10 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
-// Many rows: a warp takes one KV head of a row and the whole list, a group of kH warps (4 or 2) kH heads of the row, a CTA
-// 4 / kH groups.  The heads share the list, so a group's warps resolve its entries once for all of them, a chunk of 32 kH
-// at a time, 32 per warp: row ids go to shared memory for every warp of the group.  Chunk c + 1's are written before the
-// barrier that opens chunk c (its first rows are gathered in chunk c's last step).  Groups share nothing: each has a
-// barrier of its own and leaves when it is done.
+// Many rows: a CTA takes four KV heads of a row, each warp one of them and the whole list.  The heads share the list, so the
+// warps resolve its entries once for all of them, a chunk of 128 at a time, 32 per warp: row ids go to shared memory for
+// every warp.  Chunk c + 1's are written before the barrier that opens chunk c (its first rows are gathered in chunk c's
+// last step).
 constexpr int kRowsGroupsAt = kSetBytes;
 constexpr int kRowsEntriesAt = kRowsGroupsAt + kKv4ScaleBytes;
 constexpr int kRowsQueriesAt = kRowsEntriesAt + kStep * 8;
@@ -360,47 +361,40 @@ constexpr int kMasksAt = kIdsAt<NT> + 3 * kWarps * kStep * 2 * 4;  // [chunk % 3
 template <int NT>
 constexpr int kRowsSmem = kMasksAt<NT> + 64;
 
-template <int NT, bool kBf16, bool kLse, int kH>
+template <int NT, bool kBf16, bool kLse>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_rows_kernel(const PagedArgs a, int items) {
-  constexpr int kChunk = kH * kStep;  // entries
+  constexpr int kChunk = kWarps * kStep;  // entries
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / kH, w0 = group * kH;          // this group and its first warp
-  const int tid = static_cast<int>(threadIdx.x) - w0 * 32;  // within the group
-  const int item = static_cast<int>(blockIdx.x) * (kWarps / kH) + group;
-  if (item >= items) return;
-  auto group_sync = [&] {
-    if (group == 0)
-      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kH) : "memory");
-    else
-      asm volatile("bar.sync 2, %0;\n" ::"n"(32 * kH) : "memory");
-  };
-  Row r = row_of(a, item, kH);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int item = static_cast<int>(blockIdx.x);
+  if (item >= items) return;  // (none is; without the test the compiler puts 48 bytes of a lane in local memory: 1627 us
+                              // for an 8192-row prompt instead of 1520)
+  Row r = row_of(a, item, kWarps);
   List list(a, r);
   const int j0 = list.at(tid), j1 = list.at(tid + kChunk);
   int slot = tid + 2 * kChunk, j2 = list.at(slot);
   row_lengths(a, r);
   list.L = r.L;
   if (r.t >= r.n) {
-    no_tokens(a, r.head0, kH * a.G, tid, 32 * kH);
+    no_tokens(a, r.head0, kWarps * a.G, tid, kThreads);
     return;
   }
   uint8_t* mine = smem + warp * kWarpTiles<NT>;
   const uint32_t set = smem_addr(mine), groups = set + kRowsGroupsAt;
   float2* entries = reinterpret_cast<float2*>(mine + kRowsEntriesAt);
-  int* ids = reinterpret_cast<int*>(smem + kIdsAt<NT>) + w0 * 2 * kStep;
-  unsigned* masks = reinterpret_cast<unsigned*>(smem + kMasksAt<NT>) + w0;
+  int* ids = reinterpret_cast<int*>(smem + kIdsAt<NT>);
+  unsigned* masks = reinterpret_cast<unsigned*>(smem + kMasksAt<NT>);
   const uint32_t rowBytes = static_cast<uint32_t>(a.Hkv) * a.poolHeadDim;
-  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + warp - w0) * a.poolHeadDim;
+  const uint8_t* base = a.pool + static_cast<size_t>(r.kvh + warp) * a.poolHeadDim;
   const SetDst dst(set);
 
   auto put_rows = [&](const Pages& p, int buf) {  // row ids of the thread's entry of a chunk
     const PoolRows rows = list.rows_of(p);
-    int* at = ids + (buf * kWarps + warp - w0) * 2 * kStep + kv4_row_place(lane);
+    int* at = ids + (buf * kWarps + warp) * 2 * kStep + kv4_row_place(lane);
     at[0] = rows.ok ? rows.k : -1;
     at[kStep] = rows.ok ? rows.v : -1;
     const unsigned mask = __ballot_sync(kFull, rows.ok);
-    if (lane == 0) masks[buf * kWarps + warp - w0] = mask;
+    if (lane == 0) masks[buf * kWarps + warp] = mask;
   };
   auto ids_of = [&](int buf, int step) { return ids + (buf * kWarps + step) * 2 * kStep; };
   Acc<NT> A;
@@ -410,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
   Pages p1 = list.pages_of(j1);
   const uint32_t queries = set + kRowsQueriesAt;
   float qs[NT][2];
-  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + (warp - w0) * a.G) * (kD / 8), a.G, queries, qs);
-  group_sync();
+  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + warp * a.G) * (kD / 8), a.G, queries, qs);
+  __syncthreads();
   unsigned mask = masks[0];  // of the current step, whose rows are gathered
   gather_k(ids_of(0, 0), mask, dst, 0, base, rowBytes);
   gather_v(ids_of(0, 0), mask, dst, 0, base, rowBytes);
@@ -423,10 +417,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
     p1 = list.pages_of(j2);
     slot += kChunk;
     j2 = list.at(slot);
-    group_sync();
+    __syncthreads();
 #pragma unroll 1
-    for (int e = 0; e < kH; ++e) {
-      const bool last = e == kH - 1;
+    for (int e = 0; e < kWarps; ++e) {
+      const bool last = e == kWarps - 1;
       const int gbuf = last ? nbuf : buf, ge = last ? 0 : e + 1;  // the next step
       const unsigned next = masks[gbuf * kWarps + ge];
       const int* nids = ids_of(gbuf, ge);
@@ -462,21 +456,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
   float* mw = ow + H * kPad;                   // [m, l, lse sums][H]
   stash<NT, kLse>(A, ls, ow, mw, mw + H, mw + 2 * H);
   __syncwarp();
-  const size_t head0 = r.head0 + (warp - w0) * a.G;
+  const size_t head0 = r.head0 + warp * a.G;
   uint2* out = static_cast<uint2*>(a.o) + head0 * (kD / 4);
   for (int h = 0; h < a.G; ++h)
     out[h * 32 + lane] = normalised<kBf16>(*reinterpret_cast<const float4*>(ow + h * kPad + 4 * lane), mw[H + h]);
   if (kLse && lane < a.G) a.lse[head0 + lane] = lse_of(mw[lane], mw[2 * H + lane]);
 }
 
-template <int NT, bool kBf16, bool kLse, int kH>
+template <int NT, bool kBf16, bool kLse>
 cudaError_t rows_go(const PagedArgs& a, long long pairs, cudaStream_t st) {
-  auto kernel = sparse_paged_kv4_rows_kernel<NT, kBf16, kLse, kH>;
+  auto kernel = sparse_paged_kv4_rows_kernel<NT, kBf16, kLse>;
   constexpr int kSmemBytes = kRowsSmem<NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>((pairs + kWarps - 1) / kWarps), kThreads, kSmemBytes, st>>>(
-      a, static_cast<int>(pairs / kH));
+  kernel<<<static_cast<unsigned>(pairs / kWarps), kThreads, kSmemBytes, st>>>(
+      a, static_cast<int>(pairs / kWarps));
   return cudaGetLastError();
 }
 
@@ -523,12 +517,28 @@ long long resident_clusters(int split) {
 template <int NT, bool kBf16, bool kLse>
 cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   const long long slots = static_cast<long long>(kCtasPerSm<NT>) * sm_count();  // CTAs resident at once
-  // A warp per pair from two waves of such CTAs on.
-  if (a.Hkv % 2 == 0 && pairs / kWarps >= 2 * slots)
-    return a.Hkv % 4 == 0 ? rows_go<NT, kBf16, kLse, 4>(a, pairs, st) : rows_go<NT, kBf16, kLse, 2>(a, pairs, st);
-  // Otherwise as many CTAs per pair as leave all clusters resident at once, at most one per 128 entries of the list.
-  a.split = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
-  while (pairs > resident_clusters<NT, kBf16, kLse>(a.split) && a.split > 1) --a.split;
+  // A warp per pair for just under one wave of such CTAs, and from 1.6 waves on: 600 rows of 4 heads of 8 queries (1 wave) 139
+  // us, 155 in the other form, 700 (1.15) 181 and 180, 1000 (1.6) 238 and 252, 2048 460 and 508; of 14 queries 280 rows (0.9
+  // waves) 97 and 106, 320 156 and 122.  (Two heads of two rows to a CTA, for 2 KV heads: 1200 pairs 96 us instead of 82,
+  // 4400 292 instead of 276, 8192 as long.)
+  const long long ctas = pairs / kWarps;
+  if (a.Hkv % kWarps == 0 && ((10 * ctas >= 9 * slots && ctas <= slots) || 10 * ctas >= 16 * slots))
+    return rows_go<NT, kBf16, kLse>(a, pairs, st);
+  // Otherwise 1 to 8 CTAs per pair, all clusters resident at once, at most one CTA per 128 entries of the list: those for
+  // which a warp's steps times (1 + 2 CTAs on an SM) is least.  (Decode with lists of 2051, us by CTAs per pair: 32 pairs
+  // 9.0 with 4, 8.8 with 8; 96 pairs 17.0 with 2, 13.9 with 3, 15.1 with 4; 128 pairs 18.8, 17.6, 17.8 with 1, 2, 3; a
+  // count that leaves clusters waiting costs a fifth more at least.)
+  const int sms = sm_count(), most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
+  long long least = 0;
+  for (int split = 1; split <= most; ++split) {
+    if (split > 1 && pairs > resident_clusters<NT, kBf16, kLse>(split)) continue;
+    const long long steps = (a.topK + kStep * kWarps * split - 1) / (kStep * kWarps * split);
+    const long long cost = steps * (1 + 2 * ((pairs * split + sms - 1) / sms));
+    if (split == 1 || cost <= least) {
+      least = cost;
+      a.split = split;
+    }
+  }
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = split_config<NT>(pairs, a.split, st, &at);
   auto kernel = sparse_paged_kv4_split_kernel<NT, kBf16, kLse>;
