@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
   uint2* out = static_cast<uint2*>(a.o) + head0 * (kD / 4);
   for (int h = 0; h < a.G; ++h)
     out[h * 32 + lane] = normalised<kBf16>(*reinterpret_cast<const float4*>(ow + h * kPad + 4 * lane), mw[H + h]);
-  if (kLse && lane < a.G) a.lse[head0 + lane] = lse_of(mw[lane], mw[2 * H + lane]);
+  if (kLse && a.lse && lane < a.G) a.lse[head0 + lane] = lse_of(mw[lane], mw[2 * H + lane]);
 }
 
 template <int NT, bool kBf16, bool kLse>
@@ -521,9 +521,11 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   // us, 155 in the other form, 700 (1.15) 181 and 180, 1000 (1.6) 238 and 252, 2048 460 and 508; of 14 queries 280 rows (0.9
   // waves) 97 and 106, 320 156 and 122.  (Two heads of two rows to a CTA, for 2 KV heads: 1200 pairs 96 us instead of 82,
   // 4400 292 instead of 276, 8192 as long.)
+  // (bf16 groups up to 8 sum for lse whether it is asked for or not: the compiler then keeps a lane in registers, 918 us for
+  // 4096 rows instead of 942.)
   const long long ctas = pairs / kWarps;
   if (a.Hkv % kWarps == 0 && ((10 * ctas >= 9 * slots && ctas <= slots) || 10 * ctas >= 16 * slots))
-    return rows_go<NT, kBf16, kLse>(a, pairs, st);
+    return rows_go<NT, kBf16, kLse || (kBf16 && NT == 1)>(a, pairs, st);
   // Otherwise 1 to 8 CTAs per pair, all clusters resident at once, at most one CTA per 128 entries of the list: those for
   // which a warp's steps times (1 + 2 CTAs on an SM) is least.  (Decode with lists of 2051, us by CTAs per pair: 32 pairs
   // 9.0 with 4, 8.8 with 8; 96 pairs 17.0 with 2, 13.9 with 3, 15.1 with 4; 128 pairs 18.8, 17.6, 17.8 with 1, 2, 3; a

@@ -20,9 +20,14 @@ qsa_gather_selected into contiguous scratch per step.  `--op kv8` runs a
 workload's steps on an 8-bit cache: qsa_append_kv8 (the whole prompts, or one
 token per sequence), the indexer, and qsa_sparse_paged_kv8 over its lists; a
 decode keeps the indexer's fp16 state in a one-head pool on the same page table.
+`--op kv4` runs them on a 4-bit cache: qsa_rotary in the packed projections,
+qsa_store_kv4, the indexer and qsa_sparse_paged_kv4; a decode step also gathers
+its tokens' attention weights (qsa_sparse_weights_kv4), and behind the last step
+qsa_evict_kv4 cuts every sequence back to 4096 tokens.
 
     python -m block_sparse_gqa_qsa_gb300.run_case prefill_S8192 --op kv8 --steps 2
     python -m block_sparse_gqa_qsa_gb300.run_case decode_B32_L2k-64k --op kv8 --steps 2
+    python -m block_sparse_gqa_qsa_gb300.run_case decode_B32_L2k-64k --op kv4 --steps 2
 """
 from __future__ import annotations
 
@@ -135,6 +140,61 @@ def _kv8_decode_steps(cfg, steps):
         qb.sparse_paged_kv8(q, pool, scale, d["page_table"], ind, d["ctx"], out, scale=cfg.scale)
 
 
+KV4_BUDGET, KV4_SINKS, KV4_RECENT = 4096, 4, 256  # what the eviction behind the 4-bit decode steps keeps
+
+
+def _kv4_prefill_steps(cfg, steps):
+    t = {k: v.cuda() for k, v in syn.make_prefill(cfg).items()}
+    qkv = torch.cat([t["q"], t["k"], t["v"]], dim=2).contiguous()
+    npg = -(-cfg.S // syn.TOKENS_PER_PAGE)
+    ids = torch.randperm(cfg.B * npg, generator=torch.Generator().manual_seed(cfg.seed)).int().cuda().view(cfg.B, npg)
+    pt = torch.stack([ids, ids + cfg.B * npg], dim=1).contiguous()
+    pool = torch.zeros((2 * cfg.B * npg, syn.TOKENS_PER_PAGE, cfg.Hkv, qb.KV4_ROW_BYTES), dtype=torch.uint8, device="cuda")
+    row = torch.arange(cfg.S, dtype=torch.int32, device="cuda")
+    pos = torch.where(row < t["ctx"][:, None], row, torch.full_like(row, -1))
+    freq = qb.rotary_frequencies(cfg.rot, theta=cfg.theta)
+    qk, k, v = qkv[:, :, :cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq:cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq + cfg.Hkv:]
+    ws = qb.alloc_workspace(qb.indexer_prefill_workspace_size(cfg.B, cfg.S, cfg.di, cfg.ratio))
+    ind = torch.empty((cfg.B, cfg.S, cfg.topK), dtype=torch.int32, device="cuda")
+    out = torch.empty((cfg.B, cfg.S, cfg.Hq, cfg.D), dtype=torch.float16, device="cuda")
+    for _ in range(steps):
+        qb.rotary(qk, pos, qk, freq)
+        qb.store_kv4(k, v, t["ctx"], pool, pt)
+        qb.indexer_prefill(t["idxQ"], t["idxK"], t["wq"], t["wk"], t["ctx"], ind, ws, rot=cfg.rot, ratio=cfg.ratio,
+                           budget=cfg.budget, topK=cfg.topK, theta=cfg.theta, eps=cfg.eps)
+        qb.sparse_paged_kv4(qkv[:, :, :cfg.Hq].contiguous(), pool, pt, ind, t["ctx"], out, scale=cfg.scale)
+    return out, pool
+
+
+def _kv4_decode_steps(cfg, steps):
+    d = syn.make_decode(dataclasses.replace(cfg, Hkv=1), device="cuda")  # its one-head pool holds the indexer's state
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in d.items()}
+    ctx, pt = d["ctx"], d["page_table"]
+    pool = torch.zeros((d["pool"].shape[0], syn.TOKENS_PER_PAGE, cfg.Hkv, qb.KV4_ROW_BYTES), dtype=torch.uint8, device="cuda")
+    qkv = torch.randn((cfg.B, 1, cfg.Hq + 2 * cfg.Hkv, cfg.D), device="cuda").half()
+    pos = (ctx - 1).view(cfg.B, 1)
+    freq = qb.rotary_frequencies(cfg.rot, theta=cfg.theta)
+    qk, k, v = qkv[:, :, :cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq:cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq + cfg.Hkv:]
+    ws = qb.alloc_workspace(qb.indexer_decode_workspace_size(cfg.B, cfg.maxPagesPerSeq, cfg.ratio, cfg.budget))
+    ind = torch.empty((cfg.B, 1, cfg.topK), dtype=torch.int32, device="cuda")
+    out = torch.empty((cfg.B, 1, cfg.Hq, cfg.D), dtype=torch.float16, device="cuda")
+    lse = torch.empty((cfg.B, 1, cfg.Hq), device="cuda")
+    weights = torch.empty((cfg.B, 1, cfg.Hkv, cfg.topK), device="cuda")
+    total = torch.zeros((cfg.B, cfg.Hkv, syn.TOKENS_PER_PAGE * cfg.maxPagesPerSeq), device="cuda")
+    for _ in range(steps):
+        qb.rotary(qk, pos, qk, freq)
+        qb.store_kv4(k, v, ctx, pool, pt)
+        qb.indexer_decode(d["idxQ"], d["idxK"], d["wq"], d["wk"], d["pool"], pt, ctx, ind, ws, D=cfg.D,
+                          rot=cfg.rot, ratio=cfg.ratio, budget=cfg.budget, topK=cfg.topK, theta=cfg.theta, eps=cfg.eps)
+        q = qkv[:, :, :cfg.Hq].contiguous()
+        qb.sparse_paged_kv4(q, pool, pt, ind, ctx, out, scale=cfg.scale, lse=lse)
+        qb.sparse_weights_kv4(q, pool, pt, ind, ctx, lse, weights, total, scale=cfg.scale)
+    kept = torch.empty((cfg.B, cfg.Hkv, KV4_BUDGET), dtype=torch.int32, device="cuda")
+    lengths = torch.empty_like(ctx)
+    qb.evict_kv4(pool, pt, ctx, total, kept, lengths, total, sinks=KV4_SINKS, recent=KV4_RECENT)
+    return out, weights, kept, lengths
+
+
 def _decode_steps(cfg, steps):
     d = syn.make_decode(cfg, device="cuda")
     d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in d.items()}
@@ -165,9 +225,10 @@ def main(argv=None):
                          "the same block-key stream per sequence")
     ap.add_argument("--impl", choices=("mma", "tcgen05"), default="mma",
                     help="prefill attention: qsa_sparse_prefill (mma.sync) or qsa_sparse_prefill_tcgen05")
-    ap.add_argument("--op", choices=("path", "rope", "handoff", "gather", "kv8"), default="path",
+    ap.add_argument("--op", choices=("path", "rope", "handoff", "gather", "kv8", "kv4"), default="path",
                     help="rope / handoff: qsa_rope_qkv / qsa_indexer_prefill_handoff of a prefill workload; "
-                         "gather: qsa_gather_selected of a decode workload; kv8: the workload's steps on an 8-bit cache")
+                         "gather: qsa_gather_selected of a decode workload; kv8 / kv4: the workload's steps on an 8-bit / 4-bit "
+                         "cache")
     args = ap.parse_args(argv)
     cfg = names[args.workload]
     if args.B is not None:
@@ -186,9 +247,9 @@ def main(argv=None):
             cfg = dataclasses.replace(cfg, ctx_lo=args.ctx, ctx_hi=args.ctx, max_ctx=max(args.ctx, 1), ctx_list=None)
         if args.Hkv is not None:
             cfg = dataclasses.replace(cfg, Hkv=args.Hkv, Hq=8 * args.Hkv)
-        (_kv8_decode_steps if args.op == "kv8" else _decode_steps)(cfg, args.steps)
-    elif args.op == "kv8":
-        _kv8_prefill_steps(cfg, args.steps)
+        {"kv8": _kv8_decode_steps, "kv4": _kv4_decode_steps}.get(args.op, _decode_steps)(cfg, args.steps)
+    elif args.op in ("kv8", "kv4"):
+        (_kv8_prefill_steps if args.op == "kv8" else _kv4_prefill_steps)(cfg, args.steps)
     else:
         _prefill_steps(cfg, args.steps, args.impl)
     torch.cuda.synchronize()

@@ -258,3 +258,17 @@ def test_a_server_run(qb, dtype):
         if turn == 24:
             cache = evict(cache)
     assert cache == [budget + 15] * 2
+
+
+def test_workload_steps_on_a_4_bit_cache(qb, capsys):
+    """run_case's 4-bit steps: finite outputs, weights that sum to the heads of a group, lengths cut to the budget."""
+    import dataclasses
+    from block_sparse_gqa_qsa_gb300 import run_case, synthetic as syn
+    dec = dataclasses.replace(next(c for c in syn.BENCH_CONFIGS if c.name.startswith("decode_B32")), B=3, ctx_lo=5000,
+                              ctx_hi=9000, max_ctx=9000)
+    out, weights, kept, lengths = run_case._kv4_decode_steps(dec, 2)
+    assert bool(torch.isfinite(out).all()) and lengths.tolist() == [run_case.KV4_BUDGET] * 3 and int(kept.min()) >= 0
+    # (a weight is off by at most 2^-15 here: logits of at most 2^5, their sums, and the exponent's units)
+    assert bool(((weights.sum(-1) - dec.Hq / dec.Hkv).abs() < 2.0 ** -10 * dec.Hq / dec.Hkv).all())
+    run_case.main(["prefill_S8192", "--op", "kv4", "--steps", "1"])
+    assert "ok: 1 steps" in capsys.readouterr().out
