@@ -358,8 +358,7 @@ qsa_status_t sparse_weights_kv4_entry(const QsaSparseWeightsKv4Params* p, const 
   if (s != QSA_OK) return s;
   if (!aligned(p->weights, 4) || !aligned(p->total, 4))
     return fail(QSA_ERR_UNSUPPORTED, "%s: weights and total must be 4-byte aligned", fn);
-  if (static_cast<long long>(p->batchSize) * p->numKVHeads > 65535)
-    return fail(QSA_ERR_UNSUPPORTED, "%s: batchSize * numKVHeads > 65535", fn);
+  if (p->totalLen > (1 << 24)) return fail(QSA_ERR_UNSUPPORTED, "%s: totalLen > %d", fn, 1 << 24);
   const cudaError_t e = qsa::launch_sparse_weights_kv4(*p, bf16);
   return e == cudaSuccess ? ok() : cuda_fail(e, fn);
 }

@@ -533,7 +533,8 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   const int sms = sm_count(), most = std::min(kMaxCluster, (a.topK + kStep * kWarps - 1) / (kStep * kWarps));
   long long least = 0;
   for (int split = 1; split <= most; ++split) {
-    if (split > 1 && pairs > resident_clusters<NT, kBf16, kLse>(split)) continue;
+    const long long resident = resident_clusters<NT, kBf16, kLse>(split);
+    if (split > 1 && pairs > resident) continue;
     const long long steps = (a.topK + kStep * kWarps * split - 1) / (kStep * kWarps * split);
     const long long cost = steps * (1 + 2 * ((pairs * split + sms - 1) / sms));
     if (split == 1 || cost <= least) {

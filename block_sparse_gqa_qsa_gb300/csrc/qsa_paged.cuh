@@ -160,7 +160,8 @@ __device__ __forceinline__ void softmax32(Acc<NT>& A, float (&s)[2][NT][4], cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float& x = s[i >> 1][nt][2 * (i & 1) + h];
-        // bf16: the K scale first (the product is below 2^31, so with scales below 2^96 only a logit itself overflows)
+        // bf16: the K scale first (the product is below 2^31, 4-bit pool 2^34, so with scales below 2^96, 2^93, only a logit
+        // itself overflows)
         x = kBf16 ? fmaf(x * ks[i], qs[nt][h], lv[i]) : fmaf(x, ks[i], lv[i]);
       }
 #pragma unroll

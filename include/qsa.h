@@ -698,7 +698,8 @@ QSA_API qsa_status_t qsa_store_kv4_bf16(const QsaStoreKv4Params* params);
  * . k_j) over the row's list, -infinity for rows t >= n and rows whose list
  * names nothing: what qsa_sparse_weights_kv4 takes.
  * Arithmetic: code * s_j enters the products exactly (fp16), the rest as in
- * qsa_sparse_paged_kv8; lse sums the unrounded probabilities in fp32.  Repeated
+ * qsa_sparse_paged_kv8 (with bf16 queries attentionScale times a K row scale
+ * stays below 2^93); lse sums the unrounded probabilities in fp32.  Repeated
  * calls give identical bits.  No workspace; calls may run concurrently. */
 typedef struct {
   const void* qPtr;              /* fp16 or bf16 [B, S, numQHeads, 128]                                   */
@@ -739,7 +740,7 @@ QSA_API qsa_status_t qsa_sparse_paged_kv4_bf16(const QsaSparsePagedKv4Params* pa
  * order of the rows).  Calls that share `total` must not run concurrently.
  * Arithmetic: products as in qsa_sparse_paged_kv4, fp32 exponentials and sums.
  * status, errors and limits as for qsa_sparse_paged_kv4; total NULL with
- * totalLen 0 counts nothing.  batchSize * numKVHeads is at most 65535. */
+ * totalLen 0 counts nothing; totalLen is at most 2^24. */
 typedef struct {
   const void* qPtr;              /* fp16 or bf16 [B, S, numQHeads, 128]                                   */
   const void* kvPool;            /* bytes [numFlatPages, 128, numKVHeads, poolRowBytes]                   */

@@ -272,3 +272,49 @@ def test_workload_steps_on_a_4_bit_cache(qb, capsys):
     assert bool(((weights.sum(-1) - dec.Hq / dec.Hkv).abs() < 2.0 ** -10 * dec.Hq / dec.Hkv).all())
     run_case.main(["prefill_S8192", "--op", "kv4", "--steps", "1"])
     assert "ok: 1 steps" in capsys.readouterr().out
+
+
+FIRST_CALL = """
+import sys; sys.path[:0] = [{root!r}, {tests!r}]
+import torch, kv4_ref as ref
+from block_sparse_gqa_qsa_gb300 import _binding as qb
+G = {group}
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+pt, flat = ref.page_tables([500, 300], 1)
+pool, pt = ref.random_pool(flat, 2, 1).cuda(), pt.cuda()
+kv = torch.randn(2, 1, 4, 128, device="cuda").half()
+q = torch.randn(2, 1, 2 * G, 128, device="cuda").half()
+ctx, pos, freq = i32([500, 300]), i32([[499], [299]]), qb.rotary_frequencies(64, theta=1e4)
+lists = torch.arange({width}, dtype=torch.int32, device="cuda").expand(2, 1, {width}).contiguous()
+out, lse, w = torch.zeros_like(q), torch.zeros(2, 1, 2 * G, device="cuda"), torch.zeros(2, 1, 2, {width}, device="cuda")
+total, kept, length = torch.zeros(2, 2, 500, device="cuda"), torch.zeros(2, 2, 200, dtype=torch.int32, device="cuda"), i32([0, 0])
+def step():
+    qb.rotary(q, pos, q, freq)
+    qb.store_kv4(kv[:, :, :2], kv[:, :, 2:], ctx, pool, pt)
+    qb.sparse_paged_kv4(q, pool, pt, lists, ctx, out, scale=0.09, lse=lse)
+    qb.sparse_weights_kv4(q, pool, pt, lists, ctx, lse, w, total, scale=0.09)
+    qb.evict_kv4(pool, pt, ctx, total, kept, length, recent=16)
+state = (q, pool, total)
+saved = [t.clone() for t in state]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay(); torch.cuda.synchronize()
+first = [t.clone() for t in (q, pool, out, lse, w, total, kept, length)]
+for t, s in zip(state, saved): t.copy_(s)
+step(); torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (q, pool, out, lse, w, total, kept, length)))
+assert length.tolist() == [200, 200] and bool(out.any()) and bool((w.sum(-1) - G).abs().max() < 1e-2 * G)
+"""
+
+
+@pytest.mark.parametrize("group,width", [(4, 100), (12, 100), (8, 290)])
+def test_first_calls_of_a_process_may_be_captured(qb, group, width):
+    """Nothing is set up by a first call that a capture would not allow."""
+    import subprocess
+    import sys
+    from conftest import ROOT
+    code = FIRST_CALL.format(root=ROOT, tests=ROOT + "/tests", group=group, width=width)
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]

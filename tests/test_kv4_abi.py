@@ -133,7 +133,7 @@ def test_attend_refusals(qb, change, want):
 @pytest.mark.parametrize("change,want", READER_REFUSALS + [
     (dict(lse=None), INVALID), (dict(weights=None), INVALID), (dict(total=None), INVALID), (dict(totalLen=0), INVALID),
     (dict(totalLen=-1), INVALID), (dict(weights=FAKE + 2), UNSUPPORTED), (dict(total=FAKE + 1), UNSUPPORTED),
-    (dict(batchSize=1 << 15), UNSUPPORTED)])
+    (dict(totalLen=(1 << 24) + 1), UNSUPPORTED)])
 def test_weights_refusals(qb, change, want):
     refuses(qb, "QsaSparseWeightsKv4Params", WEIGHTS, change, want)
 
