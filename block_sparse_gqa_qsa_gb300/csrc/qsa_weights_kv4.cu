@@ -13,9 +13,10 @@
 //
 // Totals.  With one row per sequence a token is added to once per entry that
 // names it (equal addends if twice), so the order of the atomic adds does not
-// show.  With several rows the sums go through a second kernel that walks a
-// sequence's rows in order, tokens dealt out to CTAs by ranges held in shared
-// memory: a token's addends come in the order of the rows, whatever runs first.
+// show.  With several rows the sums go through a second kernel, in which a CTA
+// owns a range of a (sequence, head)'s tokens and walks the rows in order, a
+// barrier between them: a token's atomic adds come in the order of the rows,
+// whatever runs first, and give what a call per row would.
 #include <algorithm>
 
 #include "qsa_paged_kv4.cuh"
@@ -134,10 +135,14 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
   list.report();
 }
 
-// total += the weights of a sequence's rows, in the order of the rows, for the tokens [lo, lo + range) of a (sequence, head).
+// total += the weights of a sequence's rows, one row after the other, for the tokens [lo, lo + range) of a (sequence, head).
+// Every CTA reads the rows' lists; weights only where they count.  (37 rows of 3 sequences of up to 24001 tokens: the call
+// 27.4 us, this kernel half of it, without its adds or its barriers as long; sums in shared memory, added up at the end, and
+// all weights read: 29 us.)
 constexpr int kSumThreads = 512;
-constexpr int kPer = 5;    // entries of a thread that are loaded ahead
-constexpr int kAhead = 4;  // rows that they are loaded ahead
+constexpr int kPer = 5;    // entries of a thread that are loaded ahead:
+constexpr int kLists = 4;  // rows ahead their tokens,
+constexpr int kSums = 2;   // rows ahead the weights of those in the range
 
 struct SumArgs {
   const int32_t* indices;
@@ -149,47 +154,49 @@ struct SumArgs {
 };
 
 __global__ void __launch_bounds__(kSumThreads) sum_weights_kernel(const SumArgs a) {
-  extern __shared__ float acc[];  // [range]
   const int b = blockIdx.x / a.Hkv, g = blockIdx.x - b * a.Hkv, lo = blockIdx.y * a.range;
   const int L = max(0, a.ctx[b]), n = max(0, min(a.newLen ? a.newLen[b] : a.S, min(a.S, L)));
   const int range = min(a.range, min(L, a.totalLen) - lo);
-  if (range <= 0 || n == 0) return;
-  for (int i = threadIdx.x; i < range; i += kSumThreads) acc[i] = 0.f;
+  if (range <= 0) return;
   const int32_t* list = a.indices + static_cast<size_t>(b) * a.S * a.topK;
   const float* weight = a.weights + (static_cast<size_t>(b) * a.S * a.Hkv + g) * a.topK;
   const size_t hop = static_cast<size_t>(a.Hkv) * a.topK;
-  auto add = [&](int j, float w) {  // (entries that name nothing have weight 0)
-    if (static_cast<unsigned>(j - lo) < static_cast<unsigned>(range)) atomicAdd(acc + (j - lo), w);
-  };
-  int j[kAhead][kPer];
-  float w[kAhead][kPer];
-  auto load = [&](int t, int (&jt)[kPer], float (&wt)[kPer]) {
+  float* total = a.total + (static_cast<size_t>(b) * a.Hkv + g) * a.totalLen + lo;
+  auto mine = [&](int j) { return static_cast<unsigned>(j - lo) < static_cast<unsigned>(range); };
+  int j[kLists][kPer];
+  float w[kSums][kPer];
+  auto load_tokens = [&](int t, int (&jt)[kPer]) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int e = threadIdx.x + k * kSumThreads;
-      const bool in = t < n && e < a.topK;
-      jt[k] = in ? __ldg(list + static_cast<size_t>(t) * a.topK + e) : -1;
-      wt[k] = in ? __ldg(weight + t * hop + e) : 0.f;
+      jt[k] = t < n && e < a.topK ? __ldg(list + static_cast<size_t>(t) * a.topK + e) : -1;
     }
   };
+  auto load_weights = [&](int t, const int (&jt)[kPer], float (&wt)[kPer]) {  // (those of entries that name nothing are 0)
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i, j[i], w[i]);
-  for (int t0 = 0; t0 < n; t0 += kAhead)
+    for (int k = 0; k < kPer; ++k)
+      if (mine(jt[k])) wt[k] = __ldg(weight + t * hop + threadIdx.x + k * kSumThreads);
+  };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+  for (int i = 0; i < kLists; ++i) load_tokens(i, j[i]);
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) load_weights(i, j[i], w[i]);
+  for (int t0 = 0; t0 < n; t0 += kLists)
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) {
       const int t = t0 + i;
-      __syncthreads();  // the rows before this one are in
+      __syncthreads();  // the adds of the rows before this one come first
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) add(j[i][k], w[i][k]);
-      load(t + kAhead, j[i], w[i]);
+      for (int k = 0; k < kPer; ++k)
+        if (mine(j[i][k])) atomicAdd(total + (j[i][k] - lo), w[i % kSums][k]);
+      load_tokens(t + kLists, j[i]);
+      load_weights(t + kSums, j[(i + kSums) % kLists], w[i % kSums]);
       if (t < n)
-        for (int e = threadIdx.x + kPer * kSumThreads; e < a.topK; e += kSumThreads)
-          add(__ldg(list + static_cast<size_t>(t) * a.topK + e), __ldg(weight + t * hop + e));
+        for (int e = threadIdx.x + kPer * kSumThreads; e < a.topK; e += kSumThreads) {
+          const int more = __ldg(list + static_cast<size_t>(t) * a.topK + e);
+          if (mine(more)) atomicAdd(total + (more - lo), __ldg(weight + t * hop + e));
+        }
     }
-  __syncthreads();
-  float* total = a.total + (static_cast<size_t>(b) * a.Hkv + g) * a.totalLen + lo;
-  for (int i = threadIdx.x; i < range; i += kSumThreads)
-    if (acc[i] != 0.f) total[i] += acc[i];
 }
 
 template <int NT, bool kBf16>
@@ -243,14 +250,14 @@ cudaError_t launch_sparse_weights_kv4(const QsaSparseWeightsKv4Params& p, bool b
   else
     e = a.G <= 8 ? weights_go<1, false>(w, pairs, st) : weights_go<2, false>(w, pairs, st);
   if (e != cudaSuccess || p.seqLen == 1 || !p.total) return e;
-  // Ranges of 1024 to 8192 tokens, as many as give every SM a CTA.
+  // Ranges of 1024 to 8192 tokens, as many as give every SM two CTAs.
   const long long both = static_cast<long long>(p.batchSize) * p.numKVHeads;
   long long range = (p.totalLen * both / (2LL * sm_count()) + 255) / 256 * 256;
   range = std::max(1024LL, std::min(8192LL, range));
   SumArgs s{p.indices, p.contextLengths, p.newLengths, p.weights, p.total, p.seqLen, p.numKVHeads, p.topK, p.totalLen,
             static_cast<int>(range)};
   const unsigned ranges = static_cast<unsigned>((p.totalLen + range - 1) / range);
-  sum_weights_kernel<<<dim3(static_cast<unsigned>(both), ranges), kSumThreads, range * 4, st>>>(s);
+  sum_weights_kernel<<<dim3(static_cast<unsigned>(both), ranges), kSumThreads, 0, st>>>(s);
   return cudaGetLastError();
 }
 

@@ -735,9 +735,10 @@ QSA_API qsa_status_t qsa_sparse_paged_kv4_bf16(const QsaSparsePagedKv4Params* pa
  * weights is 0 for entries that name nothing and in rows t >= n; a head whose lse is
  * -infinity adds nothing.  lse, lists and lengths are those of the attention
  * call.  A token at or past totalLen is not counted (its weights are written).
- * total is read and written once per token that the call names; repeated
- * calls on equal inputs give identical bits (a token's sum is formed in the
- * order of the rows).  Calls that share `total` must not run concurrently.
+ * A token's weights are added to its total in fp32 in the order of the rows,
+ * so that repeated calls on equal inputs give identical bits, and one call of
+ * n rows those of n calls of one row.  Calls that share `total` must not run
+ * concurrently.
  * Arithmetic: products as in qsa_sparse_paged_kv4, fp32 exponentials and sums.
  * status, errors and limits as for qsa_sparse_paged_kv4; total NULL with
  * totalLen 0 counts nothing; totalLen is at most 2^24. */

@@ -273,6 +273,28 @@ def test_attend_and_weights(qb, dtype, i):
     assert torch.equal(w3, w)
 
 
+def test_totals_are_added_row_by_row(qb):
+    """The totals of several rows are, bit for bit, fp32 additions in the order of the rows, and what a call per row gives;
+    an entry named twice adds twice."""
+    c = make(B=2, S=24, Hq=12, Hkv=2, ctx=[3000, 900], new=[24, 17], topk=900, dtype="bf16", seed=13)
+    c["lists"][0, 5, 100:120] = c["lists"][0, 5, 0:20]
+    _, lse, _ = run_attend(qb, c)
+    before = torch.rand((2, 2, 3000), generator=torch.Generator().manual_seed(3))
+    total = before.cuda()
+    w, _ = run_weights(qb, c, lse, total)
+    want, one = before.clone(), before.cuda()
+    for t in range(24):
+        for b in range(2):
+            j = c["lists"][b, t].long()
+            for e in ((j >= 0) & (j < c["ctx"][b])).nonzero().flatten().tolist() if t < c["n"][b] else []:
+                for h in range(2):
+                    want[b, h, j[e]] += w[b, t, h, e].cpu()
+        row = dict(c, q=c["q"][:, t:t + 1], lists=c["lists"][:, t:t + 1], new=[int(t < n) for n in c["n"]])
+        run_weights(qb, row, lse[:, t:t + 1].contiguous(), one)
+    assert torch.equal(total.cpu(), want)
+    assert torch.equal(one, total)
+
+
 def test_totals_shorter_than_the_cache(qb):
     """Tokens at or past totalLen are not counted; nothing behind the array is written."""
     for S in (1, 6):
