@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_weights_kernel(const SumArgs 
   const float* weight = a.weights + (static_cast<size_t>(b) * a.S * a.Hkv + g) * a.topK;
   const size_t hop = static_cast<size_t>(a.Hkv) * a.topK;
   float* total = a.total + (static_cast<size_t>(b) * a.Hkv + g) * a.totalLen + lo;
-  auto mine = [&](int j) { return static_cast<unsigned>(j - lo) < static_cast<unsigned>(range); };
+  auto mine = [&](int j) { return static_cast<unsigned>(j) - static_cast<unsigned>(lo) < static_cast<unsigned>(range); };
   int j[kLists][kPer];
   float w[kSums][kPer];
   auto load_tokens = [&](int t, int (&jt)[kPer]) {
