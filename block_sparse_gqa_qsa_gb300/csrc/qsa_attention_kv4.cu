@@ -244,13 +244,14 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
   slot += hop;
   int j3 = list.at(slot);
   const uint32_t queries = smem_addr(smem + kWarps * kWarpBytes);
-  float qs[NT][2];  // (every warp writes the same queries)
-  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, queries, qs);
+  float qs[NT][2];
+  kv4_load_q<NT, kBf16, true>(static_cast<const uint4*>(a.q) + r.head0 * (kD / 8), a.G, queries, qs);
   unsigned next = resolve(p1, 1);
   p1 = list.pages_of(j2);
   __syncwarp();
   gather_keys(1, next);
   gather_values(1, next);
+  __syncthreads();  // the queries are in place
   for (int i = 0; i < steps; ++i) {
     const int par = i & 1;
     const uint32_t at = set + par * kSetBytes;
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>) sparse_paged_kv4_row
   Pages p1 = list.pages_of(j1);
   const uint32_t queries = set + kRowsQueriesAt;
   float qs[NT][2];
-  kv4_load_q<NT, kBf16>(static_cast<const uint4*>(a.q) + (r.head0 + warp * a.G) * (kD / 8), a.G, queries, qs);
+  kv4_load_q<NT, kBf16, false>(static_cast<const uint4*>(a.q) + (r.head0 + warp * a.G) * (kD / 8), a.G, queries, qs);
   __syncthreads();
   unsigned mask = masks[0];  // of the current step, whose rows are gathered
   gather_k(ids_of(0, 0), mask, dst, 0, base, rowBytes);

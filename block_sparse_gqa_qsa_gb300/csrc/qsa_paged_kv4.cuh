@@ -101,25 +101,32 @@ __device__ __forceinline__ void kv4_scores(float (&s)[2][NT][4], uint32_t codes,
   }
 }
 
-// Puts the group's queries at `queries` (a warp's work, seen by the warp after a __syncwarp): k-step w of a lane covers dims
-// 32 q + 4 w .. + 3, as the K codes do.  bf16 values are scaled by a power of two per head to fp16's upper range; qs gets
-// its inverse for the lane's heads 2 q, 2 q + 1.
-template <int NT, bool kBf16>
+// Puts the group's queries at `queries`: k-step w of a lane covers dims 32 q + 4 w .. + 3, as the K codes do.  bf16 values are
+// scaled by a power of two per head to fp16's upper range; qs gets its inverse for the lane's heads 2 q, 2 q + 1.
+// kShared: the CTA's four warps put a quarter each, all of them before a __syncthreads; otherwise a warp puts its own, before
+// a __syncwarp.
+template <int NT, bool kBf16, bool kShared>
 __device__ __forceinline__ void kv4_load_q(const uint4* q, int G, uint32_t queries, float (&qs)[NT][2]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, mine = kShared ? threadIdx.x >> 5 : 0;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int h = 8 * nt + g;
+    const uint4* src = q + h * (kD / 8) + 4 * c;
+    // 16 bytes i hold dims 32 c + 8 i .. + 7: k-steps 2 i and 2 i + 1, two words each
+    auto piece = [&](int i) { return h < G ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
     uint4 raw[4];
+    if constexpr (kBf16 || !kShared) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = h < G ? __ldg(q + h * (kD / 8) + 4 * c + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i) raw[i] = piece(i);
+    }
     float up = 1.f, down = 1.f;
     if constexpr (kBf16) {
       uint32_t m = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) m = max(m, max(word(raw[i], w) & 0x7fff, (word(raw[i], w) >> 16) & 0x7fff));
+        for (int w = 0; w < 4; ++w) m = __vmaxu2(m, word(raw[i], w) & 0x7fff7fff);
+      m = max(m & 0xffff, m >> 16);
       m = max(m, __shfl_xor_sync(kFull, m, 1));
       m = max(m, __shfl_xor_sync(kFull, m, 2));
       // exponent e of the largest: scaled by 2^(14 - e), or 2^114 where that is less, so that the inverse is a normal
@@ -131,17 +138,24 @@ __device__ __forceinline__ void kv4_load_q(const uint4* q, int G, uint32_t queri
         down = __int_as_float((127 - k) << 23);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // 16 bytes i hold dims 32 c + 8 i .. + 7: k-steps 2 i and 2 i + 1, two words each
+    auto put = [&](int i, const uint4& r) {
       uint32_t v[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        v[w] = word(raw[i], w);
+        v[w] = word(r, w);
         if constexpr (kBf16) v[w] = pack_half2(__uint_as_float(v[w] << 16) * up, __uint_as_float(v[w] & 0xffff0000u) * up);
       }
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(queries + ((4 * nt + i) * 32 + lane) * 16), "r"(v[0]),
                    "r"(v[1]), "r"(v[2]), "r"(v[3])
                    : "memory");
+    };
+    if constexpr (!kShared) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) put(i, raw[i]);
+    } else if constexpr (kBf16) {
+      put(mine, mine == 0 ? raw[0] : mine == 1 ? raw[1] : mine == 2 ? raw[2] : raw[3]);
+    } else {
+      put(mine, piece(mine));
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) qs[nt][j] = __shfl_sync(kFull, down, 4 * (2 * c + j));
