@@ -143,9 +143,10 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
 }
 
 // total += the weights of a sequence's rows, one row after the other, for the tokens [lo, lo + range) of a (sequence, head).
-// Every CTA reads the rows' lists; weights only where they count.  (37 rows of 3 sequences of up to 24001 tokens: the call
-// 27.4 us, this kernel half of it, without its adds or its barriers as long; sums in shared memory, added up at the end, and
-// all weights read: 29 us.)
+// Every CTA reads the rows' lists; weights only where they count.  What bounds it is looking at every entry (37 rows of 3
+// sequences of up to 24001 tokens: the call 24.7 us, this kernel about 11 of it, half of all issue slots busy, without its
+// adds or its barriers as long).  Sums in shared memory, added up at the end, and all weights read: 29 us for 27.4 then;
+// batches of two or four rows, loaded and added in turn: the same; branches around entries past the list: 38.
 constexpr int kSumThreads = 512;
 constexpr int kPer = 5;    // entries of a thread that are loaded ahead:
 constexpr int kLists = 4;  // rows ahead their tokens,
