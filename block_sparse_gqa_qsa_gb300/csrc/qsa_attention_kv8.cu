@@ -575,7 +575,7 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   // A warp per pair from two waves of such CTAs on: 2 x 700 rows of 4 heads (2.3 waves) took 202 us instead of 224, 2 x 350
   // (1.2 waves) 146 instead of 127.  With 2 heads 4096 rows (3.4 waves) 294 instead of 301, 8192 618 instead of 657, 12
   // query heads each 887 instead of 987, but 1100 + 1100 rows (1.8 waves) 213 instead of 198.  (All taken
-  // before the sums' weights were rounded too, which adds 1 to 3 % to either form: 202 is 205 now, 618 626, 887 911.  Two
+  // before the sums' weights were rounded too and the maximum formed only when it moves: 202 is 198 now, 618 605, 887 872.  Two
   // warps per pair, four heads: 223 us where one took 223.  Lists of their own per warp, for odd numbers of heads: 406 us
   // where the split form took 332, 8192 rows of one head.)
   if (a.Hkv % 2 == 0 && pairs / kWarps >= 2 * slots)

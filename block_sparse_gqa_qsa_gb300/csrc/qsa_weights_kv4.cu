@@ -143,10 +143,11 @@ __global__ void __launch_bounds__(kThreads) sparse_weights_kv4_kernel(const Weig
 }
 
 // total += the weights of a sequence's rows, one row after the other, for the tokens [lo, lo + range) of a (sequence, head).
-// Every CTA reads the rows' lists; weights only where they count.  What bounds it is looking at every entry (37 rows of 3
-// sequences of up to 24001 tokens: the call 24.7 us, this kernel about 11 of it, half of all issue slots busy, without its
-// adds or its barriers as long).  Sums in shared memory, added up at the end, and all weights read: 29 us for 27.4 then;
-// batches of two or four rows, loaded and added in turn: the same; branches around entries past the list: 38.
+// Every CTA reads the rows' lists; weights only where they count.  What bounds it is a row's chain of instructions from one
+// barrier to the next, 0.3 us (37 rows of 3 sequences of up to 24001 tokens: the call 24.7 us, this kernel 13 of it, issue
+// slots 38 % busy; more rows on their way, in registers or through shared memory, change nothing).  A tile of rows x tokens,
+// filled by asynchronous copies and added column by column, took 24.4 us for that call and 25 instead of 31 for 64 rows of a
+// sequence of 8000 tokens, but 84 instead of 37 for 4 rows of each of 32 sequences of 65536.
 constexpr int kSumThreads = 512;
 constexpr int kPer = 5;    // entries of a thread that are loaded ahead:
 constexpr int kLists = 4;  // rows ahead their tokens,
