@@ -26,7 +26,7 @@ namespace qsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVectors = 4;  // of a thread in flight
+constexpr int kVectors = 4;  // of a thread in flight, of 16 bytes
 constexpr int kMostHeads = 8;  // of a thread (with 4 and two vectors in flight 81 us instead of 54)
 
 struct RotaryArgs {
@@ -36,7 +36,7 @@ struct RotaryArgs {
   long long xToken, xHead, yToken, yHead;  // elements
   int tokens, heads, rot;
   int rotVectors, copyVectors;  // per head: vectors (or pairs of vectors) that turn; vectors that are copied
-  int copyBytes;                // of the latter: 16, or V elements
+  int copyBytes;                // of the latter
   int headGroups;               // threads that share a (token, vector): thread g takes heads g, g + headGroups, ..
   int ctaTokens, ctaGroups;     // of a CTA
   float magnitude;
@@ -89,11 +89,12 @@ __device__ __forceinline__ void copy_heads(const T* x, T* y, int at, long long x
 // kInter: pairs (2i, 2i + 1), else (i, i + rot / 2).  V elements a vector; interleaved with V = 1 a vector is one pair's
 // two elements, read one by one.
 template <typename T, int V, bool kInter>
-__global__ void __launch_bounds__(kThreads, kInter ? 5 : 4) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, kInter && V * sizeof(T) == 16 ? 5 : 4) rotary_kernel(const RotaryArgs a) {
   constexpr bool kSingle = kInter && V == 1;
   constexpr bool kTwo = !kInter || kSingle;            // a unit is two vectors
   constexpr int kPairs = kInter ? (V == 1 ? 1 : V / 2) : V;
-  constexpr int kBatch = kTwo ? kVectors / 2 : kVectors;  // heads in flight
+  constexpr int kFlight = V * sizeof(T) == 16 ? kVectors : 2 * kVectors;  // (8-byte vectors: 20.2 us with 4, 19.2 with 8)
+  constexpr int kBatch = kTwo ? kFlight / 2 : kFlight;  // heads in flight
   using Vector = Vec<T, V>;
   extern __shared__ float2 table[];  // [ctaTokens][rot / 2] cosine, sine, times the magnitude
   const int token0 = blockIdx.x * a.ctaTokens, g0 = blockIdx.y * a.ctaGroups, pairs = a.rot >> 1;
@@ -178,10 +179,14 @@ __global__ void __launch_bounds__(kThreads, kInter ? 5 : 4) rotary_kernel(const 
     if (token0 + tt >= a.tokens || gg >= a.headGroups || __ldg(a.positions + token0 + tt) < 0) continue;
     const T* from = row(static_cast<const T*>(a.x), a.xToken, a.xHead, tt, gg) + a.rot;
     T* to = row(static_cast<T*>(a.y), a.yToken, a.yHead, tt, gg) + a.rot;
-    if (V * sizeof(T) < 16 && a.copyBytes == 16)
+    if (a.copyBytes == 16)
       copy_heads<uint4>(from, to, v, xHop, yHop, gg, a.heads, a.headGroups);
+    else if (a.copyBytes == 8)
+      copy_heads<uint2>(from, to, v, xHop, yHop, gg, a.heads, a.headGroups);
+    else if (sizeof(T) == 4 || a.copyBytes == 4)
+      copy_heads<uint32_t>(from, to, v, xHop, yHop, gg, a.heads, a.headGroups);
     else
-      copy_heads<Vector>(from, to, v, xHop, yHop, gg, a.heads, a.headGroups);
+      copy_heads<uint16_t>(from, to, v, xHop, yHop, gg, a.heads, a.headGroups);
   }
 }
 
@@ -208,11 +213,11 @@ cudaError_t rotary_go(const QsaRotaryParams& p, const RotaryTurns& rt) {
   a.heads = p.numHeads;
   a.rot = p.rotDim;
   a.rotVectors = p.interleaved && V > 1 ? p.rotDim / V : p.rotDim / 2 / V;
-  constexpr int kWide = 16 / sizeof(T);
   const int rest = p.x == p.y ? 0 : p.headDim - p.rotDim;
-  const bool wide = rest % kWide == 0 && p.rotDim % kWide == 0 && lies_on(p, kWide, sizeof(T));
-  a.copyBytes = wide ? 16 : V * sizeof(T);
-  a.copyVectors = rest * static_cast<int>(sizeof(T)) / a.copyBytes;
+  int wide = 16 / sizeof(T);  // elements of a copied vector
+  while (wide > 1 && (rest % wide || p.rotDim % wide || !lies_on(p, wide, sizeof(T)))) wide /= 2;
+  a.copyBytes = wide * sizeof(T);
+  a.copyVectors = rest / wide;
   a.magnitude = p.magnitude;
   a.inverse = p.inverse != 0;
   std::copy(rt.turn, rt.turn + kRotaryMaxPairs, a.turn);
@@ -233,10 +238,9 @@ cudaError_t rotary_go(const QsaRotaryParams& p, const RotaryTurns& rt) {
   return cudaGetLastError();
 }
 
-// Whether vectors of v elements cut every rotated half (pair row) and every row's rest, at aligned addresses.
+// Whether vectors of v elements cut every rotated half (pair row), at aligned addresses.
 bool fits(const QsaRotaryParams& p, int v, size_t size) {
-  const int piece = p.interleaved ? p.rotDim : p.rotDim / 2;
-  return piece % v == 0 && (p.x == p.y || (p.headDim - p.rotDim) % v == 0) && lies_on(p, v, size);
+  return (p.interleaved ? p.rotDim : p.rotDim / 2) % v == 0 && lies_on(p, v, size);
 }
 
 template <typename T>
