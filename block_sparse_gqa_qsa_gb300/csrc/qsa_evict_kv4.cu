@@ -383,9 +383,10 @@ cudaError_t launch_evict_kv4(const QsaEvictKv4Params& p) {
   a.sinks = p.sinks;
   a.recent = p.recent;
   const long long pairs = static_cast<long long>(p.batchSize) * p.numKVHeads;
-  // As many CTAs per (sequence, head) as leave all clusters resident at once, with at least 1024 tokens each.
+  // As many CTAs per (sequence, head) as leave all clusters resident at once, with about 512 tokens each at least (1 x 2 heads
+  // of 900 tokens 11.7 us, 2 x 4 of 4000 cut to 3500 15.3; with 1024 tokens 14.1 and 18.6, with 256 11.6 and 15.5).
   a.cluster = kMostCluster;
-  while (a.cluster > 1 && ((a.cluster - 1) * 1024LL >= p.totalLen || pairs > resident_clusters(a.cluster))) --a.cluster;
+  while (a.cluster > 1 && ((a.cluster - 1) * 512LL >= p.totalLen || pairs > resident_clusters(a.cluster))) --a.cluster;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = config(pairs, a.cluster, static_cast<cudaStream_t>(p.stream), &at);
   // (the attributes are the context's: set with every launch, which costs less than asking whether they are)

@@ -54,7 +54,8 @@ def inputs(dtype, T, H, D, seed, hi=70000):
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("T,H,D,rot", [(1, 1, 64, 64), (37, 5, 128, 64), (3, 40, 96, 36), (130, 3, 128, 128), (7, 2, 256, 256),
-                                       (11, 4, 80, 2), (9, 3, 66, 34), (5, 2, 20, 12), (600, 36, 128, 64)])
+                                       (11, 4, 80, 2), (9, 3, 66, 34), (5, 2, 20, 12), (600, 36, 128, 64),
+                                       (6, 3, 65, 64), (400, 9, 81, 20), (5, 65, 84, 20)])
 def test_rotary(qb, dtype, interleaved, T, H, D, rot):
     freq = qb.rotary_frequencies(rot, theta=1e4)
     x, pos = inputs(dtype, T, H, D, T + H)
