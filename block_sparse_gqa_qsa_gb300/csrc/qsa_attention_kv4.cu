@@ -319,29 +319,38 @@ __global__ void __launch_bounds__(kThreads, kSplitCtasPerSm<NT>) sparse_paged_kv
   cluster_sync_all();
   const uint32_t ocAddr = smem_addr(oc), mcAddr = smem_addr(mc);
   for (int h = rank * kWarps + warp; h < a.G; h += a.split * kWarps) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ms[kMaxCluster], M = -FLT_MAX, sum = 0.f, exact = 0.f;
+    // all CTAs' parts on their way at once (with a meeting below that waits for the writes of o, 0.3 us more)
+    float4 x[kMaxCluster];
+    float ms[kMaxCluster], part[kMaxCluster], whole[kMaxCluster];
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c) {
-      ms[c] = c < a.split ? cluster_ld(cluster_addr(mcAddr + h * 4, c)) : -FLT_MAX;
-      M = fmaxf(M, ms[c]);
+      ms[c] = -FLT_MAX;
+      if (c < a.split) {
+        ms[c] = cluster_ld(cluster_addr(mcAddr + h * 4, c));
+        part[c] = cluster_ld(cluster_addr(mcAddr + (H + h) * 4, c));
+        if constexpr (kLse) whole[c] = cluster_ld(cluster_addr(mcAddr + (2 * H + h) * 4, c));
+        x[c] = cluster_ld4(cluster_addr(ocAddr + (h * kPad + 4 * lane) * 4, c));
+      }
     }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -FLT_MAX, sum = 0.f, exact = 0.f;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, ms[c]);
 #pragma unroll
     for (int c = 0; c < kMaxCluster; ++c)
       if (c < a.split) {
         const float f = exp2f(ms[c] - M);
-        const float4 x = cluster_ld4(cluster_addr(ocAddr + (h * kPad + 4 * lane) * 4, c));
-        sum += f * cluster_ld(cluster_addr(mcAddr + (H + h) * 4, c));
-        if constexpr (kLse) exact += f * cluster_ld(cluster_addr(mcAddr + (2 * H + h) * 4, c));
-        o.x += f * x.x;
-        o.y += f * x.y;
-        o.z += f * x.z;
-        o.w += f * x.w;
+        sum += f * part[c];
+        if constexpr (kLse) exact += f * whole[c];
+        o.x += f * x[c].x;
+        o.y += f * x[c].y;
+        o.z += f * x[c].z;
+        o.w += f * x[c].w;
       }
     out[h * 32 + lane] = normalised<kBf16>(o, sum);
     if (kLse && lane == 0) a.lse[r.head0 + h] = lse_of(M, exact);
   }
-  cluster_sync_all();  // no CTA leaves while another reads its shared memory
+  cluster_meet();  // no CTA leaves while another reads its shared memory
 }
 
 // Many rows: a CTA takes four KV heads of a row, each warp one of them and the whole list.  The heads share the list, so the

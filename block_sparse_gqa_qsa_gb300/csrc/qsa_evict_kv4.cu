@@ -82,12 +82,6 @@ __device__ __forceinline__ int cluster_ld_int(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];\n" : "=r"(v) : "r"(addr));
   return v;
 }
-// A meeting of the cluster's threads that waits for no write: what a thread has read stays read, and what the moves write
-// is not read again in this kernel.  (A releasing arrival waits for the round before's rows to be written.)
-__device__ __forceinline__ void cluster_meet() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
-}
-
 __global__ void __launch_bounds__(kThreads, 1) evict_kv4_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);

@@ -42,6 +42,11 @@ __device__ __forceinline__ float ex2_ftz(float x) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+// A meeting of the cluster's threads that waits for no write: what a thread has read stays read, and nothing that one of them
+// writes before it is read behind it.  (A releasing arrival waits for the thread's global writes.)
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
+}
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
