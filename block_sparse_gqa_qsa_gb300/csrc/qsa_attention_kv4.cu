@@ -537,7 +537,7 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
   if (a.Hkv % kWarps == 0 && ((10 * rowCtas >= 9 * slots && rowCtas <= slots) || 10 * rowCtas >= 16 * slots))
     return rows_go<NT, kBf16, kLse || (kBf16 && NT == 1)>(a, pairs, st);
   // Otherwise 1 to 8 CTAs per pair, all clusters resident at once, at most one CTA per 128 entries of the list: those that cost
-  // least, in units of 0.28 us: 1 + 2 CTAs of an SM for each of a warp's steps, 4 for the join, 3 for a third CTA on an SM.
+  // least, in units of 0.28 us: 1 + 2 CTAs of an SM for each of a warp's steps, 4 for the join, 4 for a third CTA on an SM.
   // (us by CTAs per pair: 128 pairs with lists of 2051 17.7, 16.3, 17.3 with 1, 2, 3, of 1027 11.2, 11.4, 11.9, of 259 5.6, 6.8,
   // 7.6; 64 pairs, 2051, 18.4, 13.0, 13.2, 12.2, 14.1, 11.9 with 1 to 6; 32 pairs, 1027, 11.9, 9.4, 7.5, 7.7, 8.1, 8.2; 192
   // pairs, 2051, 27.7, 22.6, 259 8.4, 8.8.  A count that leaves clusters waiting costs a fifth more at least.)
@@ -548,8 +548,8 @@ cudaError_t paged_go(PagedArgs a, long long pairs, cudaStream_t st) {
     if (split > 1 && pairs > resident) continue;
     const long long steps = (a.topK + kStep * kWarps * split - 1) / (kStep * kWarps * split);
     const long long ctas = (pairs * split + sms - 1) / sms;  // of an SM
-    const long long cost = steps * (1 + 2 * ctas) + (split > 1 ? 4 : 0) + (ctas > 2 ? 3 : 0);
-    if (split == 1 || cost < least) {
+    const long long cost = steps * (1 + 2 * ctas) + (split > 1 ? 4 : 0) + (ctas > 2 ? 4 : 0);
+    if (split == 1 || cost <= least) {  // (equal ones: with more CTAs fewer warps have the most steps)
       least = cost;
       a.split = split;
     }
