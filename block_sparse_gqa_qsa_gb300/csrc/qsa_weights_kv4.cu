@@ -212,8 +212,8 @@ template <int NT, bool kBf16>
 cudaError_t weights_go(WeightArgs w, unsigned pairs, cudaStream_t st) {
   // Two steps a warp (one on its way while the other is computed) where that gives every SM the warps it holds (7 CTAs;
   // larger groups 5, and a few more for rows that end early); more where there are more pairs, so that one wave does (64
-  // sequences of 4 heads 14.1 us, 15.6 with two steps; 200 42.8, 44.6 with 10 instead of 13), up to 16 (2000 rows 916 us,
-  // with 32 935).
+  // sequences of 4 heads 14.1 us with 4 steps, 15.6 with 5; 200 42.8 with 13, 44.6 with 16), up to 16 (2000 rows 916 us, with
+  // 32 935).
   const long long steps = (w.a.topK + kStep - 1) / kStep, warps = (NT == 1 ? 28LL : 24LL) * sm_count();
   long long per = std::max(2LL, std::min(16LL, (pairs * steps + warps - 1) / warps));
   per = std::max(per, (steps + 32767) / 32768);
