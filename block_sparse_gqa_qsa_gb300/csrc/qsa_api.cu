@@ -267,7 +267,8 @@ qsa_status_t rotary_entry(const QsaRotaryParams* p, const char* fn, int elem) {
   if (static_cast<long long>(p->numTokens) * p->numHeads > 0x7fffffffLL ||
       static_cast<long long>(p->numTokens) * p->numHeads * p->headDim > 0x7fffffffLL)
     return fail(QSA_ERR_UNSUPPORTED, "%s: numTokens * numHeads * headDim must stay below 2^31", fn);
-  if (p->numHeads > 65535) return fail(QSA_ERR_UNSUPPORTED, "%s: numHeads %d > 65535", fn, p->numHeads);
+  if (p->numHeads > 65535 || p->headDim > 65535)
+    return fail(QSA_ERR_UNSUPPORTED, "%s: numHeads %d or headDim %d > 65535", fn, p->numHeads, p->headDim);
   qsa::RotaryTurns rt;
   for (int i = 0; i < p->rotDim / 2; ++i) {
     double x = p->invFreq[i] / 6.283185307179586;

@@ -584,8 +584,8 @@ QSA_API qsa_status_t qsa_sparse_paged_kv8_bf16(const QsaSparsePagedKv8Params* pa
  * or > headDim, a negative stride, strides of y under which two of its rows
  * overlap, x == y with different strides, a magnitude or frequency that is not
  * finite; QSA_ERR_UNSUPPORTED for rotDim > 256, a tensor not aligned to its
- * element (positions: 4), numHeads > 65535, or numTokens * numHeads * headDim
- * of 2^31 or more.
+ * element (positions: 4), numHeads or headDim > 65535, or numTokens *
+ * numHeads * headDim of 2^31 or more.
  * Nothing is allocated; invFreq is read before the call returns. */
 typedef struct {
   const void* x;                 /* [numTokens, numHeads, headDim], by the strides below                  */

@@ -94,7 +94,8 @@ NAN_FREQ = (ctypes.c_double * 32)(*([float("nan")] * 32))
     (dict(y=FAKE, xTokenStride=2048), INVALID), (dict(magnitude=float("inf")), INVALID),
     (dict(invFreq=ctypes.addressof(NAN_FREQ)), INVALID), (dict(headDim=320, rotDim=320, yTokenStride=2560, yHeadStride=320), UNSUPPORTED),
     (dict(x=FAKE + 1), UNSUPPORTED), (dict(y=FAKE + 1), UNSUPPORTED), (dict(positions=FAKE + 2), UNSUPPORTED),
-    (dict(numTokens=1, numHeads=1 << 16), UNSUPPORTED), (dict(numTokens=1 << 21), UNSUPPORTED), (dict(numTokens=1 << 30, numHeads=1 << 30, yHeadStride=1 << 8, yTokenStride=1 << 38), UNSUPPORTED)])
+    (dict(numTokens=1, numHeads=1 << 16), UNSUPPORTED),
+    (dict(numTokens=1, numHeads=1, headDim=1 << 16), UNSUPPORTED), (dict(numTokens=1 << 21), UNSUPPORTED), (dict(numTokens=1 << 30, numHeads=1 << 30, yHeadStride=1 << 8, yTokenStride=1 << 38), UNSUPPORTED)])
 def test_rotary_refusals(qb, change, want):
     refuses(qb, "QsaRotaryParams", ROTARY, change, want)
 
