@@ -661,11 +661,16 @@ def rotary(x, positions, out, inv_freq, *, interleaved=False, inverse=False, mag
     """qsa_rotary (fp16), qsa_rotary_bf16 or qsa_rotary_f32: the heads of x [tokens, heads, D] or [B, S, heads, D] turned
     by positions int32 [tokens] or [B, S] (negative: padding, left alone) into out, which may be x.  inv_freq: rot/2
     angles per position, float64 on the host (see rotary_frequencies).  x and out may be views whose rows are contiguous.
-    The gradient is the same call with inverse=True."""
+    The gradient is the same call with inverse=True.  The call itself records nothing for autograd: with gradients enabled,
+    an x or out that requires one is refused (an autograd.Function around the two calls is what a model uses); out counts as
+    changed in place, so that a backward pass that had saved it raises."""
     et = x.dtype
     fn = _ROTARY_FN.get(et)
     if fn is None:
         raise ValueError("rotary: x must be float16, bfloat16 or float32")
+    if torch.is_grad_enabled() and (x.requires_grad or out.requires_grad):
+        raise ValueError("rotary: no gradient flows through the call: x and out must not require one (the gradient of x is "
+                         "the call with inverse=True on that of out)")
     shape, xs, ys, pairs = x.shape, x.stride(), out.stride(), inv_freq.shape
     if len(shape) not in (3, 4) or out.shape != shape or positions.shape != shape[:-2]:
         raise ValueError("rotary: x and out are [tokens, heads, D] or [B, S, heads, D], positions [tokens] or [B, S]")
@@ -686,6 +691,8 @@ def rotary(x, positions, out, inv_freq, *, interleaved=False, inverse=False, mag
         interleaved, inverse, magnitude, _raw_stream(stream, dev)))
     if r:
         _check(r)
+    if not out.is_inference():
+        torch.autograd.graph.increment_version(out)
 
 
 # -------------------------------------------------------------- 4-bit cache

@@ -183,3 +183,44 @@ def test_another_stream_and_a_graph(qb):
         graph.replay()
         torch.cuda.synchronize()
         check(out, y, size, torch.bfloat16)
+
+
+def test_autograd(qb):
+    """A Function around the call and its inverse has the formula's gradient; a tensor that a backward pass has saved and the
+    call overwrites makes that pass raise, whether the call was made with gradients enabled or not."""
+    freq = qb.rotary_frequencies(48, theta=1e4)
+    x, pos = inputs("fp32", 6, 2, 64, 4)
+    dy, _ = inputs("fp32", 6, 2, 64, 5)
+
+    class Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            y = torch.empty_like(x)
+            qb.rotary(x, pos, y, freq, magnitude=0.75)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            dx = torch.empty_like(dy)
+            qb.rotary(dy, pos, dx, freq, inverse=True, magnitude=0.75)
+            return dx
+
+    leaf = x.clone().requires_grad_()
+    y = Rotary.apply(leaf)
+    check(y.detach(), *turned(x, pos, freq, magnitude=0.75), torch.float32, 0.75)
+    y.backward(dy)
+    check(leaf.grad, *turned(dy, pos, freq, inverse=True, magnitude=0.75), torch.float32, 0.75)
+    with pytest.raises(ValueError, match="gradient"):
+        qb.rotary(leaf, pos, torch.empty_like(x), freq)
+    for enabled in (True, False):
+        w, seen = torch.ones_like(x).requires_grad_(), x.clone()
+        loss = (w * seen).sum()
+        with torch.set_grad_enabled(enabled):
+            qb.rotary(seen[:, :1], pos, seen[:, :1], freq)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():  # such tensors have no version
+        frozen = x.clone()
+    qb.rotary(frozen, pos, frozen, freq)
+    qb.rotary(x, pos, x, freq)
+    assert torch.equal(frozen, x)

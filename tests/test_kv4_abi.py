@@ -231,3 +231,18 @@ def test_binding_refuses(qb):
         for change in bad:
             with pytest.raises(ValueError):
                 call(**change)
+
+
+def test_rotary_refuses_what_autograd_would_lose(qb):
+    """The call records nothing: a tensor whose gradient would be dropped without a word is refused, in place or not; with
+    gradients disabled it goes on (here to the next check, the device's)."""
+    x, pos, f = torch.zeros(5, 3, 64), torch.zeros(5, dtype=torch.int32), torch.ones(16, dtype=torch.float64)
+    leaf = x.clone().requires_grad_()
+    computed = leaf * 2
+    for a, out in ((leaf, x), (computed, x), (computed, computed), (computed[:, :2], x[:, :2]), (x, leaf), (x, computed)):
+        with pytest.raises(ValueError, match="gradient"):
+            qb.rotary(a, pos, out, f)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+            qb.rotary(a, pos, out, f)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        qb.rotary(computed.detach(), pos, x, f)
