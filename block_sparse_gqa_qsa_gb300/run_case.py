@@ -20,7 +20,7 @@ qsa_gather_selected into contiguous scratch per step.  `--op kv8` runs a
 workload's steps on an 8-bit cache: qsa_append_kv8 (the whole prompts, or one
 token per sequence), the indexer, and qsa_sparse_paged_kv8 over its lists; a
 decode keeps the indexer's fp16 state in a one-head pool on the same page table.
-`--op kv4` runs them on a 4-bit cache: qsa_rotary in the packed projections,
+`--op kv4` runs them on a 4-bit cache: qsa_rotary of the packed projections,
 qsa_store_kv4, the indexer and qsa_sparse_paged_kv4; a decode step also gathers
 its tokens' attention weights (qsa_sparse_weights_kv4), and behind the last step
 qsa_evict_kv4 cuts every sequence back to 4096 tokens.
@@ -153,16 +153,18 @@ def _kv4_prefill_steps(cfg, steps):
     row = torch.arange(cfg.S, dtype=torch.int32, device="cuda")
     pos = torch.where(row < t["ctx"][:, None], row, torch.full_like(row, -1))
     freq = qb.rotary_frequencies(cfg.rot, theta=cfg.theta)
-    qk, k, v = qkv[:, :, :cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq:cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq + cfg.Hkv:]
+    # every step turns the projections as they were (in place, a second step would turn them twice)
+    turned = torch.zeros_like(qkv[:, :, :cfg.Hq + cfg.Hkv])
+    qk, k, v = qkv[:, :, :cfg.Hq + cfg.Hkv], turned[:, :, cfg.Hq:], qkv[:, :, cfg.Hq + cfg.Hkv:]
     ws = qb.alloc_workspace(qb.indexer_prefill_workspace_size(cfg.B, cfg.S, cfg.di, cfg.ratio))
     ind = torch.empty((cfg.B, cfg.S, cfg.topK), dtype=torch.int32, device="cuda")
     out = torch.empty((cfg.B, cfg.S, cfg.Hq, cfg.D), dtype=torch.float16, device="cuda")
     for _ in range(steps):
-        qb.rotary(qk, pos, qk, freq)
+        qb.rotary(qk, pos, turned, freq)
         qb.store_kv4(k, v, t["ctx"], pool, pt)
         qb.indexer_prefill(t["idxQ"], t["idxK"], t["wq"], t["wk"], t["ctx"], ind, ws, rot=cfg.rot, ratio=cfg.ratio,
                            budget=cfg.budget, topK=cfg.topK, theta=cfg.theta, eps=cfg.eps)
-        qb.sparse_paged_kv4(qkv[:, :, :cfg.Hq].contiguous(), pool, pt, ind, t["ctx"], out, scale=cfg.scale)
+        qb.sparse_paged_kv4(turned[:, :, :cfg.Hq].contiguous(), pool, pt, ind, t["ctx"], out, scale=cfg.scale)
     return out, pool
 
 
@@ -174,7 +176,9 @@ def _kv4_decode_steps(cfg, steps):
     qkv = torch.randn((cfg.B, 1, cfg.Hq + 2 * cfg.Hkv, cfg.D), device="cuda").half()
     pos = (ctx - 1).view(cfg.B, 1)
     freq = qb.rotary_frequencies(cfg.rot, theta=cfg.theta)
-    qk, k, v = qkv[:, :, :cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq:cfg.Hq + cfg.Hkv], qkv[:, :, cfg.Hq + cfg.Hkv:]
+    # every step turns the projections as they were (in place, a second step would turn them twice)
+    turned = torch.zeros_like(qkv[:, :, :cfg.Hq + cfg.Hkv])
+    qk, k, v = qkv[:, :, :cfg.Hq + cfg.Hkv], turned[:, :, cfg.Hq:], qkv[:, :, cfg.Hq + cfg.Hkv:]
     ws = qb.alloc_workspace(qb.indexer_decode_workspace_size(cfg.B, cfg.maxPagesPerSeq, cfg.ratio, cfg.budget))
     ind = torch.empty((cfg.B, 1, cfg.topK), dtype=torch.int32, device="cuda")
     out = torch.empty((cfg.B, 1, cfg.Hq, cfg.D), dtype=torch.float16, device="cuda")
@@ -182,11 +186,11 @@ def _kv4_decode_steps(cfg, steps):
     weights = torch.empty((cfg.B, 1, cfg.Hkv, cfg.topK), device="cuda")
     total = torch.zeros((cfg.B, cfg.Hkv, syn.TOKENS_PER_PAGE * cfg.maxPagesPerSeq), device="cuda")
     for _ in range(steps):
-        qb.rotary(qk, pos, qk, freq)
+        qb.rotary(qk, pos, turned, freq)
         qb.store_kv4(k, v, ctx, pool, pt)
         qb.indexer_decode(d["idxQ"], d["idxK"], d["wq"], d["wk"], d["pool"], pt, ctx, ind, ws, D=cfg.D,
                           rot=cfg.rot, ratio=cfg.ratio, budget=cfg.budget, topK=cfg.topK, theta=cfg.theta, eps=cfg.eps)
-        q = qkv[:, :, :cfg.Hq].contiguous()
+        q = turned[:, :, :cfg.Hq].contiguous()
         qb.sparse_paged_kv4(q, pool, pt, ind, ctx, out, scale=cfg.scale, lse=lse)
         qb.sparse_weights_kv4(q, pool, pt, ind, ctx, lse, weights, total, scale=cfg.scale)
     kept = torch.empty((cfg.B, cfg.Hkv, KV4_BUDGET), dtype=torch.int32, device="cuda")

@@ -318,3 +318,20 @@ def test_first_calls_of_a_process_may_be_captured(qb, group, width):
     code = FIRST_CALL.format(root=ROOT, tests=ROOT + "/tests", group=group, width=width)
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_steps_of_a_workload_do_not_depend_on_their_number(qb):
+    """run_case's 4-bit steps give the same outputs and the same cache after one step as after three: each turns the
+    projections as they were.  (Totals add equal weights up, which keeps their order: the same tokens stay.)"""
+    import dataclasses
+    from block_sparse_gqa_qsa_gb300 import run_case, synthetic as syn
+    pre = dataclasses.replace(next(c for c in syn.BENCH_CONFIGS if c.name == "prefill_S8192"), B=2, S=600)
+    dec = dataclasses.replace(next(c for c in syn.BENCH_CONFIGS if c.name.startswith("decode_B32")), B=3, ctx_lo=5000,
+                              ctx_hi=9000, max_ctx=9000)
+    for run, cfg in ((run_case._kv4_prefill_steps, pre), (run_case._kv4_decode_steps, dec)):
+        got = []
+        for steps in (1, 3):
+            torch.manual_seed(3)
+            got.append(run(cfg, steps))
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
