@@ -648,10 +648,10 @@ QSA_API qsa_status_t qsa_rotary_frequencies(int32_t scaling, int32_t rotDim, dou
  * of token L - n + t, as
  *   t   = the smallest power of two with amax <= 2688 t, amax the row's largest finite magnitude, in [2^-48, 2^48]
  *   s_j = amax_j / (6 t), rounded to the nearest e4m3 (ties to even)
- *   code = x / (s_j t), rounded to the nearest e2m1 (ties to even, larger ones saturate at 6; a code has its
- *          value's sign even where it is 0; where s_j is 0 so are the codes)
+ *   code = x / (s_j t), rounded to the nearest e2m1 (ties to even, larger ones saturate at 6), of magnitude 0
+ *          where s_j is 0; a code has its value's sign even where its magnitude is 0
  * exactly: the bytes do not depend on how the call is split.  16 values with
- * an infinity or a NaN among them get s_j = NaN and codes 0.
+ * an infinity or a NaN among them get s_j = NaN and codes 0, without signs.
  * kOut / vOut (dense, NULL for none) get the values that the rows stand for,
  * rounded to the inputs' type (saturating), and zeros in rows t >= n, so that
  * a prompt's own attention can see what later steps will read.  k and v are never read

@@ -113,6 +113,28 @@ def test_store_borders(qb, dtype):
     check_store(qb, x.to(DT[dtype]), [24], None, pt, flat)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_codes_keep_their_signs(qb, dtype):
+    """Under a zero scale, and where a quotient rounds to 0, a code is 0 or 8 by its value's sign; next to a NaN all are 0."""
+    x = torch.zeros((1, 1, 2, D))
+    x[..., 0] = 2688.0 * 16  # t = 16: 1e-4 / 96 is nothing of a scale
+    x[..., 16:32:3], x[..., 17:32:3], x[..., 18:32:3] = -1e-4, 1e-4, -0.0
+    x[..., 32], x[..., 33:48:2], x[..., 34:48:2] = 96.0, -1e-4, 1e-4
+    x[..., 64:80], x[..., 70] = -3.0, float("nan")
+    x = x.to(DT[dtype])
+    pt, flat = ref.page_tables([1], 2)
+    check_store(qb, x, [1], None, pt, flat)
+    pool = torch.full((flat, PAGE, 1, ROW), 255, dtype=torch.uint8, device="cuda")
+    qb.store_kv4(x[:, :, :1].cuda(), x[:, :, 1:].cuda(), i32([1]).cuda(), pool, pt.cuda())
+    for plane in (0, 1):
+        row = pool[pt[0, plane, 0], 0, 0].cpu()
+        code = torch.stack([row[:64] & 15, row[:64] >> 4], -1).flatten()
+        assert row[64:72].tolist() == [0x7e, 0, 0x38, 0, 0x7f, 0, 0, 0]
+        assert torch.equal(code[16:32], 8 * torch.signbit(x[0, 0, plane, 16:32].float()).to(torch.uint8))
+        assert torch.equal(code[33:48], 8 * (torch.arange(33, 48) % 2).to(torch.uint8)) and code[32] == 7
+        assert not bool(code[64:80].any())
+
+
 def test_store_bad_pages_views_and_no_outputs(qb):
     ctx = [300, 140]
     pt, flat = ref.page_tables(ctx, 3)
