@@ -103,3 +103,34 @@ def test_work_is_counted_from_the_lengths(ops):
     work = [ops.work(c) for c in ops.listed()]
     assert all(w["bytes"] > 0 and w["flops"] > 0 for w in work)
     assert max(w["bytes"] for w in work) >= 16 * min(w["bytes"] for w in work)
+
+
+@pytest.mark.parametrize("name", ["weights4_step_B32", "weights4_window_B3_S37"])
+def test_weights_and_totals_within_their_derived_bars(ops, name):
+    """A logit is off by D 2^-23 + 2^-22 of the sum of its terms' magnitudes, at most |q| |k| scale; the log-sum-exp's
+    product and the exponential add 2^-21 of its magnitude and 2^-20: e, so that a weight is off by e (1 + e) of itself.  A
+    total is off by that much of what it was given, and by 2^-24 of itself for each of at most S additions and a rounding."""
+    case, seed = next(c for c in ops.listed() if c["name"] == name), 12
+    s = ops.prepare(case, seed)
+    ctx, new = ops._lengths(case)
+    G, scale = case["Hq"] // case["Hkv"], ops.D ** -0.5
+    e = torch.zeros((case["B"], case["S"], case["Hkv"]), dtype=torch.float64, device="cuda")
+    for b, (L, n) in enumerate(zip(ctx, new)):
+        for h in range(case["Hkv"]):
+            longest = ops._exact_cache(s, b, h, 0, L).norm(dim=-1).max()
+            q = s["q"][b, :n, h * G:(h + 1) * G].double().norm(dim=-1)
+            lse = s["lse"][b, :n, h * G:(h + 1) * G].double().abs()
+            e[b, :n, h] = ((ops.D * 2.0 ** -23 + 2.0 ** -22) * scale * longest * q + 2.0 ** -21 * lse + 2.0 ** -20).amax(-1)
+    before, want = s["total"].double(), ops.exact(case, seed)
+    rel = (e * (1 + e))[..., None]
+    most = rel.amax((1, 3))[..., None]
+    added = want["total"] - before
+    bar = most * added + (max(new) + 1) * 2.0 ** -24 * want["total"] * (1 + 2.0 ** -10)
+    for own in (False, True):
+        ops.own = own
+        try:
+            out = ops.run(ops.prepare(case, seed))
+        finally:
+            ops.own = False
+        assert bool(((out["weights"].double() - want["weights"]).abs() <= rel * want["weights"] + 1e-37).all())
+        assert bool(((out["total"].double() - want["total"]).abs() <= bar).all())
