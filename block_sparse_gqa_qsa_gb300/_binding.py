@@ -812,7 +812,8 @@ def evict_kv4(pool, page_table, ctx, total, kept, kept_lengths, total_out=None, 
     """qsa_evict_kv4: cuts every sequence of pool uint8 [numFlat,128,Hkv,rowBytes >= 80] back to budget = kept.shape[2]
     tokens per KV head, by total float32 [B,Hkv,tokens]; the first `sinks` and the last `recent` always stay.  kept int32
     [B,Hkv,budget] gets the tokens now in each slot (-1 behind the last), kept_lengths int32 [B] the new lengths, total_out
-    (may be total) their totals, zeros behind them."""
+    (may be total) their totals, zeros behind them.  Tokens that total is too short for are discarded.  A sequence that has
+    been cut can no longer be indexed: its lists name slots and are the caller's own."""
     nflat, Hkv, row, B, pages = _pool4(pool, page_table, "evict_kv4")
     shape, slots = total.shape, kept.shape
     if len(shape) != 3 or shape[:2] != (B, Hkv) or len(slots) != 3 or slots[:2] != (B, Hkv) or \

@@ -735,7 +735,8 @@ QSA_API qsa_status_t qsa_sparse_paged_kv4_bf16(const QsaSparsePagedKv4Params* pa
  *   total[b,g,j]    += the sum of weights[b,t,g,e] over the rows t and entries e that name j
  * weights is 0 for entries that name nothing and in rows t >= n; a head whose lse is
  * -infinity adds nothing.  lse, lists and lengths are those of the attention
- * call.  A token at or past totalLen is not counted (its weights are written).
+ * call.  A token at or past totalLen is not counted (its weights are written;
+ * qsa_evict_kv4 would discard it).
  * A token's weights are added to its total in fp32 in the order of the rows,
  * so that repeated calls on equal inputs give identical bits, and one call of
  * n rows those of n calls of one row.  Calls that share `total` must not run
@@ -782,12 +783,20 @@ QSA_API qsa_status_t qsa_sparse_weights_kv4_bf16(const QsaSparseWeightsKv4Params
  *   kept[b,g,i]     the token now in slot i, -1 for i >= K
  *   keptLengths[b]  K, the sequence's new length
  *   totalOut[b,g,i] total[b,g,kept[i]], 0 for i >= K (may be total itself, or NULL)
+ * Tokens at or past totalLen are not looked at: they are discarded, `recent`
+ * counts from the last token before totalLen, and keptLengths is at most
+ * totalLen, although nothing else would have to go; no status bit tells.  So
+ * totals that end in an eviction cover the cache (totalLen >= every length),
+ * unlike those that qsa_sparse_weights_kv4 only adds to.
  * Pool rows of slots K .. L - 1 are left as they were (some have moved up);
  * no other byte of the pool is written.  New tokens go to slot K on
  * (qsa_store_kv4 with the new lengths), rotated at their own positions
- * (qsa_rotary), and lists name slots.  Sequences that share pages, the
- * indexer's state in such a pool, and calls that share a pool concurrently
- * are the caller's to keep apart.
+ * (qsa_rotary), and lists name slots.  The indexers' lists do not: their block
+ * keys stand for runs of consecutive tokens, the same for all heads, and are
+ * not moved along, so that a sequence that an eviction has cut can no longer be
+ * indexed.  Its lists are the caller's own, for instance all of its slots.
+ * Sequences that share pages, the indexer's state in such a pool, and calls
+ * that share a pool concurrently are the caller's to keep apart.
  * status (may be NULL): bit 1 (value 2): a page id of a moving row lies
  * outside [0, numFlatPages); that row does not move.
  * Errors: QSA_ERR_INVALID_ARG for NULL required pointers, sizes < 1, sinks or
