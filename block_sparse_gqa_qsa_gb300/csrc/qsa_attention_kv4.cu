@@ -57,14 +57,6 @@ __device__ __forceinline__ float2 entry_of(const PagedArgs& a, bool ok, uint32_t
   return ok ? make_float2(read_scale(tk) * a.sl2, lg2_ftz(tv)) : make_float2(0.f, -INFINITY);
 }
 
-// Two transposed 16 x 16 byte matrices (rows at the addresses of lanes 0..15 and 16..31): of each, the lane gets rows
-// 4 q .. 4 q + 3 of column g, then of column g + 8.
-__device__ __forceinline__ void ldsm_bytes_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
 // A step's V scales by group: piece 4 j + q of `groups` gets group j's scales of keys 4 q + i and 4 q + i + 16, i = 0..3, as
 // f16 pairs.
 // (Columns 8 and on of the scale chunks, the row scales, are dropped.)
