@@ -8,14 +8,16 @@
 // few tokens: it forms the tokens' cosines and sines once, in shared memory; a
 // thread then owns one vector of a token's pairs (of up to 16 bytes; half
 // layout: a vector and its partner) for up to 8 heads, keeps its cosines and
-// sines in registers, and has four vectors on their way before the first is used.  Neighbouring threads hold neighbouring vectors of a head.  Out of
-// place, the threads then copy the vectors behind rotDim.
-// 16384 tokens of 36 16-bit heads of 128, all dims turning: halves 50 us, pairs 46
-// (0.89 and 0.95 of the copy rate).  What that took: cosines and sines formed by
+// sines in registers, and has four vectors on their way before the first is used.
+// Neighbouring threads hold neighbouring vectors of a head.  Out of place, the
+// threads then copy the vectors behind rotDim.
+// 16384 tokens of 36 16-bit heads of 128, all dims turning: halves 49.6 us, pairs
+// 45.4 (0.91 and 0.99 of the copy rate).  What that took: cosines and sines formed by
 // every thread for itself 100 us in halves, 145 with rotDim 64 (the copying
 // threads being in the same warps); formed by the CTA 76; few registers, so that
-// four CTAs lie on an SM (five for pairs), and the first loads in front of the
-// table 54; two elements to a conversion 50.
+// four CTAs lie on an SM (five for pairs, whose 48 registers leave 44 bytes of a
+// thread in local memory with 16-bit elements, 8 with fp32), and the first loads in
+// front of the table 54; two elements to a conversion 50.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,8 +28,10 @@ namespace qsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVectors = 4;  // of a thread in flight, of 16 bytes
-constexpr int kMostHeads = 8;  // of a thread (with 4 and two vectors in flight 81 us instead of 54)
+// Of a thread: vectors of 16 bytes in flight (with 2 halves 57.8 us and pairs 51.2), heads (with 4 48.6 and 55.6, with 16
+// 50.9 and 46.6).
+constexpr int kVectors = 4;
+constexpr int kMostHeads = 8;
 
 struct RotaryArgs {
   const void* x;
